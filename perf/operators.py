@@ -1,0 +1,374 @@
+"""The 8-bit and mixture-of-experts operators next to the FP4 linear layer: cases, plain forms and exact values.
+
+A mixed-precision block keeps its sensitive projections in 8 bits (E4M3 with one float32 scale for 128 values) and its
+experts in MXFP4 (E2M1 with an E8M0 scale for 32, in the block-Hadamard basis of fp4_quantize_weights):
+
+    norm      h = x + residual; n = h * rsqrt(mean(h^2) + eps) * weight; n in 8 bits with a scale for 128 values, and in bf16
+    quantize  activations (a scale for 1 x 128) or weights (a scale for 128 x 128) in 8 bits
+    linear    Y = dq(Xq) dq(Wq)^T
+    route     softmax(x Wr^T), the k largest, ties to the lowest index
+    experts   y_t = sum_j p_tj W2[e_tj] H (silu(G[e_tj] H x_t) * (U[e_tj] H x_t)), experts of -1 left out
+
+`run` computes a case in plain torch operations in float32, or with `own` through the framework's operators.
+"""
+import math
+
+import torch
+
+own = False
+
+E4M3_MAX = 448.0
+AMAX_FLOOR = 2.0 ** -100  # a group of zeros still has a finite scale and a finite reciprocal
+G = 128                   # values along K that share a scale
+E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+def listed():
+    return [
+        # one token of a decode step: two rows of 8 KB, a latency
+        {"name": "norm_token", "op": "norm", "M": 1, "K": 4096, "residual": True, "normed": True, "ld": 4096},
+        # a long prompt batch: bound by memory
+        {"name": "norm_prompt", "op": "norm", "M": 16384, "K": 8192, "residual": True, "normed": False, "ld": 8192},
+        # the input of an output projection: odd rows, a slice of a wider buffer
+        {"name": "quantize_rows", "op": "quantize", "M": 2047, "K": 4096, "ld": 6144, "weights": False},
+        # a projection's weights, once, when a model is loaded
+        {"name": "quantize_weights", "op": "quantize", "M": 14336, "K": 4096, "ld": 4096, "weights": True},
+        # one token against a wide layer: bound by reading the weights
+        {"name": "linear_token", "op": "linear", "M": 1, "N": 14336, "K": 4096, "out": "bf16"},
+        # a ragged decode batch against a layer whose width is no multiple of a tile
+        {"name": "linear_batch", "op": "linear", "M": 37, "N": 4100, "K": 4096, "out": "bf16"},
+        # a prompt of 2048 tokens
+        {"name": "linear_prompt", "op": "linear", "M": 2048, "N": 14336, "K": 4096, "out": "bf16"},
+        # many prompts at once, outputs kept in float32
+        {"name": "linear_large", "op": "linear", "M": 8192, "N": 28672, "K": 8192, "out": "f32"},
+        # the router for one token
+        {"name": "route_token", "op": "route", "T": 1, "E": 128, "D": 2048, "k": 8, "renormalize": True},
+        # the router for an odd decode batch
+        {"name": "route_batch", "op": "route", "T": 61, "E": 256, "D": 4096, "k": 6, "renormalize": False},
+        # the experts for one token: 8 small matrices of 128
+        {"name": "experts_token", "op": "experts", "T": 1, "E": 128, "D": 2048, "I": 768, "k": 8, "block": 32, "drop": 0.0},
+        # the experts for a decode batch: nearly all of them are read, some slots are unused
+        {"name": "experts_batch", "op": "experts", "T": 64, "E": 64, "D": 4096, "I": 1408, "k": 6, "block": 128, "drop": 0.1},
+    ]
+
+
+def _log(rng, lo, hi):
+    return min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi))))))
+
+
+def _times(rng, unit, lo, hi):
+    """A multiple of `unit`, spread over the logarithm of [lo, hi]."""
+    while True:
+        v = unit * max(1, int(round(_log(rng, lo, hi) / unit)))
+        if v != 3072 and lo <= v <= hi:
+            return v
+
+
+def draw(rng):
+    op = rng.choice(["norm", "quantize", "linear", "linear", "route", "experts", "experts"])
+    if op == "norm":
+        K = _times(rng, 128, 256, 16384)
+        M = _log(rng, 1, max(1, (16384 * 8192) // K))
+        return {"op": op, "M": M, "K": K, "residual": rng.random() < 0.75, "normed": rng.random() < 0.5,
+                "ld": K + rng.choice([0, 0, 8, 256])}
+    if op == "quantize":
+        K = _times(rng, 128, 256, 16384)
+        M = _log(rng, 1, max(1, (14336 * 8192) // K))
+        return {"op": op, "M": M, "K": K, "ld": K + rng.choice([0, 0, 8, 256]), "weights": rng.random() < 0.5}
+    if op == "linear":
+        N = _log(rng, 64, 28672)
+        N += 1 if N == 3072 else 0
+        M = _log(rng, 1, 8192)
+        M += 1 if M == 3072 else 0
+        return {"op": op, "M": M, "N": N, "K": _times(rng, 128, 256, 8192), "out": rng.choice(["bf16", "f32"])}
+    if op == "route":
+        E = rng.choice([8, 16, 32, 60, 64, 128, 160, 256])
+        return {"op": op, "T": _log(rng, 1, 512), "E": E, "D": _times(rng, 128, 512, 7168), "k": rng.randint(1, 8),
+                "renormalize": rng.random() < 0.5}
+    while True:
+        E, D, I = rng.choice([8, 16, 32, 60, 64, 128, 160, 256]), _times(rng, 128, 512, 7168), _times(rng, 128, 128, 2048)
+        if E * D * I <= 64 * 4096 * 1408 and 2 * I != 3072:
+            return {"op": op, "T": _log(rng, 1, 64), "E": E, "D": D, "I": I, "k": rng.randint(1, 8),
+                    "block": rng.choice([16, 32, 64, 128]), "drop": rng.choice([0.0, 0.0, 0.25])}
+
+
+# ---- inputs ----------------------------------------------------------------------------------------------------------
+
+def _activations(g, rows, cols, ld):
+    """Student-t(5) values with 1% of the channels 30 times as large, as bf16 rows in a buffer of `ld` columns."""
+    x = torch.randn(rows, ld, generator=g, device="cuda")
+    chi = torch.zeros_like(x)
+    for _ in range(5):
+        chi += torch.randn(rows, ld, generator=g, device="cuda").square_()
+    x /= chi.div_(5.0).sqrt_()
+    x *= 1.0 + 29.0 * (torch.rand(ld, generator=g, device="cuda") < 0.01).float()
+    return x.bfloat16()[:, :cols]
+
+
+def _to_e4m3(x, rows):
+    """Codes and scales of float32 x, one scale for rows x 128 values."""
+    M, K = x.shape
+    R = -(-M // rows)
+    if R * rows != M:
+        x = torch.cat([x, x.new_zeros(R * rows - M, K)])
+    t = x.view(R, rows, K // G, G)
+    amax = t.abs().amax(dim=(1, 3)).clamp_min(AMAX_FLOOR)
+    inv = E4M3_MAX / amax
+    codes = (t * inv[:, None, :, None]).reshape(R * rows, K)[:M].to(torch.float8_e4m3fn)
+    return codes, amax / E4M3_MAX
+
+
+def _mxfp4(g, E, rows, K):
+    """E matrices of N(0, 0.02^2) weights in MXFP4: nibble codes (element 2j low) and E8M0 codes. A rotated matrix of such
+    weights has the same distribution, so these stand for weights in the block-Hadamard basis."""
+    codes = torch.empty(E, rows, K // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(E, rows, K // 32, dtype=torch.uint8, device="cuda")
+    edges = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], device="cuda")
+    step = max(1, (1 << 26) // (rows * K))
+    for e in range(0, E, step):
+        n = min(step, E - e)
+        w = torch.randn(n, rows, K // 32, 32, generator=g, device="cuda") * 0.02
+        ex = torch.ceil(torch.log2(w.abs().amax(-1, keepdim=True) / 6.0))
+        q = torch.bucketize((w * torch.exp2(-ex)).abs_(), edges).to(torch.uint8) + 8 * (w < 0).to(torch.uint8)
+        q = q.view(n, rows, K // 2, 2)
+        codes[e:e + n] = q[..., 0] | (q[..., 1] << 4)
+        scales[e:e + n] = (ex[..., 0] + 127.0).to(torch.uint8)
+    return codes, scales
+
+
+def prepare(case, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    s = dict(case)
+    op = case["op"]
+
+    def out(shape, dtype):
+        return torch.empty(shape, dtype=dtype, device="cuda")
+
+    if op == "norm":
+        M, K = case["M"], case["K"]
+        s["x"] = _activations(g, M, K, case["ld"])
+        s["w"] = (1.0 + 0.1 * torch.randn(K, generator=g, device="cuda")).bfloat16()
+        s["r"] = (2.0 * torch.randn(M, case["ld"], generator=g, device="cuda")).bfloat16()[:, :K] if case["residual"] else None
+        s["buffers"] = (out((M, K), torch.float8_e4m3fn), out((M, K // G), torch.float32),
+                        out((M, K), torch.bfloat16) if case["residual"] else None,
+                        out((M, K), torch.bfloat16) if case["normed"] else None)
+    elif op == "quantize":
+        M, K = case["M"], case["K"]
+        if case["weights"]:
+            s["x"] = (0.02 * torch.randn(M, case["ld"], generator=g, device="cuda")).bfloat16()[:, :K]
+        else:
+            s["x"] = _activations(g, M, K, case["ld"])
+        R = -(-M // G) if case["weights"] else M
+        s["buffers"] = (out((M, K), torch.float8_e4m3fn), out((R, K // G), torch.float32))
+    elif op == "linear":
+        M, N, K = case["M"], case["N"], case["K"]
+        s["xq"], s["xs"] = _to_e4m3(_activations(g, M, K, K).float(), 1)
+        s["wq"], s["ws"] = _to_e4m3(0.02 * torch.randn(N, K, generator=g, device="cuda"), G)
+        s["type"] = torch.bfloat16 if case["out"] == "bf16" else torch.float32
+        s["y"] = out((M, N), s["type"])
+    elif op == "route":
+        T, E, D = case["T"], case["E"], case["D"]
+        s["x"] = torch.randn(T, D, generator=g, device="cuda").bfloat16()
+        s["wr"] = (torch.randn(E, D, generator=g, device="cuda") / math.sqrt(D)).bfloat16()
+        s["buffers"] = (out((T, case["k"]), torch.int32), out((T, case["k"]), torch.float32))
+    else:
+        T, E, D, I, k = (case[n] for n in ("T", "E", "D", "I", "k"))
+        s["x"] = torch.randn(T, D, generator=g, device="cuda").bfloat16()
+        s["w13"] = _mxfp4(g, E, 2 * I, D)
+        s["w2"] = _mxfp4(g, E, D, I)
+        p, ids = torch.softmax(torch.randn(T, E, generator=g, device="cuda"), 1).topk(k, dim=1)
+        gone = torch.rand(T, k, generator=g, device="cuda") < case["drop"]
+        s["ids"] = torch.where(gone, -1, ids).to(torch.int32)
+        s["p"] = (p / p.sum(1, keepdim=True)).contiguous()
+        s["y"] = out((T, D), torch.bfloat16)
+    return s
+
+
+# ---- plain forms, in float32 -----------------------------------------------------------------------------------------
+
+def _plain_norm(s):
+    h = s["x"].float()
+    if s["r"] is not None:
+        h = h + s["r"].float()
+    n = h * torch.rsqrt(h.square().mean(-1, keepdim=True) + 1e-6) * s["w"].float()
+    codes, scales = _to_e4m3(n, 1)
+    return codes, scales, h.bfloat16() if s["r"] is not None else None, n.bfloat16() if s["normed"] else None
+
+
+def _plain_linear(s):
+    xq, wq = s["xq"].float(), s["wq"].float()
+    (M, K), N = xq.shape, wq.shape[0]
+    x = (xq.view(M, K // G, G) * s["xs"][:, :, None]).view(M, K)
+    ws = s["ws"].repeat_interleave(G, 0)[:N]
+    w = (wq.view(N, K // G, G) * ws[:, :, None]).view(N, K)
+    return (x @ w.t()).to(s["type"])
+
+
+def _plain_route(s):
+    p = torch.softmax(s["x"].float() @ s["wr"].float().t(), dim=1)
+    p, ids = torch.sort(p, dim=1, descending=True, stable=True)
+    p, ids = p[:, :s["k"]], ids[:, :s["k"]]
+    if s["renormalize"]:
+        p = p / p.sum(1, keepdim=True)
+    return ids.to(torch.int32), p.contiguous()
+
+
+def _hadamard(b, dtype):
+    i = torch.arange(b, device="cuda")
+    v, parity = i[:, None] & i[None, :], torch.zeros(b, b, dtype=torch.int64, device="cuda")
+    for bit in range(7):
+        parity ^= (v >> bit) & 1
+    return (1 - 2 * parity).to(dtype) / math.sqrt(b)
+
+
+def _rotate(x, b):
+    return (x.reshape(-1, b) @ _hadamard(b, x.dtype)).view(x.shape)
+
+
+def _pairs_of_codes():
+    v = torch.tensor(E2M1 + tuple(-e for e in E2M1), device="cuda")
+    b = torch.arange(256, device="cuda")
+    return torch.stack([v[b & 15], v[b >> 4]], 1)
+
+
+def _plain_weights(codes, scales):
+    w = _pairs_of_codes()[codes.int()].view(*scales.shape, 32)
+    return (w * torch.exp2(scales.float() - 127.0)[..., None]).view(*codes.shape[:-1], -1)
+
+
+def _plain_experts(s):
+    (T, D), E, I, k, b = s["x"].shape, s["E"], s["I"], s["k"], s["block"]
+    p, ids = torch.where(s["ids"] >= 0, s["p"], 0.0), s["ids"].clamp_min(0).long()
+    x = _rotate(s["x"].float(), b)
+    if T * k <= E:  # few pairs: each with the matrices of its expert
+        at = ids.reshape(-1)
+        x = x.repeat_interleave(k, 0)[:, :, None]
+        y = _plain_weights(s["w13"][0][at], s["w13"][1][at]).bmm(x)[:, :, 0]
+        h = _rotate(torch.nn.functional.silu(y[:, :I]) * y[:, I:], b)
+        y = _plain_weights(s["w2"][0][at], s["w2"][1][at]).bmm(h[:, :, None])
+        return (y.view(T, k, D) * p[:, :, None]).sum(1).bfloat16()
+    share = torch.zeros(T, E, device="cuda").scatter_add_(1, ids, p)
+    y = x @ _plain_weights(*s["w13"]).view(E * 2 * I, D).t()
+    y = y.view(T, E, 2 * I)
+    h = _rotate(torch.nn.functional.silu(y[:, :, :I]) * y[:, :, I:], b) * share[:, :, None]
+    w2 = _plain_weights(*s["w2"])
+    return torch.bmm(h.transpose(0, 1).contiguous(), w2.transpose(1, 2)).sum(0).bfloat16()
+
+
+def _plain(s):
+    op = s["op"]
+    if op == "norm":
+        return _plain_norm(s)
+    if op == "quantize":
+        return _to_e4m3(s["x"].float(), G if s["weights"] else 1)
+    if op == "linear":
+        return _plain_linear(s)
+    if op == "route":
+        return _plain_route(s)
+    return _plain_experts(s)
+
+
+def run(s):
+    if not own:
+        return _plain(s)
+    import microscaling_fp4_quantized_amd as F
+
+    op = s["op"]
+    if op == "norm":
+        return F.fp8_add_rmsnorm_quantize(s["x"], s["w"], residual=s["r"], eps=1e-6, normed=s["normed"], out=s["buffers"])
+    if op == "quantize":
+        return (F.fp8_quantize_weights if s["weights"] else F.fp8_quantize)(s["x"], out=s["buffers"])
+    if op == "linear":
+        return F.fp8_linear(s["xq"], s["xs"], s["wq"], s["ws"], out_dtype=s["type"], out=s["y"])
+    if op == "route":
+        return F.fp4_moe_route(s["x"], s["wr"], s["k"], renormalize=s["renormalize"], out=s["buffers"])
+    return F.fp4_moe_experts(s["x"], s["ids"], s["p"], s["w13"][0], s["w13"][1], s["w2"][0], s["w2"][1], s["block"], out=s["y"])
+
+
+def work(case):
+    op = case["op"]
+    if op in ("norm", "quantize"):
+        M, K = case["M"], case["K"]
+        weights = op == "quantize" and case["weights"]
+        b = M * K * (2 + 1) + (-(-M // G) if weights else M) * (K // G) * 4
+        if op == "norm":
+            b += 2 * K + M * K * ((4 if case["residual"] else 0) + (2 if case["normed"] else 0))
+        return {"bytes": b, "flops": M * K * (6 if op == "norm" else 2)}
+    if op == "linear":
+        M, N, K = case["M"], case["N"], case["K"]
+        b = (M + N) * K + 4 * (K // G) * (M + -(-N // G)) + M * N * (2 if case["out"] == "bf16" else 4)
+        return {"bytes": b, "flops": 2 * M * N * K}
+    if op == "route":
+        T, E, D = case["T"], case["E"], case["D"]
+        return {"bytes": 2 * D * (T + E) + 8 * T * case["k"], "flops": 2 * T * E * D}
+    T, E, D, I, k = (case[n] for n in ("T", "E", "D", "I", "k"))
+    pairs = T * k * (1.0 - case["drop"])
+    used = E * (1.0 - (1.0 - k * (1.0 - case["drop"]) / E) ** T)  # experts that some token has, on average
+    return {"bytes": used * 3 * D * I * (0.5 + 1 / 32) + 4 * T * D + 8 * T * k, "flops": pairs * 6 * D * I}
+
+
+# ---- exact values, in 64 bits, before the one rounding of each output ------------------------------------------------
+
+def _exact_groups(n, rows):
+    """The values that the 8-bit codes round, and the scales."""
+    M, K = n.shape
+    R = -(-M // rows)
+    tall = torch.zeros(R * rows, K, dtype=torch.float64, device="cuda")
+    tall[:M] = n.abs()
+    scale = tall.reshape(R, rows, K // G, G).amax(3).amax(1).clamp(min=AMAX_FLOOR) / E4M3_MAX
+    at = torch.arange(M, device="cuda") // rows
+    return n / scale[at].repeat_interleave(G, 1), scale
+
+
+def _exact_matrix(codes, scales):
+    c = codes.long()
+    q = torch.stack([c % 16, c // 16], -1).flatten(-2)
+    m, e, neg = q % 2, (q // 2) % 4, q // 8
+    v = torch.where(e == 0, m * 0.5, (1.0 + 0.5 * m.double()) * 2.0 ** (e.double() - 1.0)) * (1.0 - 2.0 * neg.double())
+    return v * (2.0 ** (scales.double() - 127.0)).repeat_interleave(32, -1)
+
+
+def _exact_rotated(x, b):
+    y = x.reshape(-1, b)
+    h = 1
+    while h < b:
+        y = y.view(-1, b // (2 * h), 2, h)
+        y = torch.stack([y[:, :, 0] + y[:, :, 1], y[:, :, 0] - y[:, :, 1]], 2).reshape(-1, b)
+        h *= 2
+    return (y / b ** 0.5).view(x.shape)
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    op = case["op"]
+    if op == "norm":
+        h = s["x"].double() + (s["r"].double() if case["residual"] else 0.0)
+        n = h / (h.pow(2).sum(1, keepdim=True) / case["K"] + 1e-6).sqrt() * s["w"].double()
+        v, scale = _exact_groups(n, 1)
+        return v, scale, h if case["residual"] else None, n if case["normed"] else None
+    if op == "quantize":
+        return _exact_groups(s["x"].double(), G if case["weights"] else 1)
+    if op == "linear":
+        x = s["xq"].double() * s["xs"].double().repeat_interleave(G, 1)
+        at = torch.arange(case["N"], device="cuda") // G
+        w = s["wq"].double() * s["ws"].double()[at].repeat_interleave(G, 1)
+        return torch.cat([c @ w.t() for c in x.split(2048)])
+    if op == "route":
+        z = s["x"].double() @ s["wr"].double().t()
+        p = (z - z.amax(1, keepdim=True)).exp()
+        p = p / p.sum(1, keepdim=True)
+        top = p.topk(case["k"], dim=1)[0]
+        return None, top / top.sum(1, keepdim=True) if case["renormalize"] else top
+    x = _exact_rotated(s["x"].double(), case["block"])
+    y = torch.zeros(case["T"], case["D"], dtype=torch.float64, device="cuda")
+    for e in range(case["E"]):
+        share = (s["p"].double() * (s["ids"] == e)).sum(1)
+        at = share.nonzero()[:, 0]
+        if not len(at):
+            continue
+        u = x[at] @ _exact_matrix(s["w13"][0][e], s["w13"][1][e]).t()
+        a, c = u[:, :case["I"]], u[:, case["I"]:]
+        h = _exact_rotated(a / (1.0 + (-a).exp()) * c, case["block"])
+        y[at] += (h @ _exact_matrix(s["w2"][0][e], s["w2"][1][e]).t()) * share[at, None]
+    return y
