@@ -34,13 +34,13 @@ def listed():
         # a projection's weights, once, when a model is loaded
         {"name": "quantize_weights", "op": "quantize", "M": 14336, "K": 4096, "ld": 4096, "weights": True},
         # one token against a wide layer: bound by reading the weights
-        {"name": "linear_token", "op": "linear", "M": 1, "N": 14336, "K": 4096, "out": "bf16"},
+        {"name": "linear_token", "op": "linear", "M": 1, "N": 14336, "K": 4096},
         # a ragged decode batch against a layer whose width is no multiple of a tile
-        {"name": "linear_batch", "op": "linear", "M": 37, "N": 4100, "K": 4096, "out": "bf16"},
+        {"name": "linear_batch", "op": "linear", "M": 37, "N": 4100, "K": 4096},
         # a prompt of 2048 tokens
-        {"name": "linear_prompt", "op": "linear", "M": 2048, "N": 14336, "K": 4096, "out": "bf16"},
-        # many prompts at once, outputs kept in float32
-        {"name": "linear_large", "op": "linear", "M": 8192, "N": 28672, "K": 8192, "out": "f32"},
+        {"name": "linear_prompt", "op": "linear", "M": 2048, "N": 14336, "K": 4096},
+        # many prompts at once
+        {"name": "linear_large", "op": "linear", "M": 8192, "N": 28672, "K": 8192},
         # the router for one token
         {"name": "route_token", "op": "route", "T": 1, "E": 128, "D": 2048, "k": 8, "renormalize": True},
         # the router for an odd decode batch
@@ -80,7 +80,7 @@ def draw(rng):
         N += 1 if N == 3072 else 0
         M = _log(rng, 1, 8192)
         M += 1 if M == 3072 else 0
-        return {"op": op, "M": M, "N": N, "K": _times(rng, 128, 256, 8192), "out": rng.choice(["bf16", "f32"])}
+        return {"op": op, "M": M, "N": N, "K": _times(rng, 128, 256, 8192)}
     if op == "route":
         E = rng.choice([8, 16, 32, 60, 64, 128, 160, 256])
         return {"op": op, "T": _log(rng, 1, 512), "E": E, "D": _times(rng, 128, 512, 7168), "k": rng.randint(1, 8),
@@ -165,8 +165,7 @@ def prepare(case, seed):
         M, N, K = case["M"], case["N"], case["K"]
         s["xq"], s["xs"] = _to_e4m3(_activations(g, M, K, K).float(), 1)
         s["wq"], s["ws"] = _to_e4m3(0.02 * torch.randn(N, K, generator=g, device="cuda"), G)
-        s["type"] = torch.bfloat16 if case["out"] == "bf16" else torch.float32
-        s["y"] = out((M, N), s["type"])
+        s["y"] = out((M, N), torch.bfloat16)
     elif op == "route":
         T, E, D = case["T"], case["E"], case["D"]
         s["x"] = torch.randn(T, D, generator=g, device="cuda").bfloat16()
@@ -202,7 +201,7 @@ def _plain_linear(s):
     x = (xq.view(M, K // G, G) * s["xs"][:, :, None]).view(M, K)
     ws = s["ws"].repeat_interleave(G, 0)[:N]
     w = (wq.view(N, K // G, G) * ws[:, :, None]).view(N, K)
-    return (x @ w.t()).to(s["type"])
+    return (x @ w.t()).bfloat16()
 
 
 def _plain_route(s):
@@ -280,7 +279,7 @@ def run(s):
     if op == "quantize":
         return (F.fp8_quantize_weights if s["weights"] else F.fp8_quantize)(s["x"], out=s["buffers"])
     if op == "linear":
-        return F.fp8_linear(s["xq"], s["xs"], s["wq"], s["ws"], out_dtype=s["type"], out=s["y"])
+        return F.fp8_linear(s["xq"], s["xs"], s["wq"], s["ws"], out=s["y"])
     if op == "route":
         return F.fp4_moe_route(s["x"], s["wr"], s["k"], renormalize=s["renormalize"], out=s["buffers"])
     return F.fp4_moe_experts(s["x"], s["ids"], s["p"], s["w13"][0], s["w13"][1], s["w2"][0], s["w2"][1], s["block"], out=s["y"])
@@ -297,7 +296,7 @@ def work(case):
         return {"bytes": b, "flops": M * K * (6 if op == "norm" else 2)}
     if op == "linear":
         M, N, K = case["M"], case["N"], case["K"]
-        b = (M + N) * K + 4 * (K // G) * (M + -(-N // G)) + M * N * (2 if case["out"] == "bf16" else 4)
+        b = (M + N) * K + 4 * (K // G) * (M + -(-N // G)) + 2 * M * N
         return {"bytes": b, "flops": 2 * M * N * K}
     if op == "route":
         T, E, D = case["T"], case["E"], case["D"]
