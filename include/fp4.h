@@ -255,6 +255,71 @@ FP4_API int fp4_rotate_quantize_linear_noalloc(const void *X, int64_t M, int64_t
                                                const uint8_t *Wq, const uint8_t *Ws, int64_t N, void *Y,
                                                int y_dtype, void *stream);
 
+/*
+ * The 8-bit operators: the layers of a mixed-precision model that keep more than 4 bits.
+ *
+ * Values are E4M3 codes (1 sign, 4 exponent, 3 mantissa bits, no infinity, largest 448) with one
+ * float32 scale for 128 of them along K; no rotation. A group with largest magnitude a is stored as
+ *   code = e4m3(fl32(x * inv)), inv = fl32(448 / a'), scale = fl32(a' * fl32(1 / 448)), a' = max(a, 2^-100)
+ * rounded to nearest, ties to even; the value a code stands for is e4m3(code) * scale. A group of
+ * zeros has codes 0 and a small finite scale. A NaN makes its whole group NaN; an infinity gives its
+ * group the scale infinity, whose values are NaN.
+ * K is a multiple of 128 throughout. Calls, errors and streams as above: validated before anything
+ * is launched, nothing allocated, one kernel launch each on `stream`.
+ */
+
+/*
+ * fp8_quantize - activations, one scale for 1 x 128 values.
+ *  X       device bf16 [M, ldx], 16-byte aligned, ldx >= K, ldx % 8 == 0.
+ *  codes   device uint8 [M, K], 16-byte aligned.
+ *  scales  device float [M, K / 128].
+ *  M >= 1, M * K / 8 < 2^31.
+ * fp8_quantize_weights - weights, one scale for 128 x 128 values (fewer rows in the last block of an
+ * N that is no multiple of 128): scales is float [ceil(N / 128), K / 128].
+ * Errors: FP4_E_NULLPTR, FP4_E_SHAPE, FP4_E_ALIGN.
+ */
+FP4_API int fp8_quantize(const void *X, int64_t M, int64_t K, int64_t ldx, uint8_t *codes, float *scales,
+                         void *stream);
+FP4_API int fp8_quantize_weights(const void *W, int64_t N, int64_t K, int64_t ldw, uint8_t *codes, float *scales,
+                                 void *stream);
+
+/*
+ * fp8_add_rmsnorm_quantize - the residual's addition, the RMS norm and the quantizer in one pass:
+ *   h = x + r;  n = h / sqrt(mean_k(h^2) + eps) * weight;  codes, scales = fp8_quantize(n)
+ * in float32 from bf16 x, r and weight; h and n are not rounded on the way to the codes.
+ *  X             device bf16 [M, ldx].
+ *  residual      device bf16 [M, ldr], or NULL: h = x.
+ *  weight        device bf16 [K].
+ *  eps           finite, >= 0 (with 0, a row of zeros gives NaN, as the formula does).
+ *  codes, scales as fp8_quantize.
+ *  residual_out  device bf16 [M, K]: h rounded. Non-NULL exactly when residual is. It may be the
+ *                residual's own buffer (ldr == K); no other overlap of buffers is allowed.
+ *  normed        device bf16 [M, K], or NULL: n rounded, for the layers that take bf16.
+ *  M >= 1; K <= 65536. Matrices 16-byte aligned, ldx, ldr >= K and multiples of 8.
+ * Errors: FP4_E_NULLPTR, FP4_E_SHAPE (also eps), FP4_E_ALIGN.
+ */
+FP4_API int fp8_add_rmsnorm_quantize(const void *X, int64_t M, int64_t K, int64_t ldx, const void *residual,
+                                     int64_t ldr, const void *weight, float eps, uint8_t *codes, float *scales,
+                                     void *residual_out, void *normed, void *stream);
+
+/*
+ * fp8_linear - Y[m, n] = sum_b Xs[m, b] * Ws[n / 128, b] * sum_{k in block b} e4m3(Xq[m, k]) * e4m3(Wq[n, k]):
+ * rounded once to bf16 (to nearest even). The blocks' sums are scaled and added in float32.
+ * The matrix cores add the products of E4M3 numbers eight at a time, aligned to the largest of the eight
+ * and cut 13 bits below it, and those sums in float32: relative to the float64 product Y has, before its
+ * rounding, an error near 1.4e-5 in norm (measured on normal operands, whatever K). That is far below
+ * bf16's and far above float32's, so there is no float32 Y.
+ *  Xq, Xs  device uint8 [M, K], float [M, K / 128]               (fp8_quantize, fp8_add_rmsnorm_quantize)
+ *  Wq, Ws  device uint8 [N, K], float [ceil(N / 128), K / 128]   (fp8_quantize_weights)
+ *  Y       device bf16 [M, N] row-major.
+ *  M, N >= 1, at most 2^31 - 1; K <= 2^24; M * K and N * K <= 2^40.
+ *  Xq, Wq and Y 16-byte aligned, Xs and Ws 4-byte aligned.
+ * Results do not depend on timing: partial sums meet in a fixed order.
+ * Errors: FP4_E_NULLPTR, FP4_E_SHAPE, FP4_E_ALIGN.
+ */
+FP4_API int fp8_linear(const uint8_t *Xq, const float *Xs, const uint8_t *Wq, const float *Ws, int64_t M, int64_t N,
+                       int64_t K, void *Y, void *stream);
+
 /* Message for the last non-OK status returned on this thread ("" if none). */
 FP4_API const char *fp4_last_error(void);
 

@@ -24,6 +24,10 @@ __all__ = [
     "fp4_rotate_quantize_linear",
     "fp4_rotate_quantize_linear_noalloc",
     "linear_workspace_bytes",
+    "fp8_quantize",
+    "fp8_quantize_weights",
+    "fp8_add_rmsnorm_quantize",
+    "fp8_linear",
     "fp4_abi_version",
     "group_size",
 ]
@@ -74,6 +78,14 @@ def load_library() -> ctypes.CDLL:
     lib.fp4_rotate_quantize_linear_noalloc.restype = i32
     lib.fp4_linear.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, vp, i32, vp]
     lib.fp4_linear.restype = i32
+    for name in ("fp8_quantize", "fp8_quantize_weights"):
+        f = getattr(lib, name)
+        f.argtypes = [vp, i64, i64, i64, vp, vp, vp]
+        f.restype = i32
+    lib.fp8_add_rmsnorm_quantize.argtypes = [vp, i64, i64, i64, vp, i64, vp, ctypes.c_float, vp, vp, vp, vp, vp]
+    lib.fp8_add_rmsnorm_quantize.restype = i32
+    lib.fp8_linear.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, vp]
+    lib.fp8_linear.restype = i32
     lib.fp4_last_error.argtypes = []
     lib.fp4_last_error.restype = ctypes.c_char_p
     lib.fp4_abi_version.argtypes = []
@@ -300,6 +312,111 @@ def fp4_rotate_quantize_linear_noalloc(x: torch.Tensor, wq, ws, block: int, out_
     _check(_launch(x.device, lib.fp4_rotate_quantize_linear_noalloc, _ptr(x), M, K, x.stride(0), int(block),
                    _ptr(wq), _ptr(ws), N, _ptr(y), ydt))
     return y
+
+
+FP8_GROUP = 128  # values along K (and rows of a weight matrix) that share an 8-bit scale
+
+
+def _rows(t, name, what):
+    """A 2-D bf16 CUDA tensor of rows with unit column stride: its shape and row stride."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype != torch.bfloat16 or not t.is_cuda or t.stride(1) != 1:
+        raise ValueError(f"{name}: {what} must be a 2-D bf16 CUDA tensor with unit column stride")
+    # the stride of a single row says nothing: torch may give any
+    return t.shape[0], t.shape[1], t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _quantize8(name, x, rows, out):
+    lib = load_library()
+    M, K, ld = _rows(x, name, "the input")
+    shape = (-(-M // rows), K // FP8_GROUP)
+    if out is None:
+        codes = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=x.device)
+        scales = torch.empty(shape, dtype=torch.float32, device=x.device)
+    else:
+        codes, scales = out
+        _expect(codes, (M, K), torch.float8_e4m3fn, name, "codes")
+        _expect(scales, shape, torch.float32, name, "scales")
+        _same_device(name, x.device, codes, scales)
+    _check(_launch(x.device, getattr(lib, name), x.data_ptr(), M, K, ld, codes.data_ptr(), scales.data_ptr()))
+    return codes, scales
+
+
+def fp8_quantize(x: torch.Tensor, out=None):
+    """bf16 activations [M, K] -> (codes [M, K] float8_e4m3fn, scales [M, K/128] float32).
+
+    One scale for 128 consecutive values of a row; K a multiple of 128. ``out`` may pass
+    preallocated (codes, scales)."""
+    return _quantize8("fp8_quantize", x, 1, out)
+
+
+def fp8_quantize_weights(w: torch.Tensor, out=None):
+    """bf16 weights [N, K] -> (codes [N, K] float8_e4m3fn, scales [ceil(N/128), K/128] float32), one scale
+    for a block of 128 x 128."""
+    return _quantize8("fp8_quantize_weights", w, FP8_GROUP, out)
+
+
+def fp8_add_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual=None, eps: float = 1e-6,
+                             normed: bool = False, out=None):
+    """h = x + residual; n = h / sqrt(mean(h^2) + eps) * weight; n quantized as fp8_quantize does.
+
+    Returns (codes, scales, h in bf16 or None without a residual, n in bf16 or None unless ``normed``).
+    ``out`` may pass those four preallocated (None where there is none); h may be the residual itself,
+    which is then updated in place."""
+    name = "fp8_add_rmsnorm_quantize"
+    lib = load_library()
+    M, K, ld = _rows(x, name, "x")
+    dev = x.device
+    _expect(weight, (K,), torch.bfloat16, name, "weight")
+    ldr = 0
+    if residual is not None:
+        Mr, Kr, ldr = _rows(residual, name, "residual")
+        if (Mr, Kr) != (M, K):
+            raise ValueError(f"{name}: residual must have the shape of x, {(M, K)}, got {(Mr, Kr)}")
+    if out is None:
+        codes = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
+        scales = torch.empty((M, K // FP8_GROUP), dtype=torch.float32, device=dev)
+        h = torch.empty((M, K), dtype=torch.bfloat16, device=dev) if residual is not None else None
+        n = torch.empty((M, K), dtype=torch.bfloat16, device=dev) if normed else None
+    else:
+        codes, scales, h, n = out
+        _expect(codes, (M, K), torch.float8_e4m3fn, name, "codes")
+        _expect(scales, (M, K // FP8_GROUP), torch.float32, name, "scales")
+        if (h is None) != (residual is None) or (n is None) == bool(normed):
+            raise ValueError(f"{name}: out must hold the residual's sum exactly with a residual, and the normed rows "
+                             "exactly with normed")
+        for t, what in ((h, "the residual's sum"), (n, "the normed rows")):
+            if t is not None:
+                _expect(t, (M, K), torch.bfloat16, name, what)
+    _same_device(name, dev, weight, residual, codes, scales, h, n)
+    _check(_launch(dev, lib.fp8_add_rmsnorm_quantize, x.data_ptr(), M, K, ld,
+                   residual.data_ptr() if residual is not None else None, ldr, weight.data_ptr(), eps,
+                   codes.data_ptr(), scales.data_ptr(), h.data_ptr() if h is not None else None,
+                   n.data_ptr() if n is not None else None))
+    return codes, scales, h, n
+
+
+def fp8_linear(xq, xs, wq, ws, out=None):
+    """Y = dq(Xq) dq(Wq)^T, [M, N] in bf16, from the outputs of fp8_quantize (or
+    fp8_add_rmsnorm_quantize) and fp8_quantize_weights."""
+    name = "fp8_linear"
+    lib = load_library()
+    for t in (xq, wq):
+        if not isinstance(t, torch.Tensor) or t.dim() != 2:
+            raise ValueError(f"{name}: Xq and Wq must be 2-D tensors of codes")
+    M, K = xq.shape
+    N = wq.shape[0]
+    _expect(xq, (M, K), torch.float8_e4m3fn, name, "Xq")
+    _expect(wq, (N, K), torch.float8_e4m3fn, name, "Wq")
+    _expect(xs, (M, K // FP8_GROUP), torch.float32, name, "Xs")
+    _expect(ws, (-(-N // FP8_GROUP), K // FP8_GROUP), torch.float32, name, "Ws")
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
+    else:
+        _expect(out, (M, N), torch.bfloat16, name, "out")
+    _same_device(name, xq.device, xs, wq, ws, out)
+    _check(_launch(xq.device, lib.fp8_linear, xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), M, N, K,
+                   out.data_ptr()))
+    return out
 
 
 def fp4_abi_version() -> int:

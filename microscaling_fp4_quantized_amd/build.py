@@ -26,6 +26,8 @@ SOURCES = [
     "gemm_decode.hip",
     "gemm_nvfp4.hip",
     "gemm_nvfp4_ring.hip",
+    "fp8_quant.hip",
+    "gemm_fp8_decode.hip",
     "fp4_abi.cpp",
 ]
 

@@ -126,3 +126,14 @@ inline void fp4_plan_tile_columns(int tiles_m, int64_t N, int cus, float narrow_
     }
   }
 }
+
+// 8-bit (E4M3, one float32 scale for 128 values along K) operators.
+hipError_t fp8_launch_quantize(const uint16_t* X, int64_t M, int64_t K, int64_t ldx, uint8_t* codes, float* scales,
+                               hipStream_t stream);
+hipError_t fp8_launch_quantize_weights(const uint16_t* W, int64_t N, int64_t K, int64_t ldw, uint8_t* codes,
+                                       float* scales, hipStream_t stream);
+hipError_t fp8_launch_add_rmsnorm_quantize(const uint16_t* X, int64_t M, int64_t K, int64_t ldx, const uint16_t* R,
+                                           int64_t ldr, const uint16_t* G, float eps, uint8_t* codes, float* scales,
+                                           uint16_t* H, uint16_t* Y, hipStream_t stream);
+hipError_t fp8_launch_linear(const uint8_t* Xq, const float* Xs, const uint8_t* Wq, const float* Ws, int64_t M,
+                             int64_t N, int64_t K, uint16_t* Y, hipStream_t stream);

@@ -116,6 +116,22 @@ int decode_step(const char* who, const void* X, int64_t M, int64_t K, int64_t ld
   return launched(who, e);
 }
 
+// Checks shared by the 8-bit quantizers and the norm: X [M, ld] bf16 -> codes [M, K], scales.
+int check_fp8_rows(const char* who, const void* X, int64_t M, int64_t K, int64_t ld, const uint8_t* codes,
+                   const float* scales) {
+  if (!X || !codes || !scales) return fail(FP4_E_NULLPTR, "%s: input, codes and scales must be non-NULL", who);
+  if (M < 1 || K < 128 || K % 128)
+    return fail(FP4_E_SHAPE, "%s: need rows >= 1 and K a positive multiple of 128 (rows=%lld K=%lld)", who,
+                (long long)M, (long long)K);
+  if (ld < K || ld > (int64_t)1 << 40)
+    return fail(FP4_E_SHAPE, "%s: leading dimension %lld < K=%lld, or too large", who, (long long)ld, (long long)K);
+  if (M > 0x7FFFFFFFLL / (K / 8)) return fail(FP4_E_SHAPE, "%s: tensor too large (rows*K/8 must fit in 31 bits)", who);
+  if (!aligned(X, 16) || ld % 8) return fail(FP4_E_ALIGN, "%s: input must be 16-byte aligned, ld %% 8 == 0", who);
+  if (!aligned(codes, 16) || !aligned(scales, 4))
+    return fail(FP4_E_ALIGN, "%s: codes must be 16-byte aligned, scales 4-byte aligned", who);
+  return FP4_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -202,6 +218,65 @@ int fp4_rotate_quantize_linear_noalloc(const void* X, int64_t M, int64_t K, int6
   const hipError_t e = fp4_decode_scratch(&ws);
   if (e != hipSuccess) return launched(who, e);
   return decode_step(who, X, M, K, ldx, block, Wq, Ws, N, Y, y_dtype, ws, stream);
+}
+
+int fp8_quantize(const void* X, int64_t M, int64_t K, int64_t ldx, uint8_t* codes, float* scales, void* stream) {
+  const char* who = "fp8_quantize";
+  const int st = check_fp8_rows(who, X, M, K, ldx, codes, scales);
+  if (st != FP4_OK) return st;
+  return launched(who, fp8_launch_quantize(static_cast<const uint16_t*>(X), M, K, ldx, codes, scales,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+int fp8_quantize_weights(const void* W, int64_t N, int64_t K, int64_t ldw, uint8_t* codes, float* scales,
+                         void* stream) {
+  const char* who = "fp8_quantize_weights";
+  const int st = check_fp8_rows(who, W, N, K, ldw, codes, scales);
+  if (st != FP4_OK) return st;
+  return launched(who, fp8_launch_quantize_weights(static_cast<const uint16_t*>(W), N, K, ldw, codes, scales,
+                                                   static_cast<hipStream_t>(stream)));
+}
+
+int fp8_add_rmsnorm_quantize(const void* X, int64_t M, int64_t K, int64_t ldx, const void* residual, int64_t ldr,
+                             const void* weight, float eps, uint8_t* codes, float* scales, void* residual_out,
+                             void* normed, void* stream) {
+  const char* who = "fp8_add_rmsnorm_quantize";
+  const int st = check_fp8_rows(who, X, M, K, ldx, codes, scales);
+  if (st != FP4_OK) return st;
+  if (!weight) return fail(FP4_E_NULLPTR, "%s: weight must be non-NULL", who);
+  if ((residual == nullptr) != (residual_out == nullptr))
+    return fail(FP4_E_NULLPTR, "%s: residual and residual_out go together", who);
+  if (K > 65536) return fail(FP4_E_SHAPE, "%s: K=%lld above 65536", who, (long long)K);
+  if (residual && (ldr < K || ldr > (int64_t)1 << 40))
+    return fail(FP4_E_SHAPE, "%s: residual leading dimension %lld < K=%lld, or too large", who, (long long)ldr,
+                (long long)K);
+  if (residual && residual == residual_out && ldr != K)
+    return fail(FP4_E_SHAPE, "%s: a residual written in place needs ldr == K", who);
+  if (!(eps >= 0.f) || eps > 3.0e38f) return fail(FP4_E_SHAPE, "%s: eps must be finite and not negative", who);
+  if (!aligned(weight, 16) || (residual && (!aligned(residual, 16) || ldr % 8 || !aligned(residual_out, 16))) ||
+      (normed && !aligned(normed, 16)))
+    return fail(FP4_E_ALIGN, "%s: weight, residual and outputs must be 16-byte aligned, ldr %% 8 == 0", who);
+  return launched(who, fp8_launch_add_rmsnorm_quantize(
+                           static_cast<const uint16_t*>(X), M, K, ldx, static_cast<const uint16_t*>(residual), ldr,
+                           static_cast<const uint16_t*>(weight), eps, codes, scales,
+                           static_cast<uint16_t*>(residual_out), static_cast<uint16_t*>(normed),
+                           static_cast<hipStream_t>(stream)));
+}
+
+int fp8_linear(const uint8_t* Xq, const float* Xs, const uint8_t* Wq, const float* Ws, int64_t M, int64_t N, int64_t K,
+               void* Y, void* stream) {
+  const char* who = "fp8_linear";
+  if (!Xq || !Xs || !Wq || !Ws || !Y) return fail(FP4_E_NULLPTR, "%s: operand pointers must be non-NULL", who);
+  if (M < 1 || N < 1 || K < 128 || K % 128)
+    return fail(FP4_E_SHAPE, "%s: need M, N >= 1 and K a positive multiple of 128 (M=%lld N=%lld K=%lld)", who,
+                (long long)M, (long long)N, (long long)K);
+  if (M > 0x7FFFFFFF || N > 0x7FFFFFFF || K > (1 << 24) || M * K > ((int64_t)1 << 40) || N * K > ((int64_t)1 << 40) ||
+      ((M + 127) / 128) * ((N + 63) / 64) > 0x7FFFFFFF)
+    return fail(FP4_E_SHAPE, "%s: problem too large", who);
+  if (!aligned(Xq, 16) || !aligned(Wq, 16) || !aligned(Xs, 4) || !aligned(Ws, 4) || !aligned(Y, 16))
+    return fail(FP4_E_ALIGN, "%s: codes and Y must be 16-byte aligned, scales 4-byte aligned", who);
+  return launched(who, fp8_launch_linear(Xq, Xs, Wq, Ws, M, N, K, static_cast<uint16_t*>(Y),
+                                         static_cast<hipStream_t>(stream)));
 }
 
 const char* fp4_last_error(void) { return g_err; }
