@@ -312,7 +312,7 @@ FP4_API int fp8_add_rmsnorm_quantize(const void *X, int64_t M, int64_t K, int64_
  *  Xq, Xs  device uint8 [M, K], float [M, K / 128]               (fp8_quantize, fp8_add_rmsnorm_quantize)
  *  Wq, Ws  device uint8 [N, K], float [ceil(N / 128), K / 128]   (fp8_quantize_weights)
  *  Y       device bf16 [M, N] row-major.
- *  M, N >= 1, at most 2^31 - 1; K <= 2^24; M * K and N * K <= 2^40.
+ *  M, N >= 1, at most 2^31 - 1; K <= 2^23; M * K and N * K <= 2^40.
  *  Xq, Wq and Y 16-byte aligned, Xs and Ws 4-byte aligned.
  * Results do not depend on timing: partial sums meet in a fixed order.
  * Errors: FP4_E_NULLPTR, FP4_E_SHAPE, FP4_E_ALIGN.

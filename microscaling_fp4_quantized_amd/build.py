@@ -28,6 +28,7 @@ SOURCES = [
     "gemm_nvfp4_ring.hip",
     "fp8_quant.hip",
     "gemm_fp8_decode.hip",
+    "gemm_fp8_ring.hip",
     "fp4_abi.cpp",
 ]
 

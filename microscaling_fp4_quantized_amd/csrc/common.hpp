@@ -137,3 +137,5 @@ hipError_t fp8_launch_add_rmsnorm_quantize(const uint16_t* X, int64_t M, int64_t
                                            uint16_t* H, uint16_t* Y, hipStream_t stream);
 hipError_t fp8_launch_linear(const uint8_t* Xq, const float* Xs, const uint8_t* Wq, const float* Ws, int64_t M,
                              int64_t N, int64_t K, uint16_t* Y, hipStream_t stream);
+hipError_t fp8_launch_linear_ring(const uint8_t* Xq, const float* Xs, const uint8_t* Wq, const float* Ws, int64_t M,
+                                  int64_t N, int64_t K, uint16_t* Y, hipStream_t stream);

@@ -270,7 +270,7 @@ int fp8_linear(const uint8_t* Xq, const float* Xs, const uint8_t* Wq, const floa
   if (M < 1 || N < 1 || K < 128 || K % 128)
     return fail(FP4_E_SHAPE, "%s: need M, N >= 1 and K a positive multiple of 128 (M=%lld N=%lld K=%lld)", who,
                 (long long)M, (long long)N, (long long)K);
-  if (M > 0x7FFFFFFF || N > 0x7FFFFFFF || K > (1 << 24) || M * K > ((int64_t)1 << 40) || N * K > ((int64_t)1 << 40) ||
+  if (M > 0x7FFFFFFF || N > 0x7FFFFFFF || K > (1 << 23) || M * K > ((int64_t)1 << 40) || N * K > ((int64_t)1 << 40) ||
       ((M + 127) / 128) * ((N + 63) / 64) > 0x7FFFFFFF)
     return fail(FP4_E_SHAPE, "%s: problem too large", who);
   if (!aligned(Xq, 16) || !aligned(Wq, 16) || !aligned(Xs, 4) || !aligned(Ws, 4) || !aligned(Y, 16))

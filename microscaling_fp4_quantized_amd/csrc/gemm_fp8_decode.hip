@@ -188,7 +188,8 @@ hipError_t fp8_launch_linear(const uint8_t* Xq, const float* Xs, const uint8_t* 
   auto go = [&](auto mf) {
     return fp4::launch<1, decltype(mf)::value>(Xq, Xs, Wq, Ws, M, (int)N, (int)K, Y, st);
   };
-  switch (M > 64 ? 4 : (int)((M + 15) / 16)) {
+  if (M > 64) return fp8_launch_linear_ring(Xq, Xs, Wq, Ws, M, N, K, Y, st);
+  switch ((int)((M + 15) / 16)) {
     case 1: return go(std::integral_constant<int, 1>{});
     case 2: return go(std::integral_constant<int, 2>{});
     case 3: return go(std::integral_constant<int, 3>{});

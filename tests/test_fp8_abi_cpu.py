@@ -52,7 +52,7 @@ def test_linear_validation(lib):
 
     assert f(Xq=None) == f(Xs=None) == f(Wq=None) == f(Ws=None) == f(Y=None) == NULLPTR
     assert f(M=0) == f(N=0) == f(K=0) == f(K=64) == f(K=320) == SHAPE
-    assert f(M=1 << 31) == f(N=1 << 31) == f(K=(1 << 24) + 128) == f(M=1 << 30, K=1 << 14) == SHAPE
+    assert f(M=1 << 31) == f(N=1 << 31) == f(K=(1 << 23) + 128) == f(M=1 << 30, K=1 << 14) == SHAPE
     assert f(M=(1 << 31) - 1, N=(1 << 31) - 1) == SHAPE  # more tiles than a grid holds
     assert f(Xq=A16 + 8) == f(Wq=A16 + 4) == f(Y=A16 + 8) == f(Xs=A16 + 2) == f(Ws=A16 + 1) == ALIGN
     assert b"fp8_linear" in lib.fp4_last_error()
