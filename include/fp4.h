@@ -320,6 +320,55 @@ FP4_API int fp8_add_rmsnorm_quantize(const void *X, int64_t M, int64_t K, int64_
 FP4_API int fp8_linear(const uint8_t *Xq, const float *Xs, const uint8_t *Wq, const float *Ws, int64_t M, int64_t N,
                        int64_t K, void *Y, void *stream);
 
+/*
+ * Mixture of experts for a few tokens, over MXFP4 experts.
+ *
+ * fp4_moe_route - the router: p = softmax(X Wr^T) over the E experts in float32, the k of the largest
+ * logits of each token in falling order (of equal ones the lowest index first; NaN below every number).
+ *  X        device bf16 [T, ldx], ldx >= D, ldx % 8 == 0.   Wr  device bf16 [E, D].
+ *  T >= 1, T * E < 2^31; D a positive multiple of 128, at most 2^24; 1 <= E <= 1024; 1 <= k <= min(E, 16).
+ *  renormalize  non-zero: the k weights of a token are divided by their sum.
+ *  ids      device int [T, k].   weights  device float [T, k].
+ *  workspace, workspace_bytes  device buffer of at least FP4_MOE_ROUTE_WORKSPACE_BYTES(T, E) bytes.
+ * X, Wr and workspace 16-byte aligned, ids and weights 4-byte aligned. Two launches on `stream`.
+ *
+ * fp4_moe_experts - Y[t] = sum_j weights[t, j] * W2[e] H (silu(G[e] H X[t]) * (U[e] H X[t])), e = ids[t, j], silu(a) =
+ * a / (1 + exp(-a)), H the block Hadamard rotation of fp4_rotate_quantize. The weights are MXFP4 as
+ * fp4_quantize_weights makes them (in the rotated basis); the activations are not quantized to 4 bits: they
+ * enter as sums of three E4M3 numbers (12 bits and more), all sums are float32, and Y is rounded once.
+ *  X            device bf16 [T, ldx], ldx >= D, ldx % 8 == 0; 1 <= T <= FP4_MOE_MAX_TOKENS.
+ *  ids          device int [T, k], weights device float [T, k], 1 <= k <= FP4_MOE_MAX_TOPK. A slot whose id is
+ *               outside [0, E) (-1, say) is unused and adds nothing; a token without a used slot gets zeros.
+ *               An expert may stand in several slots of a token.
+ *  W13q, W13s   uint8 [E, 2 I, D / 2] codes and [E, 2 I, D / 32] scales: rows 0 .. I-1 of an expert are G, the
+ *               other I are U.   W2q, W2s  uint8 [E, D, I / 2] and [E, D, I / 32].
+ *  block        16, 32, 64 or 128 (the block the weights were quantized with).
+ *  D, I multiples of 128, at most 65536; 1 <= E <= 1024.
+ *  Y            device bf16 [T, D].
+ *  workspace, workspace_bytes  device buffer of at least FP4_MOE_WORKSPACE_BYTES(T, k, D, I) bytes.
+ * Device buffers 16-byte aligned, ids and weights 4-byte aligned. Results do not depend on timing.
+ * A NaN or infinity in X[t] makes Y[t] NaN and no other row.
+ * Errors of both: FP4_E_BLOCK, FP4_E_NULLPTR, FP4_E_SHAPE (also a short workspace), FP4_E_ALIGN.
+ */
+#define FP4_MOE_MAX_TOKENS 128
+#define FP4_MOE_MAX_TOPK 16
+#define FP4_MOE_PAD_(n) (((size_t)(n) + 255) / 256 * 256)
+#define FP4_MOE_ROUTE_WORKSPACE_BYTES(T, E) ((size_t)(T) * (E) * 4)
+/* the experts' workspace: terms and scales of X, h, its terms and scales, the slots' outputs */
+#define FP4_MOE_WS_XS(T, k, D, I) FP4_MOE_PAD_((size_t)(T) * 3 * (D))
+#define FP4_MOE_WS_H(T, k, D, I) (FP4_MOE_WS_XS(T, k, D, I) + FP4_MOE_PAD_((size_t)(T) * (D) / 32))
+#define FP4_MOE_WS_HQ(T, k, D, I) (FP4_MOE_WS_H(T, k, D, I) + FP4_MOE_PAD_((size_t)(T) * (k) * (I) * 4))
+#define FP4_MOE_WS_HS(T, k, D, I) (FP4_MOE_WS_HQ(T, k, D, I) + FP4_MOE_PAD_((size_t)(T) * (k) * 3 * (I)))
+#define FP4_MOE_WS_OUT(T, k, D, I) (FP4_MOE_WS_HS(T, k, D, I) + FP4_MOE_PAD_((size_t)(T) * (k) * (I) / 32))
+#define FP4_MOE_WORKSPACE_BYTES(T, k, D, I) (FP4_MOE_WS_OUT(T, k, D, I) + (size_t)(T) * (k) * (D) * 4)
+FP4_API int fp4_moe_route(const void *X, int64_t T, int64_t D, int64_t ldx, const void *Wr, int64_t E, int k,
+                          int renormalize, int *ids, float *weights, void *workspace, size_t workspace_bytes,
+                          void *stream);
+FP4_API int fp4_moe_experts(const void *X, int64_t T, int64_t D, int64_t ldx, const int *ids, const float *weights,
+                            int k, int64_t E, int64_t I, int block, const uint8_t *W13q, const uint8_t *W13s,
+                            const uint8_t *W2q, const uint8_t *W2s, void *Y, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
 /* Message for the last non-OK status returned on this thread ("" if none). */
 FP4_API const char *fp4_last_error(void);
 

@@ -28,6 +28,9 @@ __all__ = [
     "fp8_quantize_weights",
     "fp8_add_rmsnorm_quantize",
     "fp8_linear",
+    "fp4_moe_route",
+    "fp4_moe_experts",
+    "moe_workspace_bytes",
     "fp4_abi_version",
     "group_size",
 ]
@@ -86,6 +89,11 @@ def load_library() -> ctypes.CDLL:
     lib.fp8_add_rmsnorm_quantize.restype = i32
     lib.fp8_linear.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, vp]
     lib.fp8_linear.restype = i32
+    lib.fp4_moe_route.argtypes = [vp, i64, i64, i64, vp, i64, i32, i32, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.fp4_moe_route.restype = i32
+    lib.fp4_moe_experts.argtypes = [vp, i64, i64, i64, vp, vp, i32, i64, i64, i32, vp, vp, vp, vp, vp, vp,
+                                    ctypes.c_size_t, vp]
+    lib.fp4_moe_experts.restype = i32
     lib.fp4_last_error.argtypes = []
     lib.fp4_last_error.restype = ctypes.c_char_p
     lib.fp4_abi_version.argtypes = []
@@ -416,6 +424,87 @@ def fp8_linear(xq, xs, wq, ws, out=None):
     _same_device(name, xq.device, xs, wq, ws, out)
     _check(_launch(xq.device, lib.fp8_linear, xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), M, N, K,
                    out.data_ptr()))
+    return out
+
+
+def _workspace(workspace, need, name, dev):
+    if isinstance(workspace, str) and workspace == "auto":
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or workspace.dtype != torch.uint8 or \
+            not workspace.is_contiguous():
+        raise ValueError(f'{name}: workspace must be "auto" or a contiguous uint8 CUDA tensor')
+    if workspace.numel() < need:
+        raise ValueError(f"{name}: workspace too small, {need} bytes needed")
+    return workspace
+
+
+def fp4_moe_route(x: torch.Tensor, router: torch.Tensor, k: int, renormalize: bool = True, out=None, workspace="auto"):
+    """softmax(x router^T) in float32 and its k largest of each token: (ids [T, k] int32, weights [T, k] float32).
+
+    x bf16 [T, D], router bf16 [E, D]. Of equal weights the lowest expert comes first. ``out`` may pass
+    preallocated (ids, weights); workspace: "auto", or a uint8 CUDA tensor of at least 4 T E bytes."""
+    name = "fp4_moe_route"
+    lib = load_library()
+    T, D, ld = _rows(x, name, "x")
+    if not isinstance(router, torch.Tensor) or router.dim() != 2:
+        raise ValueError(f"{name}: router must be a 2-D tensor")
+    E, k = router.shape[0], int(k)
+    _expect(router, (E, D), torch.bfloat16, name, "router")
+    if out is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=x.device)
+        weights = torch.empty((T, k), dtype=torch.float32, device=x.device)
+    else:
+        ids, weights = out
+        _expect(ids, (T, k), torch.int32, name, "ids")
+        _expect(weights, (T, k), torch.float32, name, "weights")
+    ws = _workspace(workspace, 4 * T * E, name, x.device)
+    _same_device(name, x.device, router, ids, weights, ws)
+    _check(_launch(x.device, lib.fp4_moe_route, x.data_ptr(), T, D, ld, router.data_ptr(), E, k, int(bool(renormalize)),
+                   ids.data_ptr(), weights.data_ptr(), ws.data_ptr(), ws.numel()))
+    return ids, weights
+
+
+def moe_workspace_bytes(T: int, k: int, D: int, I: int) -> int:
+    """FP4_MOE_WORKSPACE_BYTES(T, k, D, I) of include/fp4.h."""
+    def pad(n):
+        return (n + 255) // 256 * 256
+    P = T * k
+    return pad(T * 3 * D) + pad(T * D // 32) + pad(P * I * 4) + pad(P * 3 * I) + pad(P * I // 32) + P * D * 4
+
+
+def fp4_moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13q, w13s, w2q, w2s, block: int,
+                    out=None, workspace="auto"):
+    """y_t = sum_j weights[t, j] W2[e] H (silu(G[e] H x_t) * (U[e] H x_t)), e = ids[t, j]: the experts of a
+    mixture-of-experts layer for up to 128 tokens, [T, D] in bf16.
+
+    x bf16 [T, D]; ids int32 and weights float32 [T, k] (fp4_moe_route); an id outside [0, E) leaves its slot out.
+    The experts' matrices are MXFP4 from fp4_quantize_weights with this ``block``: w13q uint8 [E, 2I, D/2] and w13s
+    [E, 2I, D/32], gate rows first, w2q [E, D, I/2] and w2s [E, D, I/32]. workspace: "auto", or a uint8 CUDA
+    tensor of at least moe_workspace_bytes(T, k, D, I)."""
+    name = "fp4_moe_experts"
+    lib = load_library()
+    T, D, ld = _rows(x, name, "x")
+    for t, what in ((w13q, "w13q"), (w2q, "w2q")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            raise ValueError(f"{name}: {what} must be a 3-D tensor of codes")
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError(f"{name}: ids must be a 2-D tensor")
+    E, I, k = w13q.shape[0], 2 * w2q.shape[2], ids.shape[1]
+    _expect(ids, (T, k), torch.int32, name, "ids")
+    _expect(weights, (T, k), torch.float32, name, "weights")
+    _expect(w13q, (E, 2 * I, D // 2), torch.uint8, name, "w13q")
+    _expect(w13s, (E, 2 * I, D // 32), torch.uint8, name, "w13s")
+    _expect(w2q, (E, D, I // 2), torch.uint8, name, "w2q")
+    _expect(w2s, (E, D, I // 32), torch.uint8, name, "w2s")
+    if out is None:
+        out = torch.empty((T, D), dtype=torch.bfloat16, device=x.device)
+    else:
+        _expect(out, (T, D), torch.bfloat16, name, "out")
+    ws = _workspace(workspace, moe_workspace_bytes(T, k, D, I), name, x.device)
+    _same_device(name, x.device, ids, weights, w13q, w13s, w2q, w2s, out, ws)
+    _check(_launch(x.device, lib.fp4_moe_experts, x.data_ptr(), T, D, ld, ids.data_ptr(), weights.data_ptr(), k, E, I,
+                   int(block), w13q.data_ptr(), w13s.data_ptr(), w2q.data_ptr(), w2s.data_ptr(), out.data_ptr(),
+                   ws.data_ptr(), ws.numel()))
     return out
 
 

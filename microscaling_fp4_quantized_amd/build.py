@@ -29,6 +29,7 @@ SOURCES = [
     "fp8_quant.hip",
     "gemm_fp8_decode.hip",
     "gemm_fp8_ring.hip",
+    "moe.hip",
     "fp4_abi.cpp",
 ]
 

@@ -139,3 +139,11 @@ hipError_t fp8_launch_linear(const uint8_t* Xq, const float* Xs, const uint8_t* 
                              int64_t N, int64_t K, uint16_t* Y, hipStream_t stream);
 hipError_t fp8_launch_linear_ring(const uint8_t* Xq, const float* Xs, const uint8_t* Wq, const float* Ws, int64_t M,
                                   int64_t N, int64_t K, uint16_t* Y, hipStream_t stream);
+
+// Mixture of experts for a few tokens.
+hipError_t fp4_launch_moe_route(const uint16_t* X, int64_t T, int64_t D, int64_t ldx, const uint16_t* Wr, int64_t E, int k,
+                                int renorm, float* logits, int* ids, float* weights, hipStream_t stream);
+hipError_t fp4_launch_moe_experts(const uint16_t* X, int64_t T, int64_t D, int64_t ldx, const int* ids,
+                                  const float* weights, int k, int64_t E, int64_t I, int block, const uint8_t* W13q,
+                                  const uint8_t* W13s, const uint8_t* W2q, const uint8_t* W2s, uint16_t* Y,
+                                  uint8_t* workspace, hipStream_t stream);

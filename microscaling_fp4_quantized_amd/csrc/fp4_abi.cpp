@@ -279,6 +279,54 @@ int fp8_linear(const uint8_t* Xq, const float* Xs, const uint8_t* Wq, const floa
                                          static_cast<hipStream_t>(stream)));
 }
 
+int fp4_moe_route(const void* X, int64_t T, int64_t D, int64_t ldx, const void* Wr, int64_t E, int k, int renormalize,
+                  int* ids, float* weights, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* who = "fp4_moe_route";
+  if (!X || !Wr || !ids || !weights || !workspace) return fail(FP4_E_NULLPTR, "%s: pointers must be non-NULL", who);
+  if (T < 1 || D < 128 || D % 128 || D > (1 << 24) || E < 1 || E > 1024 || T > 0x7FFFFFFFLL / E || (T + 15) / 16 > 65535)
+    return fail(FP4_E_SHAPE, "%s: need T >= 1, D a positive multiple of 128, 1 <= E <= 1024 (T=%lld D=%lld E=%lld)", who,
+                (long long)T, (long long)D, (long long)E);
+  if (k < 1 || k > FP4_MOE_MAX_TOPK || k > E)
+    return fail(FP4_E_SHAPE, "%s: k=%d not in 1 .. min(E, %d)", who, k, FP4_MOE_MAX_TOPK);
+  if (ldx < D || ldx > (int64_t)1 << 40) return fail(FP4_E_SHAPE, "%s: leading dimension %lld < D", who, (long long)ldx);
+  if (workspace_bytes < FP4_MOE_ROUTE_WORKSPACE_BYTES(T, E))
+    return fail(FP4_E_SHAPE, "%s: workspace of %zu bytes, %zu needed", who, workspace_bytes,
+                FP4_MOE_ROUTE_WORKSPACE_BYTES(T, E));
+  if (!aligned(X, 16) || ldx % 8 || !aligned(Wr, 16) || !aligned(workspace, 16) || !aligned(ids, 4) || !aligned(weights, 4))
+    return fail(FP4_E_ALIGN, "%s: X, Wr and workspace must be 16-byte aligned, ldx %% 8 == 0, ids and weights 4-byte aligned",
+                who);
+  return launched(who, fp4_launch_moe_route(static_cast<const uint16_t*>(X), T, D, ldx, static_cast<const uint16_t*>(Wr), E,
+                                            k, renormalize, static_cast<float*>(workspace), ids, weights,
+                                            static_cast<hipStream_t>(stream)));
+}
+
+int fp4_moe_experts(const void* X, int64_t T, int64_t D, int64_t ldx, const int* ids, const float* weights, int k,
+                    int64_t E, int64_t I, int block, const uint8_t* W13q, const uint8_t* W13s, const uint8_t* W2q,
+                    const uint8_t* W2s, void* Y, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* who = "fp4_moe_experts";
+  if (block != 16 && block != 32 && block != 64 && block != 128)
+    return fail(FP4_E_BLOCK, "%s: Hadamard block %d not in {16, 32, 64, 128}", who, block);
+  if (!X || !ids || !weights || !W13q || !W13s || !W2q || !W2s || !Y || !workspace)
+    return fail(FP4_E_NULLPTR, "%s: pointers must be non-NULL", who);
+  if (T < 1 || T > FP4_MOE_MAX_TOKENS || k < 1 || k > FP4_MOE_MAX_TOPK)
+    return fail(FP4_E_SHAPE, "%s: need 1 <= T <= %d and 1 <= k <= %d (T=%lld k=%d)", who, FP4_MOE_MAX_TOKENS,
+                FP4_MOE_MAX_TOPK, (long long)T, k);
+  if (E < 1 || E > 1024 || D < 128 || D % 128 || D > 65536 || I < 128 || I % 128 || I > 65536)
+    return fail(FP4_E_SHAPE, "%s: need 1 <= E <= 1024, D and I multiples of 128 up to 65536 (E=%lld D=%lld I=%lld)", who,
+                (long long)E, (long long)D, (long long)I);
+  if (ldx < D || ldx > (int64_t)1 << 40) return fail(FP4_E_SHAPE, "%s: leading dimension %lld < D", who, (long long)ldx);
+  if (workspace_bytes < FP4_MOE_WORKSPACE_BYTES(T, k, D, I))
+    return fail(FP4_E_SHAPE, "%s: workspace of %zu bytes, %zu needed", who, workspace_bytes,
+                FP4_MOE_WORKSPACE_BYTES(T, k, D, I));
+  if (!aligned(X, 16) || ldx % 8 || !aligned(W13q, 16) || !aligned(W13s, 16) || !aligned(W2q, 16) || !aligned(W2s, 16) ||
+      !aligned(Y, 16) || !aligned(workspace, 16) || !aligned(ids, 4) || !aligned(weights, 4))
+    return fail(FP4_E_ALIGN, "%s: X, matrices, Y and workspace must be 16-byte aligned, ldx %% 8 == 0, ids and weights 4-byte "
+                "aligned", who);
+  return launched(who, fp4_launch_moe_experts(static_cast<const uint16_t*>(X), T, D, ldx, ids, weights, k, E, I, block,
+                                              W13q, W13s, W2q, W2s, static_cast<uint16_t*>(Y),
+                                              static_cast<uint8_t*>(workspace), static_cast<hipStream_t>(stream)));
+}
+
 const char* fp4_last_error(void) { return g_err; }
 
 int fp4_abi_version(void) { return 130; }
