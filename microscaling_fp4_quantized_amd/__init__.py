@@ -16,5 +16,6 @@ def __getattr__(name):
                 "FP4_NVFP4", "fp8_quantize", "fp8_quantize_weights", "fp8_add_rmsnorm_quantize", "fp8_linear",
                 "fp4_moe_route", "fp4_moe_experts", "moe_workspace_bytes"):
         from . import binding
-        return getattr(binding, name)
+        value = globals()[name] = getattr(binding, name)  # found at once from now on
+        return value
     raise AttributeError(name)

@@ -111,7 +111,14 @@ def _ptr(t):
 
 
 def _stream(dev):
-    return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    """The handle of the device's current stream. torch.cuda.current_stream builds a Stream object around it
+    (1.7 us a call, a fifth of a small call's host time); the raw form returns the number (0.06 us)."""
+    if _RAW_STREAM is not None:
+        return _RAW_STREAM(dev.index)
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+_RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _launch(dev, fn, *args):
@@ -124,6 +131,18 @@ def _launch(dev, fn, *args):
         with torch.cuda.device(dev):
             return fn(*args, _stream(dev))
     return fn(*args, _stream(dev))
+
+
+def _enqueue(fn, dev, *args):
+    """Call an entry point on the operands' device and its current stream; raise what it refuses."""
+    index = dev.index
+    if torch.cuda.current_device() == index:
+        status = fn(*args, _stream(dev))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _stream(dev))
+    if status:
+        _check(status)
 
 
 def _same_device(name, dev, *tensors):
@@ -145,7 +164,7 @@ def _expect(t, shape, dtype, name, what):
     """Refuse anything but a contiguous CUDA tensor of this shape and dtype: the kernels take plain
     pointers and trust the sizes they imply, so a short buffer would be read or written out of bounds."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or \
-            tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+            t.shape != shape or not t.is_contiguous():
         got = repr(t) if not isinstance(t, torch.Tensor) else f"{tuple(t.shape)} {t.dtype} on {t.device}"
         raise ValueError(f"{name}: {what} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}, got {got}")
 
@@ -345,7 +364,7 @@ def _quantize8(name, x, rows, out):
         _expect(codes, (M, K), torch.float8_e4m3fn, name, "codes")
         _expect(scales, shape, torch.float32, name, "scales")
         _same_device(name, x.device, codes, scales)
-    _check(_launch(x.device, getattr(lib, name), x.data_ptr(), M, K, ld, codes.data_ptr(), scales.data_ptr()))
+    _enqueue(getattr(lib, name), x.device, x.data_ptr(), M, K, ld, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -396,10 +415,9 @@ def fp8_add_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual=Non
             if t is not None:
                 _expect(t, (M, K), torch.bfloat16, name, what)
     _same_device(name, dev, weight, residual, codes, scales, h, n)
-    _check(_launch(dev, lib.fp8_add_rmsnorm_quantize, x.data_ptr(), M, K, ld,
-                   residual.data_ptr() if residual is not None else None, ldr, weight.data_ptr(), eps,
-                   codes.data_ptr(), scales.data_ptr(), h.data_ptr() if h is not None else None,
-                   n.data_ptr() if n is not None else None))
+    _enqueue(lib.fp8_add_rmsnorm_quantize, dev, x.data_ptr(), M, K, ld,
+             residual.data_ptr() if residual is not None else None, ldr, weight.data_ptr(), eps, codes.data_ptr(),
+             scales.data_ptr(), h.data_ptr() if h is not None else None, n.data_ptr() if n is not None else None)
     return codes, scales, h, n
 
 
@@ -422,8 +440,8 @@ def fp8_linear(xq, xs, wq, ws, out=None):
     else:
         _expect(out, (M, N), torch.bfloat16, name, "out")
     _same_device(name, xq.device, xs, wq, ws, out)
-    _check(_launch(xq.device, lib.fp8_linear, xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), M, N, K,
-                   out.data_ptr()))
+    _enqueue(lib.fp8_linear, xq.device, xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), M, N, K,
+             out.data_ptr())
     return out
 
 
@@ -459,8 +477,8 @@ def fp4_moe_route(x: torch.Tensor, router: torch.Tensor, k: int, renormalize: bo
         _expect(weights, (T, k), torch.float32, name, "weights")
     ws = _workspace(workspace, 4 * T * E, name, x.device)
     _same_device(name, x.device, router, ids, weights, ws)
-    _check(_launch(x.device, lib.fp4_moe_route, x.data_ptr(), T, D, ld, router.data_ptr(), E, k, int(bool(renormalize)),
-                   ids.data_ptr(), weights.data_ptr(), ws.data_ptr(), ws.numel()))
+    _enqueue(lib.fp4_moe_route, x.device, x.data_ptr(), T, D, ld, router.data_ptr(), E, k, int(bool(renormalize)),
+             ids.data_ptr(), weights.data_ptr(), ws.data_ptr(), ws.numel())
     return ids, weights
 
 
@@ -469,7 +487,7 @@ def moe_workspace_bytes(T: int, k: int, D: int, I: int) -> int:
     def pad(n):
         return (n + 255) // 256 * 256
     P = T * k
-    return pad(T * 3 * D) + pad(T * D // 32) + pad(P * I * 4) + pad(P * 3 * I) + pad(P * I // 32) + P * D * 4
+    return pad(T * 3 * D) + pad(T * D // 32) + pad(P * I * 4) + pad(P * 3 * I) + pad(P * I // 32) + pad(P * D * 4) + 20 * P
 
 
 def fp4_moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13q, w13s, w2q, w2s, block: int,
@@ -502,9 +520,9 @@ def fp4_moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w
         _expect(out, (T, D), torch.bfloat16, name, "out")
     ws = _workspace(workspace, moe_workspace_bytes(T, k, D, I), name, x.device)
     _same_device(name, x.device, ids, weights, w13q, w13s, w2q, w2s, out, ws)
-    _check(_launch(x.device, lib.fp4_moe_experts, x.data_ptr(), T, D, ld, ids.data_ptr(), weights.data_ptr(), k, E, I,
-                   int(block), w13q.data_ptr(), w13s.data_ptr(), w2q.data_ptr(), w2s.data_ptr(), out.data_ptr(),
-                   ws.data_ptr(), ws.numel()))
+    _enqueue(lib.fp4_moe_experts, x.device, x.data_ptr(), T, D, ld, ids.data_ptr(), weights.data_ptr(), k, E, I,
+             int(block), w13q.data_ptr(), w13s.data_ptr(), w2q.data_ptr(), w2s.data_ptr(), out.data_ptr(),
+             ws.data_ptr(), ws.numel())
     return out
 
 

@@ -13,15 +13,11 @@
 // 16 columns, and are added in float32 at the end. The factors 16^-i ride in the E8M0 scale operand.
 //
 // Steps of a call (each a launch; every sum in a fixed order):
-//   split x    rotate (float32), split into terms                  [T, 3, D]
-//   up         per expert and 16 features of h: gate and up rows, silu(g) * u in float32   [T k, I]
-//   split h    rotate, split                                       [T k, 3, I]
-//   down       per expert and 32 output features                   [T k, D] float32
+//   split x    rotate (float32), split into terms   [T, 3, D]; one more workgroup sorts the pairs by expert
+//   up         per used expert and 16 features of h: gate and up rows, silu(g) * u in float32   [T k, I]
+//   split h    rotate, split                        [T k, 3, I]
+//   down       per used expert and 32 output features                                           [T k, D] float32
 //   combine    y_t = sum_j p_tj * down, over the slots in order, rounded once to bf16
-// Workgroup (a, tile) finds the a-th used expert from the ids itself: a bit per expert in LDS.
-#include <atomic>
-#include <type_traits>
-
 #include "fp8_device.hpp"
 #include "quant_device.hpp"
 #include "../../include/fp4.h"
@@ -137,13 +133,16 @@ __global__ __launch_bounds__(256) void route_topk(const float* __restrict__ logi
 
 constexpr int kTerms = 3;
 constexpr int kTokens = 5;           // tokens per fragment of 16 columns
-constexpr int kMaxFrags = 4;         // fragments per pass over an expert's weights
-constexpr int kWaves = 4;
-constexpr int kThreads = kWaves * 64;
+constexpr int kMaxFrags = 2;         // fragments per pass over an expert's weights
 constexpr int kSlice = 256;          // bytes (512 elements) of a row per slice
 constexpr int kSliceBytes = 16 * kSlice;
-constexpr int kRing = 2;             // slices a wave holds or has in flight
-constexpr int kMaxPairs = FP4_MOE_MAX_TOKENS * FP4_MOE_MAX_TOPK;
+constexpr int kRing = 2;             // slices of two tiles a wave holds or has in flight
+constexpr int kExpertLds = kRing * 2 * kSliceBytes;  // 16 KB: ten waves on a CU
+
+// The pairs (t k + slot) of one used expert: list[first .. first + n - 1]; n = 0 past the last used expert.
+struct Slot {
+  int expert, first, n, pad;
+};
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_rsrc(const void* base, unsigned bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
@@ -190,16 +189,79 @@ __device__ __forceinline__ void split_chunk(float v[32], uint8_t* q, int64_t ter
   *scale = (uint8_t)(finite ? code : 127);
 }
 
+// Sort the pairs by expert: one workgroup of 256 threads. Ids outside [0, E) name no expert. The order of an
+// expert's pairs in list[] is that of the counter's updates and decides only which column a token has, never a bit
+// of a result.
+__device__ __forceinline__ void plan_experts(const int* __restrict__ ids, int pairs, int E, int slots, Slot* slot,
+                                             int* list) {
+  __shared__ int count[kMaxExperts], first[kMaxExperts], total[2][4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int e = tid; e < kMaxExperts; e += 256) count[e] = 0;
+  __syncthreads();
+  for (int p = tid; p < pairs; p += 256) {
+    const int e = ids[p];
+    if (e >= 0 && e < E) atomicAdd(&count[e], 1);
+  }
+  __syncthreads();
+  // thread tid takes experts 4 tid .. 4 tid + 3: pairs and used experts before them
+  int n[4], pairs_mine = 0, used_mine = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    n[i] = count[4 * tid + i];
+    pairs_mine += n[i];
+    used_mine += n[i] > 0;
+  }
+  int at = pairs_mine, rank = used_mine;  // inclusive sums over the wave, then the waves before
+#pragma unroll
+  for (int h = 1; h < 64; h <<= 1) {
+    const int x = __shfl_up(at, h), y = __shfl_up(rank, h);
+    if (lane >= h) at += x, rank += y;
+  }
+  if (lane == 63) total[0][wave] = at, total[1][wave] = rank;
+  __syncthreads();
+  at -= pairs_mine;
+  rank -= used_mine;
+  int used = 0;
+  for (int w = 0; w < 4; ++w) {
+    if (w < wave) at += total[0][w], rank += total[1][w];
+    used += total[1][w];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    first[4 * tid + i] = at;
+    if (n[i] > 0) slot[rank++] = Slot{4 * tid + i, at, n[i], 0};
+    at += n[i];
+  }
+  for (int i = used + tid; i < slots; i += 256) slot[i] = Slot{0, 0, 0, 0};
+  __syncthreads();
+  for (int p = tid; p < pairs; p += 256) {
+    const int e = ids[p];
+    if (e >= 0 && e < E) list[atomicAdd(&first[e], 1)] = p;
+  }
+}
+
+struct PlanArgs {
+  const int* ids;
+  int pairs, E, slots;
+  Slot* slot;
+  int* list;
+};
+
 // Rows of `cpr` chunks of 32 values -> terms [row][3][32 cpr] and scales [row][cpr]; one lane a chunk. The
-// 2 or 4 chunks of a Hadamard block of 64 or 128 sit in adjacent lanes (cpr % 4 == 0).
-template <int B, bool F32>
+// 2 or 4 chunks of a Hadamard block of 64 or 128 sit in adjacent lanes (cpr % 4 == 0). With PLAN, the first
+// workgroup sorts the pairs instead.
+template <int B, bool PLAN>
 __global__ __launch_bounds__(256) void split_rows(const void* __restrict__ V, int64_t ld, int rows, int cpr,
-                                                  uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
-  const int c = blockIdx.x * 256 + threadIdx.x;
+                                                  uint8_t* __restrict__ q, uint8_t* __restrict__ scales, PlanArgs P) {
+  if (PLAN && blockIdx.x == 0) {
+    plan_experts(P.ids, P.pairs, P.E, P.slots, P.slot, P.list);
+    return;
+  }
+  const int c = (blockIdx.x - (PLAN ? 1 : 0)) * 256 + threadIdx.x;
   if (c >= rows * cpr) return;  // whole quads: rows * cpr % 4 == 0
   const int row = c / cpr, at = c - row * cpr;
   float v[32];
-  if constexpr (F32) {
+  if constexpr (!PLAN) {  // h, float32
     const v4f* p = reinterpret_cast<const v4f*>(reinterpret_cast<const float*>(V) + row * ld + at * 32);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -207,7 +269,7 @@ __global__ __launch_bounds__(256) void split_rows(const void* __restrict__ V, in
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[4 * i + j] = w[j];
     }
-  } else {
+  } else {  // x, bf16
     const v4u* p = reinterpret_cast<const v4u*>(reinterpret_cast<const uint16_t*>(V) + row * ld + at * 32);
 #pragma unroll
     for (int i = 0; i < 4; ++i) widen8(p[i], v + 8 * i);
@@ -216,197 +278,163 @@ __global__ __launch_bounds__(256) void split_rows(const void* __restrict__ V, in
   split_chunk<B>(v, q + row * kTerms * K + at * 32, K, scales + c);
 }
 
-// The a-th used expert (in index order) and its pairs (t k + slot, in order) into list[]; the number of pairs,
-// 0 if fewer than a + 1 experts are used. Ids outside [0, E) name no expert. Every thread calls this.
-__device__ __forceinline__ int find_expert(const int* __restrict__ ids, int pairs, int E, int a, int* used,
-                                           int* list, int* found, int& expert) {
-  const int tid = threadIdx.x, lane = tid & 63;
-  for (int i = tid; i < kMaxExperts / 32; i += kThreads) used[i] = 0;
-  __syncthreads();
-  for (int p = tid; p < pairs; p += kThreads) {
-    const int e = ids[p];
-    if (e >= 0 && e < E) atomicOr(&used[e >> 5], 1 << (e & 31));
-  }
-  __syncthreads();
-  if (tid < 64) {
-    unsigned bits = lane < kMaxExperts / 32 ? (unsigned)used[lane] : 0u;
-    const int mine = __popc(bits);
-    int before = mine;
-#pragma unroll
-    for (int h = 1; h < 64; h <<= 1) {
-      const int o = __shfl_up(before, h);
-      if (lane >= h) before += o;
-    }
-    before -= mine;
-    if (lane == 0) found[0] = -1;
-    __builtin_amdgcn_wave_barrier();
-    if (a >= before && a < before + mine) {
-      for (int j = before; j < a; ++j) bits &= bits - 1;
-      found[0] = lane * 32 + __ffs(bits) - 1;
-    }
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0xC07F);
-    const int e = *(volatile int*)found;
-    int n = 0;
-    if (e >= 0) {
-      for (int p0 = 0; p0 < pairs; p0 += 64) {
-        const bool hit = p0 + lane < pairs && ids[p0 + lane] == e;
-        const uint64_t mask = __ballot(hit);
-        if (hit) list[n + __popcll(mask & ((1ull << lane) - 1))] = p0 + lane;
-        n += __popcll(mask);
-      }
-    }
-    if (lane == 0) found[1] = n;
-  }
-  __syncthreads();
-  expert = found[0];
-  return found[1];
-}
-
-// Two tiles of 16 rows of one expert's matrix by MF fragments of 5 tokens: the slices of 512 elements along K
-// go to the waves in turn, each through its own LDS ring by the LDS DMA; the waves' sums meet in LDS in order.
-// xq [row][3][K], xs [row][K / 32]; rowof[j]: the row of xq that token j of this pass has, n tokens.
-// Afterwards sums[tile][f][col][feature] (float32) is in LDS for all threads.
-template <int MF>
-__device__ __forceinline__ void expert_tiles(uint8_t* lds, const uint8_t* __restrict__ w0, const uint8_t* __restrict__ w1,
-                                             const uint8_t* __restrict__ s0, const uint8_t* __restrict__ s1, int K,
-                                             const uint8_t* __restrict__ xq, const uint8_t* __restrict__ xs,
-                                             const int* rowof, int n) {
-  constexpr int area_bytes = kRing * 2 * kSliceBytes;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int r = lane & 15, g = lane >> 4;
-  const unsigned KB = (unsigned)K / 2, KS = (unsigned)K / 32;
-  const int steps = K / 128, nsl = (steps + 3) / 4;
-  const int mine = nsl > wave ? (nsl - wave + kWaves - 1) / kWaves : 0;
-  uint8_t* area = lds + wave * area_bytes;
-  auto fetch = [&](int j) {
-    const unsigned at = (unsigned)(wave + kWaves * j) * kSlice;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(t ? w1 : w0, 16u * KB);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = 4 * i + g;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(area + ((j % kRing) * 2 + t) * kSliceBytes + i * 1024), 16,
-                                                 (unsigned)row * KB + at + 16u * (unsigned)(r ^ row), 0, 0, 0);
-      }
-    }
-  };
-  const uint8_t* xp[MF];
-  const uint8_t* xsp[MF];
-  const int term = r % kTerms;  // column 15 repeats a term and is not read
-#pragma unroll
-  for (int f = 0; f < MF; ++f) {
-    const int row = rowof[min(kTokens * f + r / kTerms, n - 1)];
-    xp[f] = xq + ((size_t)row * kTerms + term) * K + 16 * g;
-    xsp[f] = xs + (size_t)row * KS;
-  }
-  v4f acc[2][MF];
-#pragma unroll
-  for (int t = 0; t < 2; ++t)
-#pragma unroll
-    for (int f = 0; f < MF; ++f) acc[t][f] = v4f{0.f, 0.f, 0.f, 0.f};
-  for (int j = 0; j < kRing && j < mine; ++j) fetch(j);
-  for (int j = 0; j < mine; ++j) {
-    const int sl = wave + kWaves * j;
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): the slice has landed
-    asm volatile("" ::: "memory");
-    const uint8_t* sp0 = s0 + (size_t)r * KS + 16 * sl;
-    const uint8_t* sp1 = s1 + (size_t)r * KS + 16 * sl;
-    const uint8_t* wa = area + (j % kRing) * 2 * kSliceBytes + r * kSlice;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int step = 4 * sl + u;
-      if (step >= steps) break;  // wave-uniform
-      const v4u a0 = *reinterpret_cast<const v4u*>(wa + 16 * ((4 * u + g) ^ r));
-      const v4u a1 = *reinterpret_cast<const v4u*>(wa + kSliceBytes + 16 * ((4 * u + g) ^ r));
-      const v8i A0 = {(int)a0[0], (int)a0[1], (int)a0[2], (int)a0[3], 0, 0, 0, 0};
-      const v8i A1 = {(int)a1[0], (int)a1[1], (int)a1[2], (int)a1[3], 0, 0, 0, 0};
-      const int sa0 = sp0[4 * u + g], sa1 = sp1[4 * u + g];
-#pragma unroll
-      for (int f = 0; f < MF; ++f) {
-        // E4M3 operand: a lane group's 32 bytes are elements 16 g .. and 64 + 16 g .. of the step's 128
-        // (measured); block b of 32 elements is scaled by the byte of lane group b for either operand
-        const v4u x0 = *reinterpret_cast<const v4u*>(xp[f] + (size_t)step * 128);
-        const v4u x1 = *reinterpret_cast<const v4u*>(xp[f] + (size_t)step * 128 + 64);
-        const v8i B = {(int)x0[0], (int)x0[1], (int)x0[2], (int)x0[3], (int)x1[0], (int)x1[1], (int)x1[2], (int)x1[3]};
-        const int sb = xsp[f][4 * step + g] - 4 * term;
-        acc[0][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A0, B, acc[0][f], 4, 0, 0, sa0, 0, sb);
-        acc[1][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A1, B, acc[1][f], 4, 0, 0, sa1, 0, sb);
-      }
-    }
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // the slice has been read before its slot is refilled
-    asm volatile("" ::: "memory");
-    if (j + kRing < mine) fetch(j + kRing);
-  }
-  v4f* red = reinterpret_cast<v4f*>(area);
-#pragma unroll
-  for (int t = 0; t < 2; ++t)
-#pragma unroll
-    for (int f = 0; f < MF; ++f) red[(t * MF + f) * 64 + 4 * r + g] = acc[t][f];
-  __syncthreads();
-  for (int i = threadIdx.x; i < 2 * MF * 64; i += kThreads) {
-    v4f sum = reinterpret_cast<const v4f*>(lds)[i];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) sum += reinterpret_cast<const v4f*>(lds + w * area_bytes)[i];
-    reinterpret_cast<v4f*>(lds)[i] = sum;  // its own element of wave 0's area
-  }
-  __syncthreads();
-}
-
-// Sum of the three terms of token j (of a pass) and feature i of tile t.
-template <int MF>
-__device__ __forceinline__ float term_sum(const uint8_t* lds, int t, int j, int i) {
-  const float* s = reinterpret_cast<const float*>(lds) + ((t * MF + j / kTokens) * 16 + (j % kTokens) * kTerms) * 16 + i;
-  return (s[0] + s[16]) + s[32];
-}
-
 struct ExpertArgs {
-  const int* ids;
-  int pairs, k, E, D, I;
+  const Slot* slot;
+  const int* list;
+  int k, D, I;
   const uint8_t *wq, *ws;  // the experts' matrices
   const uint8_t *xq, *xs;  // terms and scales of the rows
   float* out;
 };
 
-// UP: h[pair][f0 .. f0 + 15] = silu(gate) * up.  Not UP: out[pair][n0 .. n0 + 31].
+typedef v4u v4u_dword __attribute__((aligned(4)));
+
+// The four E8M0 dwords (one per step of 128) of slice sl of a row of KS scale bytes; past the row's end the
+// last dword again.
+__device__ __forceinline__ v4u slice_scales(const uint8_t* row, int sl, int KS) {
+  if (KS % 16 == 0) return *reinterpret_cast<const v4u_dword*>(row + 16 * sl);
+  v4u s;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) s[u] = *reinterpret_cast<const unsigned*>(row + min(16 * sl + 4 * u, KS - 4));
+  return s;
+}
+
+// One wave: two tiles of 16 rows of an expert's matrix by up to 5 MF tokens, all of K. UP: the gate and up rows of
+// features f0 .. f0 + 15 of h, h[pair] = silu(gate) * up. Not UP: output features 32 tile .. + 31.
+// W streams through the wave's own LDS ring by the LDS DMA, 4 rows x 256 bytes an instruction; the tokens' terms and
+// every scale go to registers, the next slice's requested while this one is multiplied. No barrier: waves
+// share nothing.
 template <bool UP, int MF>
-__device__ __forceinline__ void expert_pass(uint8_t* lds, const ExpertArgs& A, int e, int tile, const int* list, int* rowof,
-                                            int n) {
+__device__ __forceinline__ void expert_tile(uint8_t* lds, const ExpertArgs& A, int expert, int tile, const int* list, int n) {
   const int K = UP ? A.D : A.I;
-  const size_t KB = K / 2, KS = K / 32, base = (size_t)e * (UP ? 2 * A.I : A.D);
-  const size_t r0 = base + (UP ? 16 * tile : 32 * tile), r1 = r0 + (UP ? A.I : 16);
-  for (int j = threadIdx.x; j < n; j += kThreads) rowof[j] = UP ? list[j] / A.k : list[j];
-  __syncthreads();
-  expert_tiles<MF>(lds, A.wq + r0 * KB, A.wq + r1 * KB, A.ws + r0 * KS, A.ws + r1 * KS, K, A.xq, A.xs, rowof, n);
-  if constexpr (UP) {
-    for (int i = threadIdx.x; i < n * 16; i += kThreads) {
-      const int j = i >> 4, c = i & 15;
-      const float gate = term_sum<MF>(lds, 0, j, c), up = term_sum<MF>(lds, 1, j, c);
-      A.out[(size_t)list[j] * A.I + 16 * tile + c] = gate / (1.0f + expf(-gate)) * up;
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const unsigned KB = (unsigned)K / 2, KS = (unsigned)K / 32;
+  const size_t r0 = (size_t)expert * (UP ? 2 * A.I : A.D) + (UP ? 16 : 32) * (size_t)tile, r1 = r0 + (UP ? A.I : 16);
+  const int steps = K / 128, nsl = (steps + 3) / 4;
+  auto fetch = [&](int sl) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(A.wq + (t ? r1 : r0) * KB, 16u * KB);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 4 * i + g;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(lds + ((sl % kRing) * 2 + t) * kSliceBytes + i * 1024), 16,
+                                                 (unsigned)row * KB + (unsigned)sl * kSlice + 16u * (unsigned)(r ^ row), 0, 0,
+                                                 0);
+      }
     }
-  } else {
-    for (int i = threadIdx.x; i < n * 32; i += kThreads) {
-      const int j = i >> 5, c = i & 31;
-      A.out[(size_t)list[j] * A.D + 32 * tile + c] = term_sum<MF>(lds, c >> 4, j, c & 15);
+  };
+  fetch(0);
+  const int term = r % kTerms;  // column 15 repeats a term of the next token and is not read
+  const uint8_t *xp[MF], *xsp[MF];
+#pragma unroll
+  for (int f = 0; f < MF; ++f) {
+    const int pair = list[min(kTokens * f + r / kTerms, n - 1)], row = UP ? pair / A.k : pair;
+    xp[f] = A.xq + ((size_t)row * kTerms + term) * K + 16 * g;
+    xsp[f] = A.xs + (size_t)row * KS;
+  }
+  const uint8_t *ws0 = A.ws + (r0 + r) * KS, *ws1 = A.ws + (r1 + r) * KS;
+  v4u x[MF][4][2], xs[MF], s0, s1;
+  auto load_step = [&](int sl, int u) {
+    const int step = min(4 * sl + u, steps - 1);
+#pragma unroll
+    for (int f = 0; f < MF; ++f) {
+      // E4M3 operand: a lane group's 32 bytes are elements 16 g .. and 64 + 16 g .. of the step's 128
+      // (measured); block b of 32 elements is scaled by the byte of lane group b for either operand
+      x[f][u][0] = *reinterpret_cast<const v4u*>(xp[f] + (size_t)step * 128);
+      x[f][u][1] = *reinterpret_cast<const v4u*>(xp[f] + (size_t)step * 128 + 64);
+    }
+  };
+  auto load_scales = [&](int sl) {
+    s0 = slice_scales(ws0, sl, KS);
+    s1 = slice_scales(ws1, sl, KS);
+#pragma unroll
+    for (int f = 0; f < MF; ++f) xs[f] = slice_scales(xsp[f], sl, KS);
+  };
+#pragma unroll
+  for (int u = 0; u < 4; ++u) load_step(0, u);
+  load_scales(0);
+  if (nsl > 1) fetch(1);
+  v4f acc[2][MF];
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int f = 0; f < MF; ++f) acc[t][f] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int sl = 0; sl < nsl; ++sl) {
+    // the slice has landed, and everything requested after it but the next slice's 8 loads
+    if (sl + 1 < nsl) __builtin_amdgcn_s_waitcnt(0x0F70 | 8);
+    else __builtin_amdgcn_s_waitcnt(0x0F70);
+    asm volatile("" ::: "memory");
+    const uint8_t* wa = lds + (sl % kRing) * 2 * kSliceBytes + r * kSlice;
+    v4u a[4][2];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      a[u][0] = *reinterpret_cast<const v4u*>(wa + 16 * ((4 * u + g) ^ r));
+      a[u][1] = *reinterpret_cast<const v4u*>(wa + kSliceBytes + 16 * ((4 * u + g) ^ r));
+    }
+    const v4u c0 = s0, c1 = s1;
+    v4u cx[MF];
+#pragma unroll
+    for (int f = 0; f < MF; ++f) cx[f] = xs[f];
+    if (sl + 1 < nsl) load_scales(sl + 1);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (4 * sl + u < steps) {  // uniform
+        const v8i A0 = {(int)a[u][0][0], (int)a[u][0][1], (int)a[u][0][2], (int)a[u][0][3], 0, 0, 0, 0};
+        const v8i A1 = {(int)a[u][1][0], (int)a[u][1][1], (int)a[u][1][2], (int)a[u][1][3], 0, 0, 0, 0};
+        const int sa0 = (int)(c0[u] >> (8 * g)), sa1 = (int)(c1[u] >> (8 * g));
+#pragma unroll
+        for (int f = 0; f < MF; ++f) {
+          const v8i B = {(int)x[f][u][0][0], (int)x[f][u][0][1], (int)x[f][u][0][2], (int)x[f][u][0][3],
+                         (int)x[f][u][1][0], (int)x[f][u][1][1], (int)x[f][u][1][2], (int)x[f][u][1][3]};
+          const int sb = (int)((cx[f][u] >> (8 * g)) & 0xFFu) - 4 * term;
+          acc[0][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A0, B, acc[0][f], 4, 0, 0, sa0, 0, sb);
+          acc[1][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A1, B, acc[1][f], 4, 0, 0, sa1, 0, sb);
+        }
+      }
+      if (sl + 1 < nsl) load_step(sl + 1, u);
+    }
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the slice has been read before its slot is refilled
+    asm volatile("" ::: "memory");
+    if (sl + kRing < nsl) fetch(sl + kRing);
+  }
+  // The three terms of token j are columns 3 j .. 3 j + 2 of a DPP row; lane (3 j, g) ends with features 4 g .. + 3.
+#pragma unroll
+  for (int f = 0; f < MF; ++f) {
+    v4f y[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float v = acc[t][f][i];
+        const int b = __float_as_int(v);
+        y[t][i] = (v + __int_as_float(__builtin_amdgcn_update_dpp(0, b, 0x101, 0xF, 0xF, false))) +  // row_shl:1
+                  __int_as_float(__builtin_amdgcn_update_dpp(0, b, 0x102, 0xF, 0xF, false));         // row_shl:2
+      }
+    const int j = kTokens * f + r / kTerms;
+    if (term != 0 || r == 15 || j >= n) continue;
+    const size_t pair = list[j];
+    if constexpr (UP) {
+      v4f h;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i] = y[0][i] / (1.0f + expf(-y[0][i])) * y[1][i];
+      *reinterpret_cast<v4f*>(A.out + pair * A.I + 16 * tile + 4 * g) = h;
+    } else {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) *reinterpret_cast<v4f*>(A.out + pair * A.D + 32 * tile + 16 * t + 4 * g) = y[t];
     }
   }
-  __syncthreads();  // the sums and rowof are read before the next pass
 }
 
 template <bool UP>
-__global__ __launch_bounds__(kThreads) void expert_gemm(ExpertArgs A, int tiles) {
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  __shared__ int used[kMaxExperts / 32], list[kMaxPairs], rowof[kTokens * kMaxFrags], found[2];
-  const int a = blockIdx.x / tiles, tile = blockIdx.x % tiles;
-  int e;
-  const int n = find_expert(A.ids, A.pairs, A.E, a, used, list, found, e);
-  if (n == 0) return;
-  for (int j = 0; j < n; j += kTokens * kMaxFrags) {
-    const int m = min(n - j, kTokens * kMaxFrags);
-    if (m <= kTokens) expert_pass<UP, 1>(lds, A, e, tile, list + j, rowof, m);
-    else if (m <= 2 * kTokens) expert_pass<UP, 2>(lds, A, e, tile, list + j, rowof, m);
-    else expert_pass<UP, kMaxFrags>(lds, A, e, tile, list + j, rowof, m);
+__global__ __launch_bounds__(64) void expert_gemm(ExpertArgs A, int tiles) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kExpertLds];
+  const Slot s = A.slot[blockIdx.x / tiles];
+  const int tile = blockIdx.x % tiles;
+  for (int j = 0; j < s.n; j += kTokens * kMaxFrags) {
+    const int m = min(s.n - j, kTokens * kMaxFrags);
+    if (m <= kTokens) expert_tile<UP, 1>(lds, A, s.expert, tile, A.list + s.first + j, m);
+    else expert_tile<UP, 2>(lds, A, s.expert, tile, A.list + s.first + j, m);
   }
 }
 
@@ -432,36 +460,18 @@ __global__ __launch_bounds__(256) void combine(const int* __restrict__ ids, cons
   *reinterpret_cast<v2u*>(Y + (size_t)t * D + d) = v2u{b[0] | b[1] << 16, b[2] | b[3] << 16};
 }
 
-template <bool F32>
-hipError_t launch_split(int block, const void* V, int64_t ld, int rows, int K, uint8_t* q, uint8_t* s, hipStream_t st) {
+template <bool PLAN>
+hipError_t launch_split(int block, const void* V, int64_t ld, int rows, int K, uint8_t* q, uint8_t* s, const PlanArgs& P,
+                        hipStream_t st) {
   const int cpr = K / 32;
-  const dim3 grid((unsigned)(((int64_t)rows * cpr + 255) / 256));
+  const dim3 grid((unsigned)(((int64_t)rows * cpr + 255) / 256 + (PLAN ? 1 : 0)));
   switch (block) {
-    case 16: hipLaunchKernelGGL((split_rows<16, F32>), grid, dim3(256), 0, st, V, ld, rows, cpr, q, s); break;
-    case 32: hipLaunchKernelGGL((split_rows<32, F32>), grid, dim3(256), 0, st, V, ld, rows, cpr, q, s); break;
-    case 64: hipLaunchKernelGGL((split_rows<64, F32>), grid, dim3(256), 0, st, V, ld, rows, cpr, q, s); break;
-    default: hipLaunchKernelGGL((split_rows<128, F32>), grid, dim3(256), 0, st, V, ld, rows, cpr, q, s);
+    case 16: hipLaunchKernelGGL((split_rows<16, PLAN>), grid, dim3(256), 0, st, V, ld, rows, cpr, q, s, P); break;
+    case 32: hipLaunchKernelGGL((split_rows<32, PLAN>), grid, dim3(256), 0, st, V, ld, rows, cpr, q, s, P); break;
+    case 64: hipLaunchKernelGGL((split_rows<64, PLAN>), grid, dim3(256), 0, st, V, ld, rows, cpr, q, s, P); break;
+    default: hipLaunchKernelGGL((split_rows<128, PLAN>), grid, dim3(256), 0, st, V, ld, rows, cpr, q, s, P);
   }
   return hipGetLastError();
-}
-
-constexpr int kExpertLds = kWaves * kRing * 2 * kSliceBytes;
-static_assert(2 * kMaxFrags * 1024 <= kRing * 2 * kSliceBytes, "the partial sums fit a wave's ring");
-
-// The dynamic LDS limit of both expert kernels, raised once per device.
-hipError_t raise_lds_limits() {
-  static std::atomic<int> ready[64];
-  int dev = 0;
-  hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess) return e;
-  const bool cached = dev >= 0 && dev < 64;
-  if (cached && ready[dev].load(std::memory_order_acquire)) return hipSuccess;
-  for (const void* k : {(const void*)expert_gemm<true>, (const void*)expert_gemm<false>}) {
-    e = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, kExpertLds);
-    if (e != hipSuccess) return e;
-  }
-  if (cached) ready[dev].store(1, std::memory_order_release);
-  return hipSuccess;
 }
 
 }  // namespace
@@ -491,19 +501,18 @@ hipError_t fp4_launch_moe_experts(const uint16_t* X, int64_t T, int64_t D, int64
   uint8_t* hq = ws + FP4_MOE_WS_HQ(T, k, D, I);
   uint8_t* hs = ws + FP4_MOE_WS_HS(T, k, D, I);
   float* out = reinterpret_cast<float*>(ws + FP4_MOE_WS_OUT(T, k, D, I));
-  hipError_t e = raise_lds_limits();
+  Slot* slot = reinterpret_cast<Slot*>(ws + FP4_MOE_WS_PLAN(T, k, D, I));
+  int* list = reinterpret_cast<int*>(slot + pairs);
+  const PlanArgs plan{ids, pairs, (int)E, slots, slot, list};
+  hipError_t e = launch_split<true>(block, X, ldx, (int)T, (int)D, xq, xs, plan, st);
   if (e != hipSuccess) return e;
-  e = launch_split<false>(block, X, ldx, (int)T, (int)D, xq, xs, st);
-  if (e != hipSuccess) return e;
-  ExpertArgs up{ids, pairs, k, (int)E, (int)D, (int)I, W13q, W13s, xq, xs, h};
-  hipLaunchKernelGGL(expert_gemm<true>, dim3((unsigned)(slots * (I / 16))), dim3(kThreads), kExpertLds, st, up,
-                     (int)(I / 16));
+  const ExpertArgs up{slot, list, k, (int)D, (int)I, W13q, W13s, xq, xs, h};
+  hipLaunchKernelGGL(expert_gemm<true>, dim3((unsigned)(slots * (I / 16))), dim3(64), 0, st, up, (int)(I / 16));
   e = hipGetLastError();
-  if (e == hipSuccess) e = launch_split<true>(block, h, I, pairs, (int)I, hq, hs, st);
+  if (e == hipSuccess) e = launch_split<false>(block, h, I, pairs, (int)I, hq, hs, plan, st);
   if (e != hipSuccess) return e;
-  ExpertArgs down{ids, pairs, k, (int)E, (int)D, (int)I, W2q, W2s, hq, hs, out};
-  hipLaunchKernelGGL(expert_gemm<false>, dim3((unsigned)(slots * (D / 32))), dim3(kThreads), kExpertLds, st, down,
-                     (int)(D / 32));
+  const ExpertArgs down{slot, list, k, (int)D, (int)I, W2q, W2s, hq, hs, out};
+  hipLaunchKernelGGL(expert_gemm<false>, dim3((unsigned)(slots * (D / 32))), dim3(64), 0, st, down, (int)(D / 32));
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(combine, dim3((unsigned)((T * (D / 4) + 255) / 256)), dim3(256), 0, st, ids, weights, out, (int)T, k,
