@@ -14,9 +14,9 @@
 //
 // Steps of a call (each a launch; every sum in a fixed order):
 //   split x    rotate (float32), split into terms   [T, 3, D]; one more workgroup sorts the pairs by expert
-//   up         per used expert and 16 features of h: gate and up rows, silu(g) * u in float32   [T k, I]
+//   up         per used expert and 32 features of h: gate and up rows, silu(g) * u in float32   [T k, I]
 //   split h    rotate, split                        [T k, 3, I]
-//   down       per used expert and 32 output features                                           [T k, D] float32
+//   down       per used expert and 64 output features                                           [T k, D] float32
 //   combine    y_t = sum_j p_tj * down, over the slots in order, rounded once to bf16
 #include "fp8_device.hpp"
 #include "quant_device.hpp"
@@ -134,10 +134,13 @@ __global__ __launch_bounds__(256) void route_topk(const float* __restrict__ logi
 constexpr int kTerms = 3;
 constexpr int kTokens = 5;           // tokens per fragment of 16 columns
 constexpr int kMaxFrags = 2;         // fragments per pass over an expert's weights
-constexpr int kSlice = 256;          // bytes (512 elements) of a row per slice
-constexpr int kSliceBytes = 16 * kSlice;
-constexpr int kRing = 2;             // slices of two tiles a wave holds or has in flight
-constexpr int kExpertLds = kRing * 2 * kSliceBytes;  // 16 KB: ten waves on a CU
+constexpr int kTiles = 4;            // tiles of 16 rows per wave
+constexpr int kHalf = 128;           // bytes (256 elements) of a row per half slice
+constexpr int kHalfBytes = kTiles * 16 * kHalf;
+constexpr int kRing = 2;             // half slices a wave holds or has in flight
+constexpr int kScaleRow = 128;       // scale bytes of a row in LDS at once: 4096 elements
+constexpr int kScaleBytes = kTiles * 16 * kScaleRow;
+constexpr int kExpertLds = kRing * kHalfBytes + kScaleBytes;  // 24 KB: six waves on a CU
 
 // The pairs (t k + slot) of one used expert: list[first .. first + n - 1]; n = 0 past the last used expert.
 struct Slot {
@@ -299,32 +302,83 @@ __device__ __forceinline__ v4u slice_scales(const uint8_t* row, int sl, int KS) 
   return s;
 }
 
-// One wave: two tiles of 16 rows of an expert's matrix by up to 5 MF tokens, all of K. UP: the gate and up rows of
-// features f0 .. f0 + 15 of h, h[pair] = silu(gate) * up. Not UP: output features 32 tile .. + 31.
-// W streams through the wave's own LDS ring by the LDS DMA, 4 rows x 256 bytes an instruction; the tokens' terms and
-// every scale go to registers, the next slice's requested while this one is multiplied. No barrier: waves
-// share nothing.
+// W's scale bytes of a wave's 64 rows in LDS, up to 128 of a row at a time, so that each line of them is read
+// from memory once: read 16 bytes a slice, a third of them came from HBM again, W having pushed them out of the L2
+// between slices. Rows of up to 128 bytes lie back to back in memory (32 or 64 of them) and are copied whole; of
+// longer rows one 128-byte window is held, the last one ending with the row. Where a row is whole 16-byte
+// chunks, chunk q of row r sits at slot (q + r) % chunks: rows 0 .. 7 read the same byte of different banks.
+struct ScaleWindow {
+  int KS, chunks;  // chunks 0: rows as they lie in memory
+  __device__ __forceinline__ explicit ScaleWindow(int ks) : KS(ks), chunks(ks > kScaleRow ? 8 : ks % 16 ? 0 : ks / 16) {}
+  __device__ __forceinline__ int start(int step) const { return KS > kScaleRow ? min(step / 32 * kScaleRow, KS - kScaleRow) : 0; }
+
+  // Request the window that holds `step`: rows base .. + 31 and base + skip .. + 31.
+  __device__ __forceinline__ void fetch(uint8_t* lds, const uint8_t* mat, unsigned rows, unsigned skip, int step) const {
+    const int lane = threadIdx.x & 63;
+    const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(mat, rows * (unsigned)KS);
+    auto row_at = [&](unsigned r) { return (r < 32 ? r : r - 32 + skip) * (unsigned)KS; };
+    const int units = KS > kScaleRow ? kTiles * 16 * 8 : 4 * KS;  // of 16 bytes
+    for (int u0 = 0; u0 < units; u0 += 64) {
+      const unsigned u = u0 + lane;
+      unsigned off;
+      if (chunks == 0) {
+        off = 16 * u + (u >= 2u * KS ? (skip - 32) * (unsigned)KS : 0u);
+      } else {
+        const unsigned r = u / chunks, slot = u - r * chunks, q = (slot + chunks * 64u - r) % chunks;
+        off = row_at(r) + (unsigned)start(step) + 16 * q;
+      }
+      if (u >= (unsigned)units) off = 0xFFFFFFF0u;  // reads as zero
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + u0 * 16), 16, off, 0, 0, 0);
+    }
+  }
+
+  // Byte of row r, step and lane group g.
+  __device__ __forceinline__ unsigned get(const uint8_t* lds, int r, int step, int g) const {
+    const int at = 4 * step - start(step) + g;
+    return chunks == 0 ? lds[r * KS + at] : lds[(r * chunks + ((at >> 4) + r) % chunks) * 16 + (at & 15)];
+  }
+};
+
+// 16-byte chunk q of row r of a tile's half slice sits at slot q ^ swz(r): the 16 rows of a fragment read take
+// every slot twice, once on even and once on odd rows.
+__device__ __forceinline__ int swz(int r) { return (r ^ ((r >> 3) & 1)) & 7; }
+
+// One wave: four tiles of 16 rows of an expert's matrix by up to 5 MF tokens, all of K. UP: the gate and up rows of
+// features 32 tile .. + 31 of h (two tiles each), h[pair] = silu(gate) * up. Not UP: output features 64 tile .. + 63.
+// W streams through the wave's own LDS ring by the LDS DMA in half slices of 256 elements, 8 rows x 128 bytes an
+// instruction; the tokens' terms and every scale go to registers, the next ones requested while these are
+// multiplied. Four tiles share what is read of the tokens (with two, reading it from L2 took a third more time).
+// No barrier: waves share nothing.
 template <bool UP, int MF>
 __device__ __forceinline__ void expert_tile(uint8_t* lds, const ExpertArgs& A, int expert, int tile, const int* list, int n) {
   const int K = UP ? A.D : A.I;
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const unsigned KB = (unsigned)K / 2, KS = (unsigned)K / 32;
-  const size_t r0 = (size_t)expert * (UP ? 2 * A.I : A.D) + (UP ? 16 : 32) * (size_t)tile, r1 = r0 + (UP ? A.I : 16);
-  const int steps = K / 128, nsl = (steps + 3) / 4;
-  auto fetch = [&](int sl) {
+  const int steps = K / 128, nsl = (steps + 3) / 4, nhalf = (steps + 1) / 2;
+  const size_t base = (size_t)expert * (UP ? 2 * A.I : A.D) + (UP ? 32 : 64) * (size_t)tile;
+  auto row0 = [&](int t) { return base + (UP ? (t >> 1) * A.I + 16 * (t & 1) : 16 * t); };
+  auto fetch = [&](int i) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(A.wq + (t ? r1 : r0) * KB, 16u * KB);
+    for (int t = 0; t < kTiles; ++t) {
+      const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(A.wq + row0(t) * KB, 16u * KB);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = 4 * i + g;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(lds + ((sl % kRing) * 2 + t) * kSliceBytes + i * 1024), 16,
-                                                 (unsigned)row * KB + (unsigned)sl * kSlice + 16u * (unsigned)(r ^ row), 0, 0,
-                                                 0);
+      for (int q = 0; q < 2; ++q) {
+        const int row = 8 * q + (lane >> 3);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(lds + (i % kRing) * kHalfBytes + t * 2048 + q * 1024), 16,
+                                                 (unsigned)row * KB + (unsigned)i * kHalf +
+                                                     16u * (unsigned)((lane & 7) ^ swz(row)),
+                                                 0, 0, 0);
       }
     }
   };
+  constexpr int kFetch = 2 * kTiles;  // loads of a fetch
+  const ScaleWindow win((int)KS);
+  uint8_t* wscl = lds + kRing * kHalfBytes;
+  auto fetch_scales = [&](int step) {
+    win.fetch(wscl, A.ws + base * KS, UP ? A.I + 32u : 64u, UP ? (unsigned)A.I : 32u, step);
+  };
   fetch(0);
+  fetch_scales(0);
   const int term = r % kTerms;  // column 15 repeats a term of the next token and is not read
   const uint8_t *xp[MF], *xsp[MF];
 #pragma unroll
@@ -333,10 +387,9 @@ __device__ __forceinline__ void expert_tile(uint8_t* lds, const ExpertArgs& A, i
     xp[f] = A.xq + ((size_t)row * kTerms + term) * K + 16 * g;
     xsp[f] = A.xs + (size_t)row * KS;
   }
-  const uint8_t *ws0 = A.ws + (r0 + r) * KS, *ws1 = A.ws + (r1 + r) * KS;
-  v4u x[MF][4][2], xs[MF], s0, s1;
-  auto load_step = [&](int sl, int u) {
-    const int step = min(4 * sl + u, steps - 1);
+  v4u x[MF][2][2], xs[MF];
+  auto load_step = [&](int step, int u) {
+    step = min(step, steps - 1);
 #pragma unroll
     for (int f = 0; f < MF; ++f) {
       // E4M3 operand: a lane group's 32 bytes are elements 16 g .. and 64 + 16 g .. of the step's 128
@@ -346,64 +399,78 @@ __device__ __forceinline__ void expert_tile(uint8_t* lds, const ExpertArgs& A, i
     }
   };
   auto load_scales = [&](int sl) {
-    s0 = slice_scales(ws0, sl, KS);
-    s1 = slice_scales(ws1, sl, KS);
 #pragma unroll
     for (int f = 0; f < MF; ++f) xs[f] = slice_scales(xsp[f], sl, KS);
   };
-#pragma unroll
-  for (int u = 0; u < 4; ++u) load_step(0, u);
   load_scales(0);
-  if (nsl > 1) fetch(1);
-  v4f acc[2][MF];
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
+  for (int u = 0; u < 2; ++u) load_step(u, u);
+  if (nhalf > 1) fetch(1);
+  v4f acc[kTiles][MF];
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t)
 #pragma unroll
     for (int f = 0; f < MF; ++f) acc[t][f] = v4f{0.f, 0.f, 0.f, 0.f};
   for (int sl = 0; sl < nsl; ++sl) {
-    // the slice has landed, and everything requested after it but the next slice's 8 loads
-    if (sl + 1 < nsl) __builtin_amdgcn_s_waitcnt(0x0F70 | 8);
-    else __builtin_amdgcn_s_waitcnt(0x0F70);
-    asm volatile("" ::: "memory");
-    const uint8_t* wa = lds + (sl % kRing) * 2 * kSliceBytes + r * kSlice;
-    v4u a[4][2];
+    unsigned wb[kTiles][4], xb[MF][4];  // this slice's scale bytes of the lane's group, one per step
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      a[u][0] = *reinterpret_cast<const v4u*>(wa + 16 * ((4 * u + g) ^ r));
-      a[u][1] = *reinterpret_cast<const v4u*>(wa + kSliceBytes + 16 * ((4 * u + g) ^ r));
-    }
-    const v4u c0 = s0, c1 = s1;
-    v4u cx[MF];
+    for (int h = 0; h < 2; ++h) {
+      const int i = 2 * sl + h;
+      if (i >= nhalf) break;  // uniform
+      // the half slice has landed, and everything requested after it but the next one's loads
+      if (i + 1 < nhalf) __builtin_amdgcn_s_waitcnt(0x0F70 | kFetch);
+      else __builtin_amdgcn_s_waitcnt(0x0F70);
+      asm volatile("" ::: "memory");
+      if (h == 0) {
 #pragma unroll
-    for (int f = 0; f < MF; ++f) cx[f] = xs[f];
-    if (sl + 1 < nsl) load_scales(sl + 1);
+        for (int u = 0; u < 4; ++u) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (4 * sl + u < steps) {  // uniform
-        const v8i A0 = {(int)a[u][0][0], (int)a[u][0][1], (int)a[u][0][2], (int)a[u][0][3], 0, 0, 0, 0};
-        const v8i A1 = {(int)a[u][1][0], (int)a[u][1][1], (int)a[u][1][2], (int)a[u][1][3], 0, 0, 0, 0};
-        const int sa0 = (int)(c0[u] >> (8 * g)), sa1 = (int)(c1[u] >> (8 * g));
+          for (int t = 0; t < kTiles; ++t) wb[t][u] = win.get(wscl, 16 * t + r, min(4 * sl + u, steps - 1), g);
 #pragma unroll
-        for (int f = 0; f < MF; ++f) {
-          const v8i B = {(int)x[f][u][0][0], (int)x[f][u][0][1], (int)x[f][u][0][2], (int)x[f][u][0][3],
-                         (int)x[f][u][1][0], (int)x[f][u][1][1], (int)x[f][u][1][2], (int)x[f][u][1][3]};
-          const int sb = (int)((cx[f][u] >> (8 * g)) & 0xFFu) - 4 * term;
-          acc[0][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A0, B, acc[0][f], 4, 0, 0, sa0, 0, sb);
-          acc[1][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A1, B, acc[1][f], 4, 0, 0, sa1, 0, sb);
+          for (int f = 0; f < MF; ++f) xb[f][u] = ((xs[f][u] >> (8 * g)) & 0xFFu) - 4u * (unsigned)term;
         }
       }
-      if (sl + 1 < nsl) load_step(sl + 1, u);
+      const uint8_t* wa = lds + (i % kRing) * kHalfBytes + r * kHalf;
+      v4u a[2][kTiles];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+          a[u][t] = *reinterpret_cast<const v4u*>(wa + t * 2048 + 16 * ((4 * u + g) ^ swz(r)));
+      if (h == 0 && sl % 8 == 7 && sl + 1 < nsl) {  // the last slice of a window: its bytes are in registers
+        __builtin_amdgcn_s_waitcnt(0xC07F);
+        asm volatile("" ::: "memory");
+        fetch_scales(4 * sl + 4);
+      }
+      if (h == 1 && sl + 1 < nsl) load_scales(sl + 1);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (2 * i + u < steps) {  // uniform
+#pragma unroll
+          for (int f = 0; f < MF; ++f) {
+            const v8i B = {(int)x[f][u][0][0], (int)x[f][u][0][1], (int)x[f][u][0][2], (int)x[f][u][0][3],
+                           (int)x[f][u][1][0], (int)x[f][u][1][1], (int)x[f][u][1][2], (int)x[f][u][1][3]};
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+              const v8i W = {(int)a[u][t][0], (int)a[u][t][1], (int)a[u][t][2], (int)a[u][t][3], 0, 0, 0, 0};
+              acc[t][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(W, B, acc[t][f], 4, 0, 0, (int)wb[t][2 * h + u], 0,
+                                                                           (int)xb[f][2 * h + u]);
+            }
+          }
+        }
+        if (i + 1 < nhalf) load_step(2 * i + 2 + u, u);
+      }
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the half slice has been read before its slot is refilled
+      asm volatile("" ::: "memory");
+      if (i + kRing < nhalf) fetch(i + kRing);
     }
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the slice has been read before its slot is refilled
-    asm volatile("" ::: "memory");
-    if (sl + kRing < nsl) fetch(sl + kRing);
   }
   // The three terms of token j are columns 3 j .. 3 j + 2 of a DPP row; lane (3 j, g) ends with features 4 g .. + 3.
 #pragma unroll
   for (int f = 0; f < MF; ++f) {
-    v4f y[2];
+    v4f y[kTiles];
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < kTiles; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float v = acc[t][f][i];
@@ -415,13 +482,16 @@ __device__ __forceinline__ void expert_tile(uint8_t* lds, const ExpertArgs& A, i
     if (term != 0 || r == 15 || j >= n) continue;
     const size_t pair = list[j];
     if constexpr (UP) {
-      v4f h;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) h[i] = y[0][i] / (1.0f + expf(-y[0][i])) * y[1][i];
-      *reinterpret_cast<v4f*>(A.out + pair * A.I + 16 * tile + 4 * g) = h;
+      for (int t = 0; t < 2; ++t) {
+        v4f h;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = y[t][i] / (1.0f + expf(-y[t][i])) * y[t + 2][i];
+        *reinterpret_cast<v4f*>(A.out + pair * A.I + 32 * tile + 16 * t + 4 * g) = h;
+      }
     } else {
 #pragma unroll
-      for (int t = 0; t < 2; ++t) *reinterpret_cast<v4f*>(A.out + pair * A.D + 32 * tile + 16 * t + 4 * g) = y[t];
+      for (int t = 0; t < kTiles; ++t) *reinterpret_cast<v4f*>(A.out + pair * A.D + 64 * tile + 16 * t + 4 * g) = y[t];
     }
   }
 }
@@ -507,12 +577,12 @@ hipError_t fp4_launch_moe_experts(const uint16_t* X, int64_t T, int64_t D, int64
   hipError_t e = launch_split<true>(block, X, ldx, (int)T, (int)D, xq, xs, plan, st);
   if (e != hipSuccess) return e;
   const ExpertArgs up{slot, list, k, (int)D, (int)I, W13q, W13s, xq, xs, h};
-  hipLaunchKernelGGL(expert_gemm<true>, dim3((unsigned)(slots * (I / 16))), dim3(64), 0, st, up, (int)(I / 16));
+  hipLaunchKernelGGL(expert_gemm<true>, dim3((unsigned)(slots * (I / 32))), dim3(64), 0, st, up, (int)(I / 32));
   e = hipGetLastError();
   if (e == hipSuccess) e = launch_split<false>(block, h, I, pairs, (int)I, hq, hs, plan, st);
   if (e != hipSuccess) return e;
   const ExpertArgs down{slot, list, k, (int)D, (int)I, W2q, W2s, hq, hs, out};
-  hipLaunchKernelGGL(expert_gemm<false>, dim3((unsigned)(slots * (D / 32))), dim3(64), 0, st, down, (int)(D / 32));
+  hipLaunchKernelGGL(expert_gemm<false>, dim3((unsigned)(slots * (D / 64))), dim3(64), 0, st, down, (int)(D / 64));
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(combine, dim3((unsigned)((T * (D / 4) + 255) / 256)), dim3(256), 0, st, ids, weights, out, (int)T, k,

@@ -122,7 +122,8 @@ def check_experts(*a, **kw):
 EXPERTS = [(1, 1, 128, 128, 1, 32), (1, 8, 256, 128, 2, 16), (1, 16, 2048, 768, 8, 32), (2, 4, 128, 384, 4, 128),
            (3, 6, 640, 256, 3, 64), (4, 4, 1152, 128, 2, 32), (7, 3, 512, 640, 3, 128), (16, 8, 384, 256, 2, 16),
            (33, 4, 256, 128, 2, 32), (64, 16, 256, 256, 4, 64), (128, 2, 128, 128, 1, 32), (128, 3, 256, 128, 2, 128),
-           (5, 40, 4096, 128, 2, 32), (2, 3, 128, 2048, 2, 64)]
+           (5, 40, 4096, 128, 2, 32), (2, 3, 128, 2048, 2, 64), (3, 2, 4224, 128, 1, 32), (2, 3, 7168, 256, 2, 128),
+          (2, 2, 128, 4352, 1, 64), (6, 3, 8320, 128, 2, 16), (12, 2, 1408, 1408, 1, 128)]
 
 
 @pytest.mark.parametrize("T,E,D,I,k,block", EXPERTS)
