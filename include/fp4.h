@@ -352,6 +352,7 @@ FP4_API int fp8_linear(const uint8_t *Xq, const float *Xs, const uint8_t *Wq, co
  */
 #define FP4_MOE_MAX_TOKENS 128
 #define FP4_MOE_MAX_TOPK 16
+#define FP4_MOE_WS_PLAN_PAIR 68
 #define FP4_MOE_PAD_(n) (((size_t)(n) + 255) / 256 * 256)
 #define FP4_MOE_ROUTE_WORKSPACE_BYTES(T, E) ((size_t)(T) * (E) * 4)
 /* the experts' workspace: terms and scales of X, h, its terms and scales, the slots'
@@ -362,7 +363,7 @@ FP4_API int fp8_linear(const uint8_t *Xq, const float *Xs, const uint8_t *Wq, co
 #define FP4_MOE_WS_HS(T, k, D, I) (FP4_MOE_WS_HQ(T, k, D, I) + FP4_MOE_PAD_((size_t)(T) * (k) * 3 * (I)))
 #define FP4_MOE_WS_OUT(T, k, D, I) (FP4_MOE_WS_HS(T, k, D, I) + FP4_MOE_PAD_((size_t)(T) * (k) * (I) / 32))
 #define FP4_MOE_WS_PLAN(T, k, D, I) (FP4_MOE_WS_OUT(T, k, D, I) + FP4_MOE_PAD_((size_t)(T) * (k) * (D) * 4))
-#define FP4_MOE_WORKSPACE_BYTES(T, k, D, I) (FP4_MOE_WS_PLAN(T, k, D, I) + (size_t)(T) * (k) * 20)
+#define FP4_MOE_WORKSPACE_BYTES(T, k, D, I) (FP4_MOE_WS_PLAN(T, k, D, I) + (size_t)(T) * (k) * FP4_MOE_WS_PLAN_PAIR)
 FP4_API int fp4_moe_route(const void *X, int64_t T, int64_t D, int64_t ldx, const void *Wr, int64_t E, int k,
                           int renormalize, int *ids, float *weights, void *workspace, size_t workspace_bytes,
                           void *stream);

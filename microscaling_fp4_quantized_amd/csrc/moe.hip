@@ -15,9 +15,11 @@
 // Steps of a call (each a launch; every sum in a fixed order):
 //   split x    rotate (float32), split into terms   [T, 3, D]; one more workgroup sorts the pairs by expert
 //   up         per used expert and 32 features of h: gate and up rows, silu(g) * u in float32   [T k, I]
-//   split h    rotate, split                        [T k, 3, I]
-//   down       per used expert and 64 output features                                           [T k, D] float32
+//   split h    rotate, split                                                                    [T k, 3, I]
+//   down       per used expert and 64 output features, float32                                  [T k, D]
 //   combine    y_t = sum_j p_tj * down, over the slots in order, rounded once to bf16
+#include <atomic>
+
 #include "fp8_device.hpp"
 #include "quant_device.hpp"
 #include "../../include/fp4.h"
@@ -140,15 +142,23 @@ constexpr int kHalfBytes = kTiles * 16 * kHalf;
 constexpr int kRing = 2;             // half slices a wave holds or has in flight
 constexpr int kScaleRow = 128;       // scale bytes of a row in LDS at once: 4096 elements
 constexpr int kScaleBytes = kTiles * 16 * kScaleRow;
-constexpr int kExpertLds = kRing * kHalfBytes + kScaleBytes;  // 24 KB: six waves on a CU
 
-// The pairs (t k + slot) of one used expert: list[first .. first + n - 1]; n = 0 past the last used expert.
+// The pairs (t k + slot) of one used expert: list[first .. first + n - 1], and the first of them here, so that a
+// workgroup has them with its first load; n = 0 past the last used expert.
+constexpr int kSlotPairs = 12;
 struct Slot {
-  int expert, first, n, pad;
+  int expert, n, first, pad, pairs[kSlotPairs];
 };
+static_assert(sizeof(Slot) + 4 == FP4_MOE_WS_PLAN_PAIR, "the plan's bytes per pair");
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_rsrc(const void* base, unsigned bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
+}
+
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 0xF) | (0x7 << 4) | (0xF << 8) | (((N >> 4) & 3) << 14));
 }
 
 // Rotate 32 values (a chunk of the Hadamard block, see fwht) and write their terms and the group's E8M0
@@ -197,7 +207,7 @@ __device__ __forceinline__ void split_chunk(float v[32], uint8_t* q, int64_t ter
 // of a result.
 __device__ __forceinline__ void plan_experts(const int* __restrict__ ids, int pairs, int E, int slots, Slot* slot,
                                              int* list) {
-  __shared__ int count[kMaxExperts], first[kMaxExperts], total[2][4];
+  __shared__ int count[kMaxExperts], first[kMaxExperts], start[kMaxExperts], rank_of[kMaxExperts], total[2][4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   for (int e = tid; e < kMaxExperts; e += 256) count[e] = 0;
   __syncthreads();
@@ -232,14 +242,23 @@ __device__ __forceinline__ void plan_experts(const int* __restrict__ ids, int pa
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     first[4 * tid + i] = at;
-    if (n[i] > 0) slot[rank++] = Slot{4 * tid + i, at, n[i], 0};
+    if (n[i] > 0) {
+      slot[rank].expert = 4 * tid + i;
+      slot[rank].n = n[i];
+      slot[rank].first = at;
+      rank_of[4 * tid + i] = rank++;
+      start[4 * tid + i] = at;
+    }
     at += n[i];
   }
-  for (int i = used + tid; i < slots; i += 256) slot[i] = Slot{0, 0, 0, 0};
+  for (int i = used + tid; i < slots; i += 256) slot[i].n = 0;
   __syncthreads();
   for (int p = tid; p < pairs; p += 256) {
     const int e = ids[p];
-    if (e >= 0 && e < E) list[atomicAdd(&first[e], 1)] = p;
+    if (e < 0 || e >= E) continue;
+    const int j = atomicAdd(&first[e], 1);
+    list[j] = p;
+    if (j - start[e] < kSlotPairs) slot[rank_of[e]].pairs[j - start[e]] = p;
   }
 }
 
@@ -290,52 +309,43 @@ struct ExpertArgs {
   float* out;
 };
 
-typedef v4u v4u_dword __attribute__((aligned(4)));
-
-// The four E8M0 dwords (one per step of 128) of slice sl of a row of KS scale bytes; past the row's end the
-// last dword again.
-__device__ __forceinline__ v4u slice_scales(const uint8_t* row, int sl, int KS) {
-  if (KS % 16 == 0) return *reinterpret_cast<const v4u_dword*>(row + 16 * sl);
-  v4u s;
-#pragma unroll
-  for (int u = 0; u < 4; ++u) s[u] = *reinterpret_cast<const unsigned*>(row + min(16 * sl + 4 * u, KS - 4));
-  return s;
-}
-
-// W's scale bytes of a wave's 64 rows in LDS, up to 128 of a row at a time, so that each line of them is read
-// from memory once: read 16 bytes a slice, a third of them came from HBM again, W having pushed them out of the L2
-// between slices. Rows of up to 128 bytes lie back to back in memory (32 or 64 of them) and are copied whole; of
-// longer rows one 128-byte window is held, the last one ending with the row. Where a row is whole 16-byte
-// chunks, chunk q of row r sits at slot (q + r) % chunks: rows 0 .. 7 read the same byte of different banks.
+// W's scale bytes of a workgroup's 64 rows in LDS, up to 128 of a row at a time, so that each line of them is read
+// from memory once (read 16 bytes a slice, a third of them came from HBM again, W having pushed them out of the L2
+// between slices). Rows of up to 128 bytes lie back to back in memory (32 or 64 of them) and are copied whole; of
+// longer rows one window of 128 bytes (4096 elements) is held, the last one ending with the row. Where a row is
+// whole 16-byte chunks, chunk q of row r sits at slot (q + r) % chunks: rows 0 .. 7 read the same byte of
+// different banks.
 struct ScaleWindow {
   int KS, chunks;  // chunks 0: rows as they lie in memory
   __device__ __forceinline__ explicit ScaleWindow(int ks) : KS(ks), chunks(ks > kScaleRow ? 8 : ks % 16 ? 0 : ks / 16) {}
-  __device__ __forceinline__ int start(int step) const { return KS > kScaleRow ? min(step / 32 * kScaleRow, KS - kScaleRow) : 0; }
+  // First byte of a row in window c.
+  __device__ __forceinline__ int start(int c) const { return KS > kScaleRow ? min(c * kScaleRow, KS - kScaleRow) : 0; }
 
-  // Request the window that holds `step`: rows base .. + 31 and base + skip .. + 31.
-  __device__ __forceinline__ void fetch(uint8_t* lds, const uint8_t* mat, unsigned rows, unsigned skip, int step) const {
+  // Request window c: rows 0 .. 31 and skip .. skip + 31 of the `rows` rows at mat; wave w of S takes its part.
+  __device__ __forceinline__ void fetch(uint8_t* lds, const uint8_t* mat, unsigned rows, unsigned skip, int c, int w,
+                                        int S) const {
     const int lane = threadIdx.x & 63;
     const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(mat, rows * (unsigned)KS);
-    auto row_at = [&](unsigned r) { return (r < 32 ? r : r - 32 + skip) * (unsigned)KS; };
     const int units = KS > kScaleRow ? kTiles * 16 * 8 : 4 * KS;  // of 16 bytes
-    for (int u0 = 0; u0 < units; u0 += 64) {
+    for (int u0 = 64 * w; u0 < units; u0 += 64 * S) {
       const unsigned u = u0 + lane;
       unsigned off;
       if (chunks == 0) {
         off = 16 * u + (u >= 2u * KS ? (skip - 32) * (unsigned)KS : 0u);
       } else {
         const unsigned r = u / chunks, slot = u - r * chunks, q = (slot + chunks * 64u - r) % chunks;
-        off = row_at(r) + (unsigned)start(step) + 16 * q;
+        off = (r < 32 ? r : r - 32 + skip) * (unsigned)KS + (unsigned)start(c) + 16 * q;
       }
       if (u >= (unsigned)units) off = 0xFFFFFFF0u;  // reads as zero
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + u0 * 16), 16, off, 0, 0, 0);
     }
   }
 
-  // Byte of row r, step and lane group g.
-  __device__ __forceinline__ unsigned get(const uint8_t* lds, int r, int step, int g) const {
-    const int at = 4 * step - start(step) + g;
-    return chunks == 0 ? lds[r * KS + at] : lds[(r * chunks + ((at >> 4) + r) % chunks) * 16 + (at & 15)];
+  // Where byte `at` (uniform) of row r's window lies; rm = r % chunks.
+  __device__ __forceinline__ int where(int r, int rm, int at) const {
+    if (chunks == 0) return r * KS + at;
+    const int slot = (at >> 4) + rm;
+    return (r * chunks + (slot >= chunks ? slot - chunks : slot)) * 16 + (at & 15);
   }
 };
 
@@ -343,169 +353,223 @@ struct ScaleWindow {
 // every slot twice, once on even and once on odd rows.
 __device__ __forceinline__ int swz(int r) { return (r ^ ((r >> 3) & 1)) & 7; }
 
-// One wave: four tiles of 16 rows of an expert's matrix by up to 5 MF tokens, all of K. UP: the gate and up rows of
-// features 32 tile .. + 31 of h (two tiles each), h[pair] = silu(gate) * up. Not UP: output features 64 tile .. + 63.
-// W streams through the wave's own LDS ring by the LDS DMA in half slices of 256 elements, 8 rows x 128 bytes an
-// instruction; the tokens' terms and every scale go to registers, the next ones requested while these are
-// multiplied. Four tiles share what is read of the tokens (with two, reading it from L2 took a third more time).
-// No barrier: waves share nothing.
-template <bool UP, int MF>
-__device__ __forceinline__ void expert_tile(uint8_t* lds, const ExpertArgs& A, int expert, int tile, const int* list, int n) {
-  const int K = UP ? A.D : A.I;
-  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+// Four tiles of 16 rows of an expert's matrix by up to 5 MF tokens, all of K, by a workgroup of S waves. UP: the gate
+// and up rows of features 32 tile .. + 31 of h (two tiles each), h[pair] = silu(gate) * up. Not UP: output
+// features 64 tile .. + 63.
+// Half slice i of 256 elements along K goes to wave i % S, which streams W through its own LDS ring by the LDS DMA, 8
+// rows x 128 bytes an instruction; the tokens' terms go to registers, requested two half slices ahead. Four
+// tiles share what is read of the tokens (with two, reading it from L2 took a third more time). The waves' sums meet
+// once, through LDS, in the order of the waves.
+template <bool UP, int S, int MF>
+__device__ __forceinline__ void expert_tile(uint8_t* lds, const ExpertArgs& A, const Slot* slot, int tile, int j0, int n) {
+  const int K = UP ? A.D : A.I, expert = slot->expert;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
   const unsigned KB = (unsigned)K / 2, KS = (unsigned)K / 32;
-  const int steps = K / 128, nsl = (steps + 3) / 4, nhalf = (steps + 1) / 2;
+  const int steps = K / 128, nhalf = (steps + 1) / 2;
+  const int mine = nhalf > wave ? (nhalf - wave + S - 1) / S : 0;  // this wave's half slices
   const size_t base = (size_t)expert * (UP ? 2 * A.I : A.D) + (UP ? 32 : 64) * (size_t)tile;
-  auto row0 = [&](int t) { return base + (UP ? (t >> 1) * A.I + 16 * (t & 1) : 16 * t); };
-  auto fetch = [&](int i) {
+  uint8_t* ring = lds + wave * (kRing * kHalfBytes);
+  uint8_t* wscl = lds + S * (kRing * kHalfBytes);
+  const ScaleWindow win((int)KS);
+  auto fetch_scales = [&](int c) {
+    win.fetch(wscl, A.ws + base * KS, UP ? A.I + 32u : 64u, UP ? (unsigned)A.I : 32u, c, wave, S);
+  };
+  auto fetch = [&](int j) {
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
-      const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(A.wq + row0(t) * KB, 16u * KB);
+      const size_t row0 = base + (UP ? (t >> 1) * A.I + 16 * (t & 1) : 16 * t);
+      const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(A.wq + row0 * KB, 16u * KB);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const int row = 8 * q + (lane >> 3);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(lds + (i % kRing) * kHalfBytes + t * 2048 + q * 1024), 16,
-                                                 (unsigned)row * KB + (unsigned)i * kHalf +
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(ring + (j % kRing) * kHalfBytes + t * 2048 + q * 1024), 16,
+                                                 (unsigned)row * KB + (unsigned)(wave + S * j) * kHalf +
                                                      16u * (unsigned)((lane & 7) ^ swz(row)),
                                                  0, 0, 0);
       }
     }
   };
-  constexpr int kFetch = 2 * kTiles;  // loads of a fetch
-  const ScaleWindow win((int)KS);
-  uint8_t* wscl = lds + kRing * kHalfBytes;
-  auto fetch_scales = [&](int step) {
-    win.fetch(wscl, A.ws + base * KS, UP ? A.I + 32u : 64u, UP ? (unsigned)A.I : 32u, step);
-  };
-  fetch(0);
+  constexpr int kFetch = 2 * kTiles, kTokenLoads = 6 * MF;  // loads of a fetch, and of a half slice's tokens
   fetch_scales(0);
+  if (mine > 0) fetch(0);
   const int term = r % kTerms;  // column 15 repeats a term of the next token and is not read
+  const int* list = A.list + slot->first;
+  auto pair_of = [&](int j) { return j < kSlotPairs ? slot->pairs[j] : list[j]; };
   const uint8_t *xp[MF], *xsp[MF];
 #pragma unroll
   for (int f = 0; f < MF; ++f) {
-    const int pair = list[min(kTokens * f + r / kTerms, n - 1)], row = UP ? pair / A.k : pair;
+    const int pair = pair_of(j0 + min(kTokens * f + r / kTerms, n - 1)), row = UP ? pair / A.k : pair;
     xp[f] = A.xq + ((size_t)row * kTerms + term) * K + 16 * g;
     xsp[f] = A.xs + (size_t)row * KS;
   }
-  v4u x[MF][2][2], xs[MF];
-  auto load_step = [&](int step, int u) {
-    step = min(step, steps - 1);
+  v4u x[2][MF][2][2];  // [half slice % 2][fragment][step of it][16 bytes]
+  unsigned xs[2][MF][2];
+  auto load_tokens = [&](int j, int h) {
 #pragma unroll
-    for (int f = 0; f < MF; ++f) {
-      // E4M3 operand: a lane group's 32 bytes are elements 16 g .. and 64 + 16 g .. of the step's 128
-      // (measured); block b of 32 elements is scaled by the byte of lane group b for either operand
-      x[f][u][0] = *reinterpret_cast<const v4u*>(xp[f] + (size_t)step * 128);
-      x[f][u][1] = *reinterpret_cast<const v4u*>(xp[f] + (size_t)step * 128 + 64);
+    for (int u = 0; u < 2; ++u) {
+      const int step = min(2 * (wave + S * j) + u, steps - 1);
+#pragma unroll
+      for (int f = 0; f < MF; ++f) {
+        // E4M3 operand: a lane group's 32 bytes are elements 16 g .. and 64 + 16 g .. of the step's 128
+        // (measured); block b of 32 elements is scaled by the byte of lane group b for either operand
+        x[h][f][u][0] = *reinterpret_cast<const v4u*>(xp[f] + (size_t)step * 128);
+        x[h][f][u][1] = *reinterpret_cast<const v4u*>(xp[f] + (size_t)step * 128 + 64);
+        xs[h][f][u] = *reinterpret_cast<const unsigned*>(xsp[f] + 4 * step);
+      }
     }
   };
-  auto load_scales = [&](int sl) {
-#pragma unroll
-    for (int f = 0; f < MF; ++f) xs[f] = slice_scales(xsp[f], sl, KS);
-  };
-  load_scales(0);
-#pragma unroll
-  for (int u = 0; u < 2; ++u) load_step(u, u);
-  if (nhalf > 1) fetch(1);
+  if (mine > 0) load_tokens(0, 0);
+  if (mine > 1) {
+    load_tokens(1, 1);
+    fetch(1);
+  }
+  // window 0 has landed: it was requested first
+  if (mine > 1) wait_vmcnt<2 * kFetch + 2 * kTokenLoads>();
+  else wait_vmcnt<0>();
+  __syncthreads();
   v4f acc[kTiles][MF];
 #pragma unroll
   for (int t = 0; t < kTiles; ++t)
 #pragma unroll
     for (int f = 0; f < MF; ++f) acc[t][f] = v4f{0.f, 0.f, 0.f, 0.f};
-  for (int sl = 0; sl < nsl; ++sl) {
-    unsigned wb[kTiles][4], xb[MF][4];  // this slice's scale bytes of the lane's group, one per step
+  const int rm = win.chunks ? r % win.chunks : 0, rm16 = win.chunks ? 16 % win.chunks : 0;
+  constexpr int kWindow = kScaleRow / 8 / S;  // half slices of a wave per window (of rows longer than one)
+  const int windows = KS > kScaleRow ? (int)((KS + kScaleRow - 1) / kScaleRow) : 1;
+  static_assert(kWindow % 2 == 0, "windows hold whole pairs of half slices");
+  for (int c = 0; c < windows; ++c) {
+    if (c > 0) {
+      __syncthreads();  // every wave has read the window before
+      fetch_scales(c);
+      wait_vmcnt<0>();
+      __syncthreads();
+    }
+    const int start = win.start(c), end = c + 1 < windows ? (c + 1) * kWindow : mine;
+    for (int jj = c * kWindow; jj < end; jj += 2) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = 2 * sl + h;
-      if (i >= nhalf) break;  // uniform
-      // the half slice has landed, and everything requested after it but the next one's loads
-      if (i + 1 < nhalf) __builtin_amdgcn_s_waitcnt(0x0F70 | kFetch);
-      else __builtin_amdgcn_s_waitcnt(0x0F70);
-      asm volatile("" ::: "memory");
-      if (h == 0) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-#pragma unroll
-          for (int t = 0; t < kTiles; ++t) wb[t][u] = win.get(wscl, 16 * t + r, min(4 * sl + u, steps - 1), g);
-#pragma unroll
-          for (int f = 0; f < MF; ++f) xb[f][u] = ((xs[f][u] >> (8 * g)) & 0xFFu) - 4u * (unsigned)term;
-        }
-      }
-      const uint8_t* wa = lds + (i % kRing) * kHalfBytes + r * kHalf;
-      v4u a[2][kTiles];
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t)
-          a[u][t] = *reinterpret_cast<const v4u*>(wa + t * 2048 + 16 * ((4 * u + g) ^ swz(r)));
-      if (h == 0 && sl % 8 == 7 && sl + 1 < nsl) {  // the last slice of a window: its bytes are in registers
-        __builtin_amdgcn_s_waitcnt(0xC07F);
+      for (int h = 0; h < 2; ++h) {
+        const int j = jj + h, i = wave + S * j;
+        if (j >= mine) break;  // uniform in the wave
+        // the half slice has landed: at least the next one's tokens and W were requested after it
+        if (j + 1 < mine) wait_vmcnt<kTokenLoads + kFetch>();
+        else wait_vmcnt<0>();
         asm volatile("" ::: "memory");
-        fetch_scales(4 * sl + 4);
-      }
-      if (h == 1 && sl + 1 < nsl) load_scales(sl + 1);
+        const uint8_t* wa = ring + (j % kRing) * kHalfBytes + r * kHalf;
+        v4u a[2][kTiles];
+        unsigned wb[2][kTiles];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (2 * i + u < steps) {  // uniform
+        for (int u = 0; u < 2; ++u) {
+          int rt = rm;
 #pragma unroll
-          for (int f = 0; f < MF; ++f) {
-            const v8i B = {(int)x[f][u][0][0], (int)x[f][u][0][1], (int)x[f][u][0][2], (int)x[f][u][0][3],
-                           (int)x[f][u][1][0], (int)x[f][u][1][1], (int)x[f][u][1][2], (int)x[f][u][1][3]};
+          for (int t = 0; t < kTiles; ++t) {
+            a[u][t] = *reinterpret_cast<const v4u*>(wa + t * 2048 + 16 * ((4 * u + g) ^ swz(r)));
+            wb[u][t] = wscl[win.where(16 * t + r, rt, 8 * i + 4 * u - start) + g];
+            rt += rm16;
+            rt -= rt >= win.chunks ? win.chunks : 0;
+          }
+        }
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-              const v8i W = {(int)a[u][t][0], (int)a[u][t][1], (int)a[u][t][2], (int)a[u][t][3], 0, 0, 0, 0};
-              acc[t][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(W, B, acc[t][f], 4, 0, 0, (int)wb[t][2 * h + u], 0,
-                                                                           (int)xb[f][2 * h + u]);
+        for (int u = 0; u < 2; ++u) {
+          if (2 * i + u < steps) {  // uniform
+#pragma unroll
+            for (int f = 0; f < MF; ++f) {
+              const v4u x0 = x[h][f][u][0], x1 = x[h][f][u][1];
+              const v8i B = {(int)x0[0], (int)x0[1], (int)x0[2], (int)x0[3], (int)x1[0], (int)x1[1], (int)x1[2], (int)x1[3]};
+              const int xb = (int)((xs[h][f][u] >> (8 * g)) & 0xFFu) - 4 * term;
+#pragma unroll
+              for (int t = 0; t < kTiles; ++t) {
+                const v8i W = {(int)a[u][t][0], (int)a[u][t][1], (int)a[u][t][2], (int)a[u][t][3], 0, 0, 0, 0};
+                acc[t][f] =
+                    __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(W, B, acc[t][f], 4, 0, 0, (int)wb[u][t], 0, xb);
+              }
             }
           }
         }
-        if (i + 1 < nhalf) load_step(2 * i + 2 + u, u);
+        if (j + 2 < mine) load_tokens(j + 2, h);
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the half slice has been read before its slot is refilled
+        asm volatile("" ::: "memory");
+        if (j + kRing < mine) fetch(j + kRing);
       }
-      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the half slice has been read before its slot is refilled
-      asm volatile("" ::: "memory");
-      if (i + kRing < nhalf) fetch(i + kRing);
     }
   }
-  // The three terms of token j are columns 3 j .. 3 j + 2 of a DPP row; lane (3 j, g) ends with features 4 g .. + 3.
+  // Partial sums into the wave's own ring, then sum them in the order of the waves.
+  v4f* red = reinterpret_cast<v4f*>(ring);
 #pragma unroll
-  for (int f = 0; f < MF; ++f) {
-    v4f y[kTiles];
+  for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t)
+    for (int f = 0; f < MF; ++f) red[(t * MF + f) * 64 + lane] = acc[t][f];
+  __syncthreads();
+  auto sum_of = [&](int t, int f) {
+    const uint8_t* at = lds + ((t * MF + f) * 64 + lane) * 16;
+    v4f v = *reinterpret_cast<const v4f*>(at), y;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float v = acc[t][f][i];
-        const int b = __float_as_int(v);
-        y[t][i] = (v + __int_as_float(__builtin_amdgcn_update_dpp(0, b, 0x101, 0xF, 0xF, false))) +  // row_shl:1
-                  __int_as_float(__builtin_amdgcn_update_dpp(0, b, 0x102, 0xF, 0xF, false));         // row_shl:2
-      }
-    const int j = kTokens * f + r / kTerms;
+    for (int w = 1; w < S; ++w) v += *reinterpret_cast<const v4f*>(at + w * (kRing * kHalfBytes));
+    // the three terms of token j are columns 3 j .. 3 j + 2 of a DPP row; lane (3 j, g) ends with features 4 g .. + 3
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int b = __float_as_int(v[i]);
+      y[i] = (v[i] + __int_as_float(__builtin_amdgcn_update_dpp(0, b, 0x101, 0xF, 0xF, false))) +  // row_shl:1
+             __int_as_float(__builtin_amdgcn_update_dpp(0, b, 0x102, 0xF, 0xF, false));             // row_shl:2
+    }
+    return y;
+  };
+  constexpr int kItems = (UP ? 2 : kTiles) * MF;
+  for (int q = wave; q < kItems; q += S) {
+    const int t = q / MF, f = q % MF, j = kTokens * f + r / kTerms;
+    const v4f y = sum_of(t, f);
+    v4f up = y;
+    if constexpr (UP) up = sum_of(t + 2, f);
     if (term != 0 || r == 15 || j >= n) continue;
-    const size_t pair = list[j];
+    const size_t pair = pair_of(j0 + j);
     if constexpr (UP) {
+      v4f h;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        v4f h;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = y[t][i] / (1.0f + expf(-y[t][i])) * y[t + 2][i];
-        *reinterpret_cast<v4f*>(A.out + pair * A.I + 32 * tile + 16 * t + 4 * g) = h;
-      }
+      for (int i = 0; i < 4; ++i) h[i] = y[i] / (1.0f + expf(-y[i])) * up[i];
+      *reinterpret_cast<v4f*>(A.out + pair * A.I + 32 * tile + 16 * t + 4 * g) = h;
     } else {
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t) *reinterpret_cast<v4f*>(A.out + pair * A.D + 64 * tile + 16 * t + 4 * g) = y[t];
+      *reinterpret_cast<v4f*>(A.out + pair * A.D + 64 * tile + 16 * t + 4 * g) = y;
     }
   }
 }
 
-template <bool UP>
-__global__ __launch_bounds__(64) void expert_gemm(ExpertArgs A, int tiles) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kExpertLds];
-  const Slot s = A.slot[blockIdx.x / tiles];
-  const int tile = blockIdx.x % tiles;
-  for (int j = 0; j < s.n; j += kTokens * kMaxFrags) {
-    const int m = min(s.n - j, kTokens * kMaxFrags);
-    if (m <= kTokens) expert_tile<UP, 1>(lds, A, s.expert, tile, A.list + s.first + j, m);
-    else expert_tile<UP, 2>(lds, A, s.expert, tile, A.list + s.first + j, m);
+template <bool UP, int S>
+__global__ __launch_bounds__(64 * S) void expert_gemm(ExpertArgs A, int tiles) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  const Slot* s = A.slot + blockIdx.x / tiles;
+  const int tile = blockIdx.x % tiles, n = s->n;
+  for (int j = 0; j < n; j += kTokens * kMaxFrags) {
+    if (j > 0) __syncthreads();  // the sums of the pass before have been read
+    const int m = min(n - j, kTokens * kMaxFrags);
+    if (m <= kTokens) expert_tile<UP, S, 1>(lds, A, s, tile, j, m);
+    else expert_tile<UP, S, 2>(lds, A, s, tile, j, m);
   }
+}
+
+template <bool UP, int S>
+hipError_t launch_gemm(const ExpertArgs& A, int slots, int tiles, hipStream_t st) {
+  static std::atomic<int> ready[64];
+  constexpr int lds = S * kRing * kHalfBytes + kScaleBytes;
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  auto kern = expert_gemm<UP, S>;
+  const bool cached = dev >= 0 && dev < 64;
+  if (!cached || !ready[dev].load(std::memory_order_acquire)) {
+    e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+    if (cached) ready[dev].store(1, std::memory_order_release);
+  }
+  hipLaunchKernelGGL(kern, dim3((unsigned)(slots * tiles)), dim3(64 * S), lds, st, A, tiles);
+  return hipGetLastError();
+}
+
+// Two waves a workgroup where there are workgroups enough for four on every CU, eight where K has to be split
+// further to fill the chip (6 of 64 experts of 4096 x 1408, 64 tokens: 151 us with two, 168 with four, 230 with
+// eight; one token, 8 of 128 of 2048 x 768: 25.6, 25.2, 25.1 us).
+template <bool UP>
+hipError_t launch_experts(const ExpertArgs& A, int slots, hipStream_t st) {
+  const int tiles = UP ? A.I / 32 : A.D / 64;
+  return slots * tiles < 1024 ? launch_gemm<UP, 8>(A, slots, tiles, st) : launch_gemm<UP, 2>(A, slots, tiles, st);
 }
 
 // y[t][d .. d + 3] = sum over the slots in order of p * out; slots without an expert add nothing.
@@ -577,13 +641,11 @@ hipError_t fp4_launch_moe_experts(const uint16_t* X, int64_t T, int64_t D, int64
   hipError_t e = launch_split<true>(block, X, ldx, (int)T, (int)D, xq, xs, plan, st);
   if (e != hipSuccess) return e;
   const ExpertArgs up{slot, list, k, (int)D, (int)I, W13q, W13s, xq, xs, h};
-  hipLaunchKernelGGL(expert_gemm<true>, dim3((unsigned)(slots * (I / 32))), dim3(64), 0, st, up, (int)(I / 32));
-  e = hipGetLastError();
+  e = launch_experts<true>(up, slots, st);
   if (e == hipSuccess) e = launch_split<false>(block, h, I, pairs, (int)I, hq, hs, plan, st);
   if (e != hipSuccess) return e;
   const ExpertArgs down{slot, list, k, (int)D, (int)I, W2q, W2s, hq, hs, out};
-  hipLaunchKernelGGL(expert_gemm<false>, dim3((unsigned)(slots * (D / 64))), dim3(64), 0, st, down, (int)(D / 64));
-  e = hipGetLastError();
+  e = launch_experts<false>(down, slots, st);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(combine, dim3((unsigned)((T * (D / 4) + 255) / 256)), dim3(256), 0, st, ids, weights, out, (int)T, k,
                      (int)E, (int)D, Y);
