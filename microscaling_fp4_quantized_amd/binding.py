@@ -460,7 +460,7 @@ def fp4_moe_route(x: torch.Tensor, router: torch.Tensor, k: int, renormalize: bo
     """softmax(x router^T) in float32 and its k largest of each token: (ids [T, k] int32, weights [T, k] float32).
 
     x bf16 [T, D], router bf16 [E, D]. Of equal weights the lowest expert comes first. ``out`` may pass
-    preallocated (ids, weights); workspace: "auto", or a uint8 CUDA tensor of at least 4 T E bytes."""
+    preallocated (ids, weights); workspace: "auto", or a uint8 CUDA tensor of at least 16 T E bytes."""
     name = "fp4_moe_route"
     lib = load_library()
     T, D, ld = _rows(x, name, "x")
@@ -475,7 +475,7 @@ def fp4_moe_route(x: torch.Tensor, router: torch.Tensor, k: int, renormalize: bo
         ids, weights = out
         _expect(ids, (T, k), torch.int32, name, "ids")
         _expect(weights, (T, k), torch.float32, name, "weights")
-    ws = _workspace(workspace, 4 * T * E, name, x.device)
+    ws = _workspace(workspace, 16 * T * E, name, x.device)
     _same_device(name, x.device, router, ids, weights, ws)
     _enqueue(lib.fp4_moe_route, x.device, x.data_ptr(), T, D, ld, router.data_ptr(), E, k, int(bool(renormalize)),
              ids.data_ptr(), weights.data_ptr(), ws.data_ptr(), ws.numel())

@@ -31,9 +31,13 @@ typedef __attribute__((address_space(3))) void lds_void;
 
 // ---- route -----------------------------------------------------------------------------------------------------------
 
-constexpr int kRouteWaves = 8;
+// Two launches: the logits, bound by the latency of reading Wr, and the choice, bound by that of k rounds of a wave.
+// D is split over kRouteSplit workgroups of kRouteWaves waves each, so that a wave has one or two loads of 16 experts'
+// rows to wait for even for one token; the choice adds the splits' sums in order. (8 of 128 experts, D 2048, 1 token:
+// 4.6 + 9.2 us with D in one workgroup and all of k rounds over 1024 experts' registers, now 3.0 + 3.2 us.)
+constexpr int kRouteWaves = 4, kRouteSplit = FP4_MOE_ROUTE_SPLIT;
 
-// Logits of 16 experts x 16 tokens: v_mfma_f32_16x16x32_bf16, products of bf16 exact in float32, the waves
+// Partial logits of 16 experts x 16 tokens: v_mfma_f32_16x16x32_bf16, products of bf16 exact in float32, the waves
 // taking slices of 128 along D. Lane group g takes 32 consecutive elements of the slice for both operands.
 __global__ __launch_bounds__(kRouteWaves * 64) void route_logits(const uint16_t* __restrict__ X, int64_t ldx,
                                                                  const uint16_t* __restrict__ Wr, int T, int E, int D,
@@ -44,7 +48,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_logits(const uint16_t*
   const uint16_t* w = Wr + (size_t)min(e0 + r, E - 1) * D + 32 * g;
   const uint16_t* x = X + (size_t)min(t0 + r, T - 1) * ldx + 32 * g;
   v4f acc = {0.f, 0.f, 0.f, 0.f};
-  for (int s = wave; s < D / 128; s += kRouteWaves) {
+  for (int s = blockIdx.z * kRouteWaves + wave; s < D / 128; s += kRouteSplit * kRouteWaves) {
     v4u a[4], b[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -64,13 +68,13 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_logits(const uint16_t*
   for (int i = 1; i < kRouteWaves; ++i) sum += red[i][lane];
   // lane holds experts e0 + 4 g + i of token t0 + r
   if (t0 + r >= T) return;
+  float* dst = logits + ((size_t)blockIdx.z * T + t0 + r) * E + e0 + 4 * g;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (e0 + 4 * g + i < E) logits[(size_t)(t0 + r) * E + e0 + 4 * g + i] = sum[i];
+    if (e0 + 4 * g + i < E) dst[i] = sum[i];
 }
 
 constexpr int kMaxExperts = 1024;
-constexpr int kRouteRegs = kMaxExperts / 64;
 
 // Unsigned order of float values: larger value, larger key; NaN below every number, and 0 below all.
 __device__ __forceinline__ unsigned order_key(float v) {
@@ -80,50 +84,69 @@ __device__ __forceinline__ unsigned order_key(float v) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u) + 1u;
 }
 
-// One wave per token: softmax over E logits, then k rounds of the largest remaining logit (lowest index first).
+// Maximum over the 64 lanes, uniform: rows of 16 by DPP rotations, then the four rows' by v_readlane.
+__device__ __forceinline__ unsigned wave_max(unsigned m) {
+  m = row16_max(m);
+  const unsigned a = __builtin_amdgcn_readlane(m, 0), b = __builtin_amdgcn_readlane(m, 16);
+  const unsigned c = __builtin_amdgcn_readlane(m, 32), d = __builtin_amdgcn_readlane(m, 48);
+  return max(max(a, b), max(c, d));
+}
+
+// One wave per token: softmax over E <= 64 R logits, then k rounds of the largest remaining logit (lowest index
+// first). Expert i * 64 + lane is in register i.
+template <int R>
 __global__ __launch_bounds__(256) void route_topk(const float* __restrict__ logits, int T, int E, int k, int renorm,
                                                   int* __restrict__ ids, float* __restrict__ weights) {
   const int lane = threadIdx.x & 63, t = blockIdx.x * 4 + (threadIdx.x >> 6);
   if (t >= T) return;
-  float v[kRouteRegs];
-  unsigned key[kRouteRegs];
-  float m = -__builtin_inff();
+  float v[R];
+  unsigned key[R], top = 0;
 #pragma unroll
-  for (int i = 0; i < kRouteRegs; ++i) {
-    const int e = i * 64 + lane;
-    v[i] = e < E ? logits[(size_t)t * E + e] : -__builtin_inff();
-    key[i] = e < E ? order_key(v[i]) : 0u;
-    m = fmaxf(m, v[i]);
+  for (int i = 0; i < R; ++i) {
+    const int e = min(i * 64 + lane, E - 1);
+    float z[kRouteSplit];
+#pragma unroll
+    for (int s = 0; s < kRouteSplit; ++s) z[s] = logits[((size_t)s * T + t) * E + e];
+    v[i] = z[0];
+#pragma unroll
+    for (int s = 1; s < kRouteSplit; ++s) v[i] += z[s];
   }
+  // the largest number: keys of numbers are above 1
 #pragma unroll
-  for (int h = 32; h > 0; h >>= 1) m = fmaxf(m, __shfl_xor(m, h));
+  for (int i = 0; i < R; ++i) {
+    key[i] = i * 64 + lane < E ? order_key(v[i]) : 0u;
+    top = max(top, key[i]);
+  }
+  top = wave_max(top);
+  const float m = top <= 1u ? 0.f  // NaN throughout
+                  : top > 0x80000000u ? __uint_as_float((top - 1u) & 0x7FFFFFFFu) : __uint_as_float(~top);
   float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < kRouteRegs; ++i)
-    if (i * 64 + lane < E) sum += expf(v[i] - m);
+  for (int i = 0; i < R; ++i) {
+    v[i] = expf(v[i] - m);
+    if (i * 64 + lane < E) sum += v[i];
+  }
   sum = wave_sum(sum);
   float mine = 0.f, chosen = 0.f;
   int my_id = 0;
   for (int j = 0; j < k; ++j) {
-    unsigned best = 0, at = 0;
+    unsigned best = key[0];
 #pragma unroll
-    for (int i = 0; i < kRouteRegs; ++i)
-      if (key[i] > best) best = key[i], at = i * 64 + lane;
+    for (int i = 1; i < R; ++i) best = max(best, key[i]);
+    best = wave_max(best);
+    bool found = false;
 #pragma unroll
-    for (int h = 32; h > 0; h >>= 1) {
-      const unsigned ob = __shfl_xor(best, h), oa = __shfl_xor(at, h);
-      if (ob > best || (ob == best && oa < at)) best = ob, at = oa;
-    }
-    float p = 0.f;
-#pragma unroll
-    for (int i = 0; i < kRouteRegs; ++i)
-      if ((unsigned)(i * 64 + lane) == at) {
-        p = expf(v[i] - m) / sum;
-        key[i] = 0;
+    for (int i = 0; i < R; ++i) {
+      const uint64_t mask = __ballot(key[i] == best);
+      if (!found && mask != 0) {  // uniform: the lowest register, then the lowest lane
+        found = true;
+        const int at = __ffsll((unsigned long long)mask) - 1;
+        const float p = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v[i]), at)) / sum;
+        chosen += p;
+        if (lane == j) mine = p, my_id = i * 64 + at;
+        if (lane == at) key[i] = 0;
       }
-    p = __shfl(p, at & 63);
-    chosen += p;
-    if (lane == j) mine = p, my_id = at;
+    }
   }
   if (lane < k) {
     ids[(size_t)t * k + lane] = my_id;
@@ -614,11 +637,12 @@ hipError_t launch_split(int block, const void* V, int64_t ld, int rows, int K, u
 hipError_t fp4_launch_moe_route(const uint16_t* X, int64_t T, int64_t D, int64_t ldx, const uint16_t* Wr, int64_t E, int k,
                                 int renorm, float* logits, int* ids, float* weights, hipStream_t st) {
   using namespace fp4;
-  const dim3 grid((unsigned)((E + 15) / 16), (unsigned)((T + 15) / 16));
+  const dim3 grid((unsigned)((E + 15) / 16), (unsigned)((T + 15) / 16), kRouteSplit);
   hipLaunchKernelGGL(route_logits, grid, dim3(kRouteWaves * 64), 0, st, X, ldx, Wr, (int)T, (int)E, (int)D, logits);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(route_topk, dim3((unsigned)((T + 3) / 4)), dim3(256), 0, st, logits, (int)T, (int)E, k, renorm, ids,
+  auto topk = E <= 64 ? route_topk<1> : E <= 128 ? route_topk<2> : E <= 256 ? route_topk<4> : route_topk<kMaxExperts / 64>;
+  hipLaunchKernelGGL(topk, dim3((unsigned)((T + 3) / 4)), dim3(256), 0, st, logits, (int)T, (int)E, k, renorm, ids,
                      weights);
   return hipGetLastError();
 }
