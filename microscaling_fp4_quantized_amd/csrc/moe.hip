@@ -372,9 +372,9 @@ struct ScaleWindow {
   }
 };
 
-// 16-byte chunk q of row r of a tile's half slice sits at slot q ^ swz(r): the 16 rows of a fragment read take
-// every slot twice, once on even and once on odd rows.
-__device__ __forceinline__ int swz(int r) { return (r ^ ((r >> 3) & 1)) & 7; }
+// 16-byte chunk q of row r of a tile's half slice sits at slot q ^ swz(r): the lanes that ds_read_b128 serves together
+// (0-3, 12-15 and 20-27, ...) then read distinct banks.
+__device__ __forceinline__ int swz(int r) { return r & 7; }
 
 // Four tiles of 16 rows of an expert's matrix by up to 5 MF tokens, all of K, by a workgroup of S waves. UP: the gate
 // and up rows of features 32 tile .. + 31 of h (two tiles each), h[pair] = silu(gate) * up. Not UP: output

@@ -173,7 +173,11 @@ LINEAR = [(1, 16, 128), (1, 1, 128), (1, 130, 384), (2, 17, 256), (3, 64, 512), 
           (17, 515, 1152), (31, 128, 4224), (33, 300, 896), (37, 4100, 1024), (48, 96, 2176), (63, 1000, 512),
           (64, 129, 8192), (65, 256, 384), (100, 200, 640), (128, 1024, 1024), (129, 1100, 1280), (200, 2050, 512),
           (255, 333, 896), (256, 256, 128), (257, 513, 1408), (300, 4100, 384), (511, 900, 2048), (1000, 1000, 640),
-          (1, 4096, 16384), (4, 20000, 256)]
+          (1, 4096, 16384), (4, 20000, 256),
+          # every tile shape of the large kernel, ragged, and K past 64 scale blocks
+          (20, 300, 8320), (64, 5000, 8448), (9, 9000, 1152), (100, 13000, 640), (128, 13001, 8320), (200, 14000, 384),
+          (250, 14100, 1152), (300, 14000, 640), (700, 8190, 1152), (700, 8192, 8320), (1030, 12300, 512),
+          (1030, 12300, 640), (1100, 12301, 1152), (1030, 12290, 2176), (1300, 12300, 8320), (4000, 5000, 896)]
 
 
 @pytest.mark.parametrize("M,N,K", LINEAR)
