@@ -352,16 +352,16 @@ FP4_API int fp8_linear(const uint8_t *Xq, const float *Xs, const uint8_t *Wq, co
  */
 #define FP4_MOE_MAX_TOKENS 128
 #define FP4_MOE_MAX_TOPK 16
-#define FP4_MOE_WS_PLAN_PAIR 68
+#define FP4_MOE_WS_PLAN_PAIR 84
 #define FP4_MOE_PAD_(n) (((size_t)(n) + 255) / 256 * 256)
 #define FP4_MOE_ROUTE_SPLIT 4 /* the logits' partial sums */
 #define FP4_MOE_ROUTE_WORKSPACE_BYTES(T, E) ((size_t)(T) * (E) * 4 * FP4_MOE_ROUTE_SPLIT)
 /* the experts' workspace: terms and scales of X, h, its terms and scales, the slots'
  * outputs, the pairs sorted by expert */
-#define FP4_MOE_WS_XS(T, k, D, I) FP4_MOE_PAD_((size_t)(T) * 3 * (D))
+#define FP4_MOE_WS_XS(T, k, D, I) FP4_MOE_PAD_((size_t)(T) * 4 * (D))
 #define FP4_MOE_WS_H(T, k, D, I) (FP4_MOE_WS_XS(T, k, D, I) + FP4_MOE_PAD_((size_t)(T) * (D) / 32))
 #define FP4_MOE_WS_HQ(T, k, D, I) (FP4_MOE_WS_H(T, k, D, I) + FP4_MOE_PAD_((size_t)(T) * (k) * (I) * 4))
-#define FP4_MOE_WS_HS(T, k, D, I) (FP4_MOE_WS_HQ(T, k, D, I) + FP4_MOE_PAD_((size_t)(T) * (k) * 3 * (I)))
+#define FP4_MOE_WS_HS(T, k, D, I) (FP4_MOE_WS_HQ(T, k, D, I) + FP4_MOE_PAD_((size_t)(T) * (k) * 4 * (I)))
 #define FP4_MOE_WS_OUT(T, k, D, I) (FP4_MOE_WS_HS(T, k, D, I) + FP4_MOE_PAD_((size_t)(T) * (k) * (I) / 32))
 #define FP4_MOE_WS_PLAN(T, k, D, I) (FP4_MOE_WS_OUT(T, k, D, I) + FP4_MOE_PAD_((size_t)(T) * (k) * (D) * 4))
 #define FP4_MOE_WORKSPACE_BYTES(T, k, D, I) (FP4_MOE_WS_PLAN(T, k, D, I) + (size_t)(T) * (k) * FP4_MOE_WS_PLAN_PAIR)

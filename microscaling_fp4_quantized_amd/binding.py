@@ -487,7 +487,7 @@ def moe_workspace_bytes(T: int, k: int, D: int, I: int) -> int:
     def pad(n):
         return (n + 255) // 256 * 256
     P = T * k
-    return pad(T * 3 * D) + pad(T * D // 32) + pad(P * I * 4) + pad(P * 3 * I) + pad(P * I // 32) + pad(P * D * 4) + 68 * P
+    return pad(T * 4 * D) + pad(T * D // 32) + pad(P * I * 4) + pad(P * 4 * I) + pad(P * I // 32) + pad(P * D * 4) + 84 * P
 
 
 def fp4_moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13q, w13s, w2q, w2s, block: int,

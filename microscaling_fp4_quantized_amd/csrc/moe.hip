@@ -9,16 +9,21 @@
 // its 16 columns free, so an activation is not rounded to 8 bits: it is stored as a sum of THREE E4M3 terms,
 //   v / s = q0 + q1 / 16 + q2 / 256,  q_i = e4m3(what is left * 16^i),  s a power of two per 32 values,
 // each rounding leaving at most 2^-4 of what it rounds, so at most 2^-12 of v (or 2^-18 of the group's largest) is
-// lost, where bf16 would lose 2^-9. The three terms are three columns of one instruction, 5 tokens to
-// 16 columns, and are added in float32 at the end. The factors 16^-i ride in the E8M0 scale operand.
+// lost, where bf16 would lose 2^-9. The three terms are three columns of one instruction, and are added in float32
+// at the end. The factors 16^-i ride in the E8M0 scale operand. A token takes four columns (the fourth is zero), 4
+// tokens to 16: a quad of lanes then reads 64 bytes that lie together. The cache serves a quad's line per clock, and
+// 16-byte pieces of four different rows four times slower (38 against 150 B/ns a CU).
 //
 // Steps of a call (each a launch; every sum in a fixed order):
-//   split x    rotate (float32), split into terms   [T, 3, D]; one more workgroup sorts the pairs by expert
+//   split x    rotate (float32), split into terms   [T, 4, D]; one more workgroup sorts the pairs by expert
 //   up         per used expert and 32 features of h: gate and up rows, silu(g) * u in float32   [T k, I]
-//   split h    rotate, split                                                                    [T k, 3, I]
+//   split h    rotate, split                                                                    [T k, 4, I]
 //   down       per used expert and 64 output features, float32                                  [T k, D]
 //   combine    y_t = sum_j p_tj * down, over the slots in order, rounded once to bf16
+#include <algorithm>
 #include <atomic>
+#include <cmath>
+#include <type_traits>
 
 #include "fp8_device.hpp"
 #include "quant_device.hpp"
@@ -157,8 +162,9 @@ __global__ __launch_bounds__(256) void route_topk(const float* __restrict__ logi
 // ---- experts ---------------------------------------------------------------------------------------------------------
 
 constexpr int kTerms = 3;
-constexpr int kTokens = 5;           // tokens per fragment of 16 columns
-constexpr int kMaxFrags = 2;         // fragments per pass over an expert's weights
+constexpr int kCols = 4;             // columns of a token: its terms, and zeros
+constexpr int kTokens = 16 / kCols;  // tokens per fragment of 16 columns
+constexpr int kMaxFrags = 4;         // fragments per pass over an expert's weights
 constexpr int kTiles = 4;            // tiles of 16 rows per wave
 constexpr int kHalf = 128;           // bytes (256 elements) of a row per half slice
 constexpr int kHalfBytes = kTiles * 16 * kHalf;
@@ -168,7 +174,7 @@ constexpr int kScaleBytes = kTiles * 16 * kScaleRow;
 
 // The pairs (t k + slot) of one used expert: list[first .. first + n - 1], and the first of them here, so that a
 // workgroup has them with its first load; n = 0 past the last used expert.
-constexpr int kSlotPairs = 12;
+constexpr int kSlotPairs = 16;
 struct Slot {
   int expert, n, first, pad, pairs[kSlotPairs];
 };
@@ -184,11 +190,18 @@ __device__ __forceinline__ void wait_vmcnt() {
   __builtin_amdgcn_s_waitcnt((N & 0xF) | (0x7 << 4) | (0xF << 8) | (((N >> 4) & 3) << 14));
 }
 
-// Rotate 32 values (a chunk of the Hadamard block, see fwht) and write their terms and the group's E8M0
-// code. The code puts the group's largest magnitude into (224, 448], and is at least 8, so that the terms'
-// codes, 4 less each, stay codes. A group that is not finite gets NaN terms.
+// Where the 16 bytes of elements 128 step + 64 half + 16 g .. + 15 and column c of a row of K elements lie, from the
+// row's start (4 K bytes a row): the order in which lane (4 token + c, g) reads them as the product's operand. (An
+// E4M3 operand's lane group g takes elements 16 g .. and 64 + 16 g .. of an instruction's 128: measured.)
+__device__ __forceinline__ int term_offset(int step, int half, int g, int c) {
+  return ((step * 2 + half) * 4 + g) * (kCols * 16) + c * 16;
+}
+
+// Rotate chunk `at` of 32 values of a row (part of its Hadamard block, see fwht) and write its terms and its E8M0
+// code. The code puts the chunk's largest magnitude into (224, 448], and is at least 12, so that the columns'
+// codes, 4 less each, stay codes. A chunk that is not finite gets NaN terms.
 template <int B>
-__device__ __forceinline__ void split_chunk(float v[32], uint8_t* q, int64_t term_stride, uint8_t* scale) {
+__device__ __forceinline__ void split_chunk(float v[32], uint8_t* row, int at, uint8_t* scale) {
   fwht<B>(v);
   const float c = __uint_as_float(hadamard_constant_bits(B));
   unsigned m = 0;
@@ -199,28 +212,30 @@ __device__ __forceinline__ void split_chunk(float v[32], uint8_t* q, int64_t ter
   }
   // |max| = 1.f * 2^(e - 127); 448 = 1.75 * 2^8
   const int e = (int)(m >> 23) - 8 + ((m & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  const int code = e < 8 ? 8 : e;
+  const int code = e < 12 ? 12 : e;
   const bool finite = m < 0x7F800000u;
   const float inv = __uint_as_float((unsigned)(254 - code) << 23);  // 2^(127 - code), code <= 247
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] *= inv;
+  const int step = at >> 2, half = (at >> 1) & 1, g = 2 * (at & 1);
 #pragma unroll
-  for (int t = 0; t < kTerms; ++t) {
-    unsigned w[8];
+  for (int t = 0; t < kCols; ++t) {
+    unsigned w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (t < kTerms) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      int b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i], v[4 * i + 1], 0, false);
-      b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2], v[4 * i + 3], b, true);
-      const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8(b, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(b, true);
-      v[4 * i] = (v[4 * i] - lo[0]) * 16.f;
-      v[4 * i + 1] = (v[4 * i + 1] - lo[1]) * 16.f;
-      v[4 * i + 2] = (v[4 * i + 2] - hi[0]) * 16.f;
-      v[4 * i + 3] = (v[4 * i + 3] - hi[1]) * 16.f;
-      w[i] = finite ? (unsigned)b : 0x7F7F7F7Fu;
+      for (int i = 0; i < 8; ++i) {
+        int b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i], v[4 * i + 1], 0, false);
+        b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2], v[4 * i + 3], b, true);
+        const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8(b, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(b, true);
+        v[4 * i] = (v[4 * i] - lo[0]) * 16.f;
+        v[4 * i + 1] = (v[4 * i + 1] - lo[1]) * 16.f;
+        v[4 * i + 2] = (v[4 * i + 2] - hi[0]) * 16.f;
+        v[4 * i + 3] = (v[4 * i + 3] - hi[1]) * 16.f;
+        w[i] = finite ? (unsigned)b : 0x7F7F7F7Fu;
+      }
     }
-    v4u* dst = reinterpret_cast<v4u*>(q + t * term_stride);
-    dst[0] = v4u{w[0], w[1], w[2], w[3]};
-    dst[1] = v4u{w[4], w[5], w[6], w[7]};
+    *reinterpret_cast<v4u*>(row + term_offset(step, half, g, t)) = v4u{w[0], w[1], w[2], w[3]};
+    *reinterpret_cast<v4u*>(row + term_offset(step, half, g + 1, t)) = v4u{w[4], w[5], w[6], w[7]};
   }
   *scale = (uint8_t)(finite ? code : 127);
 }
@@ -292,7 +307,7 @@ struct PlanArgs {
   int* list;
 };
 
-// Rows of `cpr` chunks of 32 values -> terms [row][3][32 cpr] and scales [row][cpr]; one lane a chunk. The
+// Rows of `cpr` chunks of 32 values -> terms (4 * 32 cpr bytes a row) and scales [row][cpr]; one lane a chunk. The
 // 2 or 4 chunks of a Hadamard block of 64 or 128 sit in adjacent lanes (cpr % 4 == 0). With PLAN, the first
 // workgroup sorts the pairs instead.
 template <int B, bool PLAN>
@@ -319,8 +334,20 @@ __global__ __launch_bounds__(256) void split_rows(const void* __restrict__ V, in
 #pragma unroll
     for (int i = 0; i < 4; ++i) widen8(p[i], v + 8 * i);
   }
-  const int64_t K = 32 * (int64_t)cpr;
-  split_chunk<B>(v, q + row * kTerms * K + at * 32, K, scales + c);
+  split_chunk<B>(v, q + (size_t)row * cpr * (32 * kCols), at, scales + c);
+}
+
+// The three terms of token j are columns 4 j .. 4 j + 2 of a DPP row: lane (4 j, g) ends with their sums for features
+// 4 g .. 4 g + 3.
+__device__ __forceinline__ v4f term_sums(v4f v) {
+  v4f y;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int b = __float_as_int(v[i]);
+    y[i] = (v[i] + __int_as_float(__builtin_amdgcn_update_dpp(0, b, 0x101, 0xF, 0xF, false))) +  // row_shl:1
+           __int_as_float(__builtin_amdgcn_update_dpp(0, b, 0x102, 0xF, 0xF, false));             // row_shl:2
+  }
+  return y;
 }
 
 struct ExpertArgs {
@@ -376,11 +403,12 @@ struct ScaleWindow {
 // (0-3, 12-15 and 20-27, ...) then read distinct banks.
 __device__ __forceinline__ int swz(int r) { return r & 7; }
 
-// Four tiles of 16 rows of an expert's matrix by up to 5 MF tokens, all of K, by a workgroup of S waves. UP: the gate
+// Four tiles of 16 rows of an expert's matrix by up to 4 MF tokens, all of K, by a workgroup of S waves. UP: the gate
 // and up rows of features 32 tile .. + 31 of h (two tiles each), h[pair] = silu(gate) * up. Not UP: output
 // features 64 tile .. + 63.
 // Half slice i of 256 elements along K goes to wave i % S, which streams W through its own LDS ring by the LDS DMA, 8
-// rows x 128 bytes an instruction; the tokens' terms go to registers, requested two half slices ahead. Four
+// rows x 128 bytes an instruction; the tokens' terms go to registers, requested two half slices ahead (one, with
+// more than two fragments). Four
 // tiles share what is read of the tokens (with two, reading it from L2 took a third more time). The waves' sums meet
 // once, through LDS, in the order of the waves.
 template <bool UP, int S, int MF>
@@ -416,39 +444,39 @@ __device__ __forceinline__ void expert_tile(uint8_t* lds, const ExpertArgs& A, c
   constexpr int kFetch = 2 * kTiles, kTokenLoads = 6 * MF;  // loads of a fetch, and of a half slice's tokens
   fetch_scales(0);
   if (mine > 0) fetch(0);
-  const int term = r % kTerms;  // column 15 repeats a term of the next token and is not read
+  const int col = r % kCols;
   const int* list = A.list + slot->first;
   auto pair_of = [&](int j) { return j < kSlotPairs ? slot->pairs[j] : list[j]; };
   const uint8_t *xp[MF], *xsp[MF];
 #pragma unroll
   for (int f = 0; f < MF; ++f) {
-    const int pair = pair_of(j0 + min(kTokens * f + r / kTerms, n - 1)), row = UP ? pair / A.k : pair;
-    xp[f] = A.xq + ((size_t)row * kTerms + term) * K + 16 * g;
+    const int pair = pair_of(j0 + min(kTokens * f + r / kCols, n - 1)), row = UP ? pair / A.k : pair;
+    xp[f] = A.xq + (size_t)row * K * kCols + term_offset(0, 0, g, col);
     xsp[f] = A.xs + (size_t)row * KS;
   }
-  v4u x[2][MF][2][2];  // [half slice % 2][fragment][step of it][16 bytes]
-  unsigned xs[2][MF][2];
+  constexpr int XB = MF <= 2 ? 2 : 1;  // half slices of the tokens in registers
+  v4u x[XB][MF][2][2];                 // [half slice % XB][fragment][step of it][16 bytes]
+  unsigned xs[XB][MF][2];
   auto load_tokens = [&](int j, int h) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int step = min(2 * (wave + S * j) + u, steps - 1);
 #pragma unroll
       for (int f = 0; f < MF; ++f) {
-        // E4M3 operand: a lane group's 32 bytes are elements 16 g .. and 64 + 16 g .. of the step's 128
-        // (measured); block b of 32 elements is scaled by the byte of lane group b for either operand
-        x[h][f][u][0] = *reinterpret_cast<const v4u*>(xp[f] + (size_t)step * 128);
-        x[h][f][u][1] = *reinterpret_cast<const v4u*>(xp[f] + (size_t)step * 128 + 64);
-        xs[h][f][u] = *reinterpret_cast<const unsigned*>(xsp[f] + 4 * step);
+        // block b of 32 elements is scaled by the byte of lane group b, for either operand (measured)
+        x[h % XB][f][u][0] = *reinterpret_cast<const v4u*>(xp[f] + (size_t)step * (128 * kCols));
+        x[h % XB][f][u][1] = *reinterpret_cast<const v4u*>(xp[f] + (size_t)step * (128 * kCols) + 64 * kCols);
+        xs[h % XB][f][u] = *reinterpret_cast<const unsigned*>(xsp[f] + 4 * step);
       }
     }
   };
   if (mine > 0) load_tokens(0, 0);
   if (mine > 1) {
-    load_tokens(1, 1);
+    if constexpr (XB == 2) load_tokens(1, 1);
     fetch(1);
   }
   // window 0 has landed: it was requested first
-  if (mine > 1) wait_vmcnt<2 * kFetch + 2 * kTokenLoads>();
+  if (mine > 1) wait_vmcnt<2 * kFetch + XB * kTokenLoads>();
   else wait_vmcnt<0>();
   __syncthreads();
   v4f acc[kTiles][MF];
@@ -473,8 +501,8 @@ __device__ __forceinline__ void expert_tile(uint8_t* lds, const ExpertArgs& A, c
       for (int h = 0; h < 2; ++h) {
         const int j = jj + h, i = wave + S * j;
         if (j >= mine) break;  // uniform in the wave
-        // the half slice has landed: at least the next one's tokens and W were requested after it
-        if (j + 1 < mine) wait_vmcnt<kTokenLoads + kFetch>();
+        // the half slice has landed: at least the next one's W (and, two ahead, its tokens) was requested after it
+        if (j + 1 < mine) wait_vmcnt<(XB - 1) * kTokenLoads + kFetch>();
         else wait_vmcnt<0>();
         asm volatile("" ::: "memory");
         const uint8_t* wa = ring + (j % kRing) * kHalfBytes + r * kHalf;
@@ -496,9 +524,9 @@ __device__ __forceinline__ void expert_tile(uint8_t* lds, const ExpertArgs& A, c
           if (2 * i + u < steps) {  // uniform
 #pragma unroll
             for (int f = 0; f < MF; ++f) {
-              const v4u x0 = x[h][f][u][0], x1 = x[h][f][u][1];
+              const v4u x0 = x[h % XB][f][u][0], x1 = x[h % XB][f][u][1];
               const v8i B = {(int)x0[0], (int)x0[1], (int)x0[2], (int)x0[3], (int)x1[0], (int)x1[1], (int)x1[2], (int)x1[3]};
-              const int xb = (int)((xs[h][f][u] >> (8 * g)) & 0xFFu) - 4 * term;
+              const int xb = (int)((xs[h % XB][f][u] >> (8 * g)) & 0xFFu) - 4 * col;
 #pragma unroll
               for (int t = 0; t < kTiles; ++t) {
                 const v8i W = {(int)a[u][t][0], (int)a[u][t][1], (int)a[u][t][2], (int)a[u][t][3], 0, 0, 0, 0};
@@ -508,7 +536,7 @@ __device__ __forceinline__ void expert_tile(uint8_t* lds, const ExpertArgs& A, c
             }
           }
         }
-        if (j + 2 < mine) load_tokens(j + 2, h);
+        if (j + XB < mine) load_tokens(j + XB, h);
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the half slice has been read before its slot is refilled
         asm volatile("" ::: "memory");
         if (j + kRing < mine) fetch(j + kRing);
@@ -524,25 +552,18 @@ __device__ __forceinline__ void expert_tile(uint8_t* lds, const ExpertArgs& A, c
   __syncthreads();
   auto sum_of = [&](int t, int f) {
     const uint8_t* at = lds + ((t * MF + f) * 64 + lane) * 16;
-    v4f v = *reinterpret_cast<const v4f*>(at), y;
+    v4f v = *reinterpret_cast<const v4f*>(at);
 #pragma unroll
     for (int w = 1; w < S; ++w) v += *reinterpret_cast<const v4f*>(at + w * (kRing * kHalfBytes));
-    // the three terms of token j are columns 3 j .. 3 j + 2 of a DPP row; lane (3 j, g) ends with features 4 g .. + 3
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int b = __float_as_int(v[i]);
-      y[i] = (v[i] + __int_as_float(__builtin_amdgcn_update_dpp(0, b, 0x101, 0xF, 0xF, false))) +  // row_shl:1
-             __int_as_float(__builtin_amdgcn_update_dpp(0, b, 0x102, 0xF, 0xF, false));             // row_shl:2
-    }
-    return y;
+    return term_sums(v);
   };
   constexpr int kItems = (UP ? 2 : kTiles) * MF;
   for (int q = wave; q < kItems; q += S) {
-    const int t = q / MF, f = q % MF, j = kTokens * f + r / kTerms;
+    const int t = q / MF, f = q % MF, j = kTokens * f + r / kCols;
     const v4f y = sum_of(t, f);
     v4f up = y;
     if constexpr (UP) up = sum_of(t + 2, f);
-    if (term != 0 || r == 15 || j >= n) continue;
+    if (col != 0 || j >= n) continue;
     const size_t pair = pair_of(j0 + j);
     if constexpr (UP) {
       v4f h;
@@ -556,7 +577,7 @@ __device__ __forceinline__ void expert_tile(uint8_t* lds, const ExpertArgs& A, c
 }
 
 template <bool UP, int S>
-__global__ __launch_bounds__(64 * S) void expert_gemm(ExpertArgs A, int tiles) {
+__global__ __launch_bounds__(64 * S) __attribute__((amdgpu_waves_per_eu(2, 8))) void expert_gemm(ExpertArgs A, int tiles) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   const Slot* s = A.slot + blockIdx.x / tiles;
   const int tile = blockIdx.x % tiles, n = s->n;
@@ -564,7 +585,9 @@ __global__ __launch_bounds__(64 * S) void expert_gemm(ExpertArgs A, int tiles) {
     if (j > 0) __syncthreads();  // the sums of the pass before have been read
     const int m = min(n - j, kTokens * kMaxFrags);
     if (m <= kTokens) expert_tile<UP, S, 1>(lds, A, s, tile, j, m);
-    else expert_tile<UP, S, 2>(lds, A, s, tile, j, m);
+    else if (m <= 2 * kTokens) expert_tile<UP, S, 2>(lds, A, s, tile, j, m);
+    else if (m <= 3 * kTokens) expert_tile<UP, S, 3>(lds, A, s, tile, j, m);
+    else expert_tile<UP, S, 4>(lds, A, s, tile, j, m);
   }
 }
 
@@ -588,11 +611,239 @@ hipError_t launch_gemm(const ExpertArgs& A, int slots, int tiles, hipStream_t st
 
 // Two waves a workgroup where there are workgroups enough for four on every CU, eight where K has to be split
 // further to fill the chip (6 of 64 experts of 4096 x 1408, 64 tokens: 151 us with two, 168 with four, 230 with
-// eight; one token, 8 of 128 of 2048 x 768: 25.6, 25.2, 25.1 us).
+// eight).
 template <bool UP>
 hipError_t launch_experts(const ExpertArgs& A, int slots, hipStream_t st) {
   const int tiles = UP ? A.I / 32 : A.D / 64;
   return slots * tiles < 1024 ? launch_gemm<UP, 8>(A, slots, tiles, st) : launch_gemm<UP, 2>(A, slots, tiles, st);
+}
+
+// ---- a few pairs: two launches ------------------------------------------------------------------------------------------
+
+// Where the pairs are few, five launches cost more than the work: here every pair reads its expert's matrices itself, a
+// workgroup of eight waves rotates and splits what it needs of x or of h while its first weights are on their way, and
+// the second launch takes all of a token's experts, so that their weighted sum is y.
+//   UP      workgroup (pair, 16 features of h): item = half slice (256 elements) of D, of the gate and the up rows
+//   not UP  workgroup (token, 16 output features): item = (slot, half slice of I), its product times the slot's weight
+// Items go to the waves in turn. A wave splits the vectors of two or four items at once, 8 lanes (chunks of 32) an item,
+// into its own LDS, and streams each item's 32 or 16 rows x 128 bytes of W through its own ring; a single token's columns
+// are repeated over the instruction's 16. 8 of 128 experts of 2048 x 768, one token: 25 us
+// in five launches, 16 in two; four tokens 41 and 32, eight tokens 56 and 64.
+constexpr int kFewWaves = 8;
+constexpr int kHalfTerms = 256 * kCols;  // bytes of the terms of a half slice
+template <bool UP>
+struct Few {
+  static constexpr int kTiles = UP ? 2 : 1;  // of 16 rows
+  static constexpr int kSlot = kTiles * 2048;
+  static constexpr int kItems = UP ? 2 : 4;     // split at once
+  static constexpr int kWave = kRing * kSlot + kItems * kHalfTerms;  // LDS of a wave
+  static constexpr int kLds = kFewWaves * kWave;
+};
+static_assert(Few<true>::kLds <= 80 * 1024 && Few<false>::kLds <= 80 * 1024, "two workgroups on a CU");
+
+struct FewArgs {
+  const void* v;  // x (bf16) or h (float32)
+  int64_t ld;
+  const int* ids;
+  const float* weights;
+  int k, E, D, I;
+  const uint8_t *wq, *ws;
+  void* out;  // h (float32) or y (bf16)
+};
+
+template <bool UP, int B>
+__device__ __forceinline__ void few_items(uint8_t* lds, const FewArgs& A, int tiles) {
+  constexpr int kTiles = Few<UP>::kTiles, kSlot = Few<UP>::kSlot, kWave = Few<UP>::kWave, kItems = Few<UP>::kItems;
+  const int K = UP ? A.D : A.I;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4, col = r % kCols;
+  const int who = blockIdx.x / tiles, tile = blockIdx.x % tiles;  // pair or token
+  const unsigned KB = (unsigned)K / 2, KS = (unsigned)K / 32;
+  const int steps = K / 128, nhalf = (steps + 1) / 2, items = UP ? nhalf : A.k * nhalf;
+  const int mine = items > wave ? (items - wave + kFewWaves - 1) / kFewWaves : 0;
+  uint8_t* ring = lds + wave * kWave;
+  uint8_t* terms = ring + kRing * kSlot;
+  uint8_t* tscl = terms + term_offset(0, 0, 0, kTerms);  // scale bytes, in an item's unused column
+  auto used = [&](int e) { return e >= 0 && e < A.E; };
+  auto pair_of = [&](int m) { return UP ? who : who * A.k + (wave + kFewWaves * m) / nhalf; };
+  auto half_of = [&](int m) { return UP ? wave + kFewWaves * m : (wave + kFewWaves * m) % nhalf; };
+  auto row0 = [&](int e, int t) {
+    return UP ? (size_t)e * 2 * A.I + t * A.I + 16 * (size_t)tile : (size_t)e * A.D + 16 * (size_t)tile;
+  };
+  using Slot0 = std::integral_constant<int, 0>;
+  using Slot1 = std::integral_constant<int, 1>;
+  static_assert(kRing == 2 && kItems % kRing == 0, "an item's slot goes by its place in the group");
+  unsigned sw[kRing][kTiles][2];
+  // W of item m into ring slot m % kRing (`slot`), its scale bytes to registers: 2 + 2 loads a tile, also for an unused slot, which
+  // reads nothing of W.
+  auto fetch = [&](int m, auto slot) {
+    constexpr int b = decltype(slot)::value;
+    const int id = A.ids[pair_of(m)], i = half_of(m), e = used(id) ? id : 0;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        sw[b][t][u] = *reinterpret_cast<const unsigned*>(A.ws + (row0(e, t) + r) * KS + 4 * min(2 * i + u, steps - 1));
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(A.wq + row0(e, t) * KB, 16u * KB);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int row = 8 * q + (lane >> 3);
+        const unsigned off = (unsigned)row * KB + (unsigned)i * kHalf + 16u * (unsigned)((lane & 7) ^ swz(row));
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(ring + b * kSlot + t * 2048 + q * 1024), 16,
+                                                 used(id) ? off : 0xFFFFFFF0u, 0, 0, 0);
+      }
+    }
+  };
+  constexpr int kFetch = 4 * kTiles;
+
+  v4f acc[kTiles];
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int m0 = 0; m0 < mine; m0 += kItems) {
+    // This lane's chunk: chunk lane % 8 of item m0 + lane / 8. It is requested before the ids are known; the values of
+    // an unused slot's h (whatever lies there) are split too, and go nowhere.
+    const int mi = m0 + (lane >> 3), c = lane & 7;
+    const bool any = (lane >> 3) < kItems && mi < mine;
+    const int pair = pair_of(any ? mi : m0), at = 8 * half_of(any ? mi : m0) + c;
+    const bool split = any && 32 * at < K;  // whole Hadamard blocks: K % 128 == 0
+    float v[32];
+    if (split) {
+      if constexpr (UP) {
+        const v4u* src = reinterpret_cast<const v4u*>(static_cast<const uint16_t*>(A.v) + (pair / A.k) * A.ld + at * 32);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) widen8(src[i], v + 8 * i);
+      } else {
+        const v4f* src = reinterpret_cast<const v4f*>(static_cast<const float*>(A.v) + (size_t)pair * K + at * 32);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const v4f w = src[i];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[4 * i + j] = w[j];
+        }
+      }
+    }
+    if (m0 == 0) {
+      if (UP && !used(A.ids[who])) return;  // the whole workgroup
+      fetch(0, Slot0{});
+      if (mine > 1) fetch(1, Slot1{});
+    }
+    if (split) split_chunk<B>(v, terms + (lane >> 3) * kHalfTerms, c, tscl + (lane >> 3) * kHalfTerms + c);
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the wave's own LDS
+    asm volatile("" ::: "memory");
+    auto item = [&](auto slot, int n) __attribute__((always_inline)) {  // item n of the group
+      constexpr int b = decltype(slot)::value;
+      const int m = m0 + n;
+      if (m >= mine) return;  // uniform in the wave
+      // the item has landed: at most the next one's loads are younger
+      if (m + 1 < mine) wait_vmcnt<kFetch>();
+      else wait_vmcnt<0>();
+      asm volatile("" ::: "memory");
+      if (used(A.ids[pair_of(m)])) {  // uniform in the wave
+        const int i = half_of(m);
+        const float weight = UP ? 1.f : A.weights[pair_of(m)];
+        v4f p[kTiles];
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) p[t] = UP ? acc[t] : v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (2 * i + u < steps) {
+            const uint8_t* xt = terms + n * kHalfTerms;
+            const v4u x0 = *reinterpret_cast<const v4u*>(xt + term_offset(u, 0, g, col));
+            const v4u x1 = *reinterpret_cast<const v4u*>(xt + term_offset(u, 1, g, col));
+            const v8i Bv = {(int)x0[0], (int)x0[1], (int)x0[2], (int)x0[3], (int)x1[0], (int)x1[1], (int)x1[2], (int)x1[3]};
+            const int xb = (int)tscl[n * kHalfTerms + 4 * u + g] - 4 * col;
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+              const v4u a = *reinterpret_cast<const v4u*>(ring + b * kSlot + t * 2048 + r * kHalf +
+                                                          16 * ((4 * u + g) ^ swz(r)));
+              const v8i W = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+              p[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(W, Bv, p[t], 4, 0, 0, (int)(sw[b][t][u] >> (8 * g)), 0, xb);
+            }
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          if constexpr (UP) {
+            acc[t] = p[t];
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[t][j] = __builtin_fmaf(weight, p[t][j], acc[t][j]);
+          }
+        }
+      }
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // the item has been read before its slot is refilled
+      asm volatile("" ::: "memory");
+      if (m + kRing < mine) fetch(m + kRing, slot);
+    };
+#pragma unroll
+    for (int n = 0; n < kItems; n += kRing) {
+      item(Slot0{}, n);
+      item(Slot1{}, n + 1);
+    }
+  }
+  // The waves' sums in their order, then the terms'; lane (0, g) ends with features 4 g .. + 3 of the tile.
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) *reinterpret_cast<v4f*>(ring + t * 1024 + lane * 16) = acc[t];
+  __syncthreads();
+  if (wave != 0) return;
+  auto sum_of = [&](int t) {
+    v4f v = *reinterpret_cast<const v4f*>(lds + t * 1024 + lane * 16);
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w) v += *reinterpret_cast<const v4f*>(lds + w * kWave + t * 1024 + lane * 16);
+    return term_sums(v);
+  };
+  const v4f y = sum_of(0);
+  if constexpr (UP) {
+    const v4f up = sum_of(1);
+    if (r != 0) return;
+    v4f h;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = y[j] / (1.0f + expf(-y[j])) * up[j];
+    *reinterpret_cast<v4f*>(static_cast<float*>(A.out) + (size_t)who * A.I + 16 * tile + 4 * g) = h;
+  } else {
+    if (r != 0) return;
+    unsigned b[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b[j] = __builtin_bit_cast(uint16_t, (__bf16)y[j]);
+    *reinterpret_cast<v2u*>(static_cast<uint16_t*>(A.out) + (size_t)who * A.D + 16 * tile + 4 * g) =
+        v2u{b[0] | b[1] << 16, b[2] | b[3] << 16};
+  }
+}
+
+template <bool UP, int B>
+__global__ __launch_bounds__(kFewWaves * 64) void few_experts(FewArgs A, int tiles) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  few_items<UP, B>(lds, A, tiles);
+}
+
+template <bool UP, int B>
+hipError_t launch_few_block(const FewArgs& A, int blocks, int tiles, hipStream_t st) {
+  static std::atomic<int> ready[64];
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  auto kern = few_experts<UP, B>;
+  const bool cached = dev >= 0 && dev < 64;
+  if (!cached || !ready[dev].load(std::memory_order_acquire)) {
+    e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, Few<UP>::kLds);
+    if (e != hipSuccess) return e;
+    if (cached) ready[dev].store(1, std::memory_order_release);
+  }
+  hipLaunchKernelGGL(kern, dim3((unsigned)(blocks * tiles)), dim3(kFewWaves * 64), Few<UP>::kLds, st, A, tiles);
+  return hipGetLastError();
+}
+
+template <bool UP>
+hipError_t launch_few(int block, const FewArgs& A, int blocks, hipStream_t st) {
+  const int tiles = (UP ? A.I : A.D) / 16;
+  switch (block) {
+    case 16: return launch_few_block<UP, 16>(A, blocks, tiles, st);
+    case 32: return launch_few_block<UP, 32>(A, blocks, tiles, st);
+    case 64: return launch_few_block<UP, 64>(A, blocks, tiles, st);
+    default: return launch_few_block<UP, 128>(A, blocks, tiles, st);
+  }
 }
 
 // y[t][d .. d + 3] = sum over the slots in order of p * out; slots without an expert add nothing.
@@ -661,6 +912,18 @@ hipError_t fp4_launch_moe_experts(const uint16_t* X, int64_t T, int64_t D, int64
   float* out = reinterpret_cast<float*>(ws + FP4_MOE_WS_OUT(T, k, D, I));
   Slot* slot = reinterpret_cast<Slot*>(ws + FP4_MOE_WS_PLAN(T, k, D, I));
   int* list = reinterpret_cast<int*>(slot + pairs);
+  // Two launches that read a pair's matrices for that pair (2.5 TB/s), or five that read those of the used experts once
+  // (24 us and 4.4 TB/s, as fitted to 8 .. 64 pairs of 2048 x 768 and 7168 x 1408), whichever is sooner; the used
+  // experts are guessed as those of evenly spread ids.
+  const double bytes = 1.59 * (double)D * (double)I;  // of an expert
+  const double spread = (double)E * (1.0 - std::pow(1.0 - std::min(1.0, (double)k / (double)E), (double)T));
+  if (pairs * bytes / 2.5e6 < 24.0 + std::min((double)pairs, spread) * bytes / 4.4e6) {
+    const FewArgs up{X, ldx, ids, weights, k, (int)E, (int)D, (int)I, W13q, W13s, h};
+    const hipError_t e = launch_few<true>(block, up, pairs, st);
+    if (e != hipSuccess) return e;
+    const FewArgs down{h, I, ids, weights, k, (int)E, (int)D, (int)I, W2q, W2s, Y};
+    return launch_few<false>(block, down, (int)T, st);
+  }
   const PlanArgs plan{ids, pairs, (int)E, slots, slot, list};
   hipError_t e = launch_split<true>(block, X, ldx, (int)T, (int)D, xq, xs, plan, st);
   if (e != hipSuccess) return e;
