@@ -119,6 +119,44 @@ def _stream(dev):
 
 
 _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_FAST = None
+
+
+class _Fast:
+    """The compiled module's functions, bound to the library's entry points."""
+
+    def __init__(self, module, lib):
+        def bind(function, name):
+            entry = ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+
+            def call(*args):
+                index = torch.cuda.current_device()
+                return function(entry, index, _RAW_STREAM(index), *args)
+            return call
+
+        self.quantize = {name: bind(module.quantize, name) for name in ("fp8_quantize", "fp8_quantize_weights")}
+        self.norm = bind(module.norm, "fp8_add_rmsnorm_quantize")
+        self.linear = bind(module.linear, "fp8_linear")
+        self.route = bind(module.route, "fp4_moe_route")
+        self.experts = bind(module.experts, "fp4_moe_experts")
+
+
+def _fast(t):
+    """The compiled calls (_torch_calls.so) for calls with given outputs on the GPU, where the interpreter's share of
+    a small call counts; None without them. They return a status, or None for operands that they leave to the checks
+    below, which launch or refuse."""
+    global _FAST
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        return None
+    if _FAST is None:
+        lib = load_library()
+        try:
+            from . import _torch_calls
+        except ImportError:
+            _FAST = False
+        else:
+            _FAST = _Fast(_torch_calls, lib) if _RAW_STREAM is not None else False
+    return _FAST or None
 
 
 def _launch(dev, fn, *args):
@@ -152,7 +190,7 @@ def _same_device(name, dev, *tensors):
 
 
 def _check(status: int):
-    if status != 0:
+    if status:
         raise Fp4Error(status, load_library().fp4_last_error().decode())
 
 
@@ -353,6 +391,13 @@ def _rows(t, name, what):
 
 
 def _quantize8(name, x, rows, out):
+    fast = _fast(x) if out is not None else None
+    if fast:
+        codes, scales = out
+        status = fast.quantize[name](x, rows, codes, scales)
+        if status is not None:
+            _check(status)
+            return codes, scales
     lib = load_library()
     M, K, ld = _rows(x, name, "the input")
     shape = (-(-M // rows), K // FP8_GROUP)
@@ -390,6 +435,14 @@ def fp8_add_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual=Non
     ``out`` may pass those four preallocated (None where there is none); h may be the residual itself,
     which is then updated in place."""
     name = "fp8_add_rmsnorm_quantize"
+    fast = _fast(x) if out is not None else None
+    if fast:
+        codes, scales, h, n = out
+        if (h is None) == (residual is None) and (n is None) != bool(normed):
+            status = fast.norm(x, weight, residual, eps, codes, scales, h, n)
+            if status is not None:
+                _check(status)
+                return codes, scales, h, n
     lib = load_library()
     M, K, ld = _rows(x, name, "x")
     dev = x.device
@@ -425,6 +478,12 @@ def fp8_linear(xq, xs, wq, ws, out=None):
     """Y = dq(Xq) dq(Wq)^T, [M, N] in bf16, from the outputs of fp8_quantize (or
     fp8_add_rmsnorm_quantize) and fp8_quantize_weights."""
     name = "fp8_linear"
+    fast = _fast(xq) if out is not None else None
+    if fast:
+        status = fast.linear(xq, xs, wq, ws, out)
+        if status is not None:
+            _check(status)
+            return out
     lib = load_library()
     for t in (xq, wq):
         if not isinstance(t, torch.Tensor) or t.dim() != 2:
@@ -462,11 +521,19 @@ def fp4_moe_route(x: torch.Tensor, router: torch.Tensor, k: int, renormalize: bo
     x bf16 [T, D], router bf16 [E, D]. Of equal weights the lowest expert comes first. ``out`` may pass
     preallocated (ids, weights); workspace: "auto", or a uint8 CUDA tensor of at least 16 T E bytes."""
     name = "fp4_moe_route"
-    lib = load_library()
-    T, D, ld = _rows(x, name, "x")
     if not isinstance(router, torch.Tensor) or router.dim() != 2:
         raise ValueError(f"{name}: router must be a 2-D tensor")
     E, k = router.shape[0], int(k)
+    fast = _fast(x) if out is not None else None
+    if fast:
+        ids, weights = out
+        ws = _workspace(workspace, 16 * x.shape[0] * E, name, x.device)
+        status = fast.route(x, router, k, bool(renormalize), ids, weights, ws)
+        if status is not None:
+            _check(status)
+            return ids, weights
+    lib = load_library()
+    T, D, ld = _rows(x, name, "x")
     _expect(router, (E, D), torch.bfloat16, name, "router")
     if out is None:
         ids = torch.empty((T, k), dtype=torch.int32, device=x.device)
@@ -500,6 +567,14 @@ def fp4_moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w
     [E, 2I, D/32], gate rows first, w2q [E, D, I/2] and w2s [E, D, I/32]. workspace: "auto", or a uint8 CUDA
     tensor of at least moe_workspace_bytes(T, k, D, I)."""
     name = "fp4_moe_experts"
+    fast = _fast(x) if out is not None else None
+    if fast and isinstance(ids, torch.Tensor) and isinstance(w2q, torch.Tensor) and \
+            x.dim() == ids.dim() == 2 and w2q.dim() == 3:
+        ws = _workspace(workspace, moe_workspace_bytes(*ids.shape, x.shape[1], 2 * w2q.shape[2]), name, x.device)
+        status = fast.experts(x, ids, weights, w13q, w13s, w2q, w2s, block, out, ws)
+        if status is not None:
+            _check(status)
+            return out
     lib = load_library()
     T, D, ld = _rows(x, name, "x")
     for t, what in ((w13q, "w13q"), (w2q, "w2q")):

@@ -3,7 +3,8 @@
 Usage: python -m microscaling_fp4_quantized_amd.build   (or build() from Python)
 
 Compiles every source under csrc/ to an object in _build/ (in parallel) and links
-the shared library next to this file. Always recompiles.
+the shared library next to this file, and with it _torch_calls.so, the host-only
+module that enters the library from torch tensors. Always recompiles.
 """
 from __future__ import annotations
 
@@ -12,12 +13,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfp4.so")
+CALLS = os.path.join(HERE, "_torch_calls.so")
 
 SOURCES = [
     "rotate_quant.hip",
@@ -70,10 +73,33 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_calls() -> str:
+    """_torch_calls.so against the installed torch's headers (host code only)."""
+    import torch
+    from torch.utils import cpp_extension
+
+    cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        raise RuntimeError("no host C++ compiler found")
+    tmp = CALLS + ".tmp"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-isystem{d}" for d in cpp_extension.include_paths()), f"-isystem{sysconfig.get_paths()['include']}",
+           os.path.join(CSRC, "torch_calls.cpp"), "-o", tmp,
+           *(f"-L{d}" for d in cpp_extension.library_paths()), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"host compiler failed on torch_calls.cpp:\n{r.stdout}{r.stderr}")
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(verbose: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(4, len(SOURCES))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=5) as ex:
+        calls = ex.submit(_build_calls)
         objs = list(ex.map(_compile, SOURCES))
+        calls.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -81,7 +107,7 @@ def build(verbose: bool = True) -> str:
         raise RuntimeError(f"link failed:\n{r.stdout}{r.stderr}")
     os.replace(tmp, LIB)
     if verbose:
-        print(f"built {LIB}")
+        print(f"built {LIB} and {os.path.basename(CALLS)}")
     return LIB
 
 
