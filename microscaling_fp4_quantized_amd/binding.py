@@ -525,7 +525,7 @@ def fp4_moe_route(x: torch.Tensor, router: torch.Tensor, k: int, renormalize: bo
         raise ValueError(f"{name}: router must be a 2-D tensor")
     E, k = router.shape[0], int(k)
     fast = _fast(x) if out is not None else None
-    if fast:
+    if fast and x.dim() == 2:
         ids, weights = out
         ws = _workspace(workspace, 16 * x.shape[0] * E, name, x.device)
         status = fast.route(x, router, k, bool(renormalize), ids, weights, ws)

@@ -131,6 +131,43 @@ def test_experts(T, E, D, I, k, block):
     check_experts(T, E, D, I, k, block, more=8 * (T % 3))
 
 
+# Work enough that pairs are sorted by expert and an expert's matrices are read once for all of its tokens (at least 75 MB
+# if every pair read its own): one token an expert to all of them on one; rows of scales longer than LDS holds at
+# once; K of whole and of half slices; enough tiles for small workgroups in one product, the other and neither
+SORTED = [(128, 16, 256, 128, 16, 32), (128, 16, 128, 256, 16, 16), (100, 20, 384, 640, 8, 64),
+          (64, 16, 1152, 128, 8, 128), (37, 9, 4224, 128, 7, 32), (19, 5, 128, 4352, 5, 64), (50, 12, 7168, 256, 3, 128),
+          (24, 3, 8320, 128, 3, 16), (12, 4, 1408, 1408, 2, 128), (128, 60, 640, 256, 3, 64), (90, 32, 256, 1024, 5, 32),
+          (128, 64, 1024, 128, 4, 64)]
+
+
+@pytest.mark.parametrize("T,E,D,I,k,block", SORTED)
+def test_experts_sorted(T, E, D, I, k, block):
+    check_experts(T, E, D, I, k, block, more=8 * (T % 3))
+
+
+def test_experts_sorted_all_tokens_on_one_expert_of_many():
+    check_experts(128, 120, 2048, 128, 2, 32, ids=np.full((128, 2), 119))
+
+
+def test_experts_sorted_unused_slots_and_non_finite_tokens():
+    T, E, D, k = 96, 8, 1024, 6
+    rng = np.random.default_rng(12)
+    ids = rng.integers(-3, E + 2, (T, k))
+    ids[5] = -1
+    x = bf16(rng.standard_normal((T, D)))
+    args, y = check_experts(T, E, D, 256, k, 32, ids=ids, x=x)
+    assert (y[5] == 0).all()
+    sick = x.clone()
+    ids[[7, 40], 0] = 0
+    sick[7, 100] = float("nan")
+    sick[40, 900] = -float("inf")
+    _, y, _ = run_experts(T, E, D, 256, k, 32, ids=ids, x=x)
+    _, z, _ = run_experts(T, E, D, 256, k, 32, ids=ids, x=sick)
+    assert torch.isnan(z[[7, 40]]).all()
+    rest = [t for t in range(T) if t not in (7, 40)]
+    assert torch.equal(z[rest].view(torch.int16), y[rest].view(torch.int16))
+
+
 def test_experts_unused_slots_and_repeated_experts():
     ids = np.array([[-1, -1, -1], [2, 2, 2], [0, -1, 0], [5, 7, 1 << 30], [-5, 3, 4], [1, 0, 1]])
     args, y = check_experts(6, 5, 256, 128, 3, 32, ids=ids)
