@@ -9,6 +9,7 @@
 
 #include "../../include/fp4.h"
 #include "common.hpp"
+#include "operators.hpp"
 
 namespace {
 

@@ -9,7 +9,7 @@
 // scale infinity (codes 0, and NaN at the infinity), so no group comes out finite that was not.
 #pragma once
 
-#include "common.hpp"
+#include "operators.hpp"
 
 namespace fp4 {
 
