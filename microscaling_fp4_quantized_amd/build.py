@@ -30,7 +30,7 @@ SOURCES = [
     "gemm_nvfp4.hip",
     "gemm_nvfp4_ring.hip",
     "fp8_quant.hip",
-    "gemm_fp8_decode.hip",
+    "gemm_fp8_split.hip",
     "gemm_fp8_ring.hip",
     "moe.hip",
     "fp4_abi.cpp",

@@ -47,7 +47,6 @@ struct Tile {
   static_assert((NS - 2) * KB * (A_WL + B_WL + 1) < 64, "the ring's loads in flight can be counted");
   static_assert(NS >= 2 && LDS <= 160 * 1024, "the ring fits");
 };
-using T32 = Tile<32, 32, 2, 2, 4, 4>;
 using T64 = Tile<64, 64, 4, 2, 4, 2>;
 using T128x64 = Tile<128, 64, 4, 2, 3, 2>;
 using T128 = Tile<128, 128, 4, 2, 2, 2>;     // one workgroup on a CU
@@ -495,7 +494,7 @@ hipError_t launch(const uint8_t* Xq, const float* Xs, const uint8_t* Wq, const f
     if (e != hipSuccess) return e;
     if (cached) ready[dev].store(1, std::memory_order_release);
   }
-  const int tiles_m = (M + C::BM - 1) / C::BM, tiles_n = (N + C::BN - 1) / C::BN;
+  const int tiles_m = (M - 1) / C::BM + 1, tiles_n = (N - 1) / C::BN + 1;
   hipLaunchKernelGGL(kern, dim3((unsigned)(tiles_m * tiles_n)), dim3(C::NT), C::LDS, st, Xq, Xs, Wq, Ws, Y, M, N, K,
                      tiles_m, tiles_n);
   return hipGetLastError();
@@ -511,31 +510,41 @@ hipError_t launch_turns(const uint8_t* Xq, const float* Xs, const uint8_t* Wq, c
     if (e != hipSuccess) return e;
     if (cached) ready[dev].store(1, std::memory_order_release);
   }
-  const int tiles_m = (M + PBM - 1) / PBM, tiles_n = (N + PBN - 1) / PBN;
+  const int tiles_m = (M - 1) / PBM + 1, tiles_n = (N - 1) / PBN + 1;
   hipLaunchKernelGGL(gemm_fp8_turns, dim3((unsigned)(tiles_m * tiles_n)), dim3(512), P_LDS, st, Xq, Xs, Wq, Ws, Y, M, N, K,
                      tiles_m, tiles_n);
   return hipGetLastError();
 }
 
 // The tile shapes: rows of X, rows of W, workgroups that run at once on a CU, and the time of one scale block of K in us
-// (one round of workgroups at K = 4096, the launch taken off). The least rounds times a round's time is taken:
-//   rows x N (K 4096)   32 x 32   64 x 64   128 x 64   128 x 128   the same, two a CU   256 x 256   (us)
-//   64 x 4096               9.2      11.6       15.2        20.6                 24.7        37
-//   64 x 14336             30.8      12.8       16.3        21.5                 25.6        37
-//   100 x 14336            49.8      21.8       16.5        23.7                 28.4        39
-//   200 x 14336            92.5      40.2       31.0        24.5                 28.9        39
-//   300 x 14336             126      51.3       43.4        42.3                 32.1        41
-//   1024 x 14336            390       137        108        93.4                 71.4        53
+// (one round of workgroups at K = 4096, the launch taken off). The least rounds times a round's time is taken; up
+// to 8 rows of X, which cost little beside W, go to 16 x 16. The first three split K over the waves of a workgroup
+// (gemm_fp8_split.hip); several of their workgroups run on a CU, sharing what it reads.
+//   rows x N (K 4096)   16 x 16   16 x 32   32 x 32   64 x 64   128 x 64   128 x 128   the same, two a CU   256 x 256   (us)
+//   1 x 14336              10.7      10.6      10.9      12.1
+//   16 x 4096               5.2       5.3       5.9
+//   37 x 4100               8.0       7.2       8.7      12.1
+//   64 x 4096               8.6       7.4       6.5      11.6       15.2        20.6                 24.7        37
+//   128 x 4096             14.1      11.4       9.5      11.8
+//   64 x 14336                       24.7      16.3      12.8       16.3        21.5                 25.6        37
+//   100 x 14336                                          21.8       16.5        23.7                 28.4        39
+//   200 x 14336                                          40.2       31.0        24.5                 28.9        39
+//   300 x 14336                                          51.3       43.4        42.3                 32.1        41
+//   1024 x 14336                                          137        108        93.4                 71.4        53
+//   K 8192: 1 x 28672      40.5      43.3      41.3
+//   8 x 28672              41.9      45.1      43.4
+//   16 x 28672             48.3      44.9      43.7
 struct Shape {
   int bm, bn, per_cu;
   float cost;
 };
-constexpr Shape kShapes[] = {{32, 32, 1, 0.17f}, {64, 64, 1, 0.26f}, {128, 64, 1, 0.41f},
-                             {128, 128, 1, 0.65f}, {128, 128, 2, 1.16f}, {256, 256, 1, 1.27f}};
+constexpr Shape kShapes[] = {{16, 16, 1, 0.047f}, {16, 32, 1, 0.061f}, {32, 32, 1, 0.095f}, {64, 64, 1, 0.26f},
+                             {128, 64, 1, 0.41f}, {128, 128, 1, 0.65f}, {128, 128, 2, 1.16f}, {256, 256, 1, 1.27f}};
 
 int best_shape(int64_t M, int64_t N, int64_t K, int cus) {
   int best = 0;
   double least = 0;
+  if (M <= 8) return 0;
   for (int i = 0; i < (int)(sizeof kShapes / sizeof kShapes[0]); ++i) {
     const Shape& s = kShapes[i];
     if (s.bm == PBM && K < 512) break;
@@ -549,15 +558,22 @@ int best_shape(int64_t M, int64_t N, int64_t K, int cus) {
 }  // namespace
 }  // namespace fp4
 
-hipError_t fp8_launch_linear_ring(const uint8_t* Xq, const float* Xs, const uint8_t* Wq, const float* Ws, int64_t M,
-                                  int64_t N, int64_t K, uint16_t* Y, int dev, int cus, hipStream_t st) {
-  const int m = (int)M, n = (int)N, k = (int)K;
-  switch (fp4::best_shape(M, N, K, cus)) {
-    case 0: return fp4::launch<fp4::T32>(Xq, Xs, Wq, Ws, m, n, k, Y, dev, st);
-    case 1: return fp4::launch<fp4::T64>(Xq, Xs, Wq, Ws, m, n, k, Y, dev, st);
-    case 2: return fp4::launch<fp4::T128x64>(Xq, Xs, Wq, Ws, m, n, k, Y, dev, st);
-    case 3: return fp4::launch<fp4::T128>(Xq, Xs, Wq, Ws, m, n, k, Y, dev, st);
-    case 4: return fp4::launch<fp4::T128Two>(Xq, Xs, Wq, Ws, m, n, k, Y, dev, st);
+hipError_t fp8_launch_linear(const uint8_t* Xq, const float* Xs, const uint8_t* Wq, const float* Ws, int64_t M, int64_t N,
+                             int64_t K, uint16_t* Y, hipStream_t st) {
+  int dev = 0, cus = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e == hipSuccess) e = fp4_device_cus(dev, &cus);
+  if (e != hipSuccess) return e;
+  const int m = (int)M, n = (int)N, k = (int)K, shape = fp4::best_shape(M, N, K, cus);
+  switch (shape) {
+    case 0:
+    case 1:
+    case 2:
+      return fp8_launch_linear_split(fp4::kShapes[shape].bm, fp4::kShapes[shape].bn, Xq, Xs, Wq, Ws, M, N, K, Y, dev, st);
+    case 3: return fp4::launch<fp4::T64>(Xq, Xs, Wq, Ws, m, n, k, Y, dev, st);
+    case 4: return fp4::launch<fp4::T128x64>(Xq, Xs, Wq, Ws, m, n, k, Y, dev, st);
+    case 5: return fp4::launch<fp4::T128>(Xq, Xs, Wq, Ws, m, n, k, Y, dev, st);
+    case 6: return fp4::launch<fp4::T128Two>(Xq, Xs, Wq, Ws, m, n, k, Y, dev, st);
     default: return fp4::launch_turns(Xq, Xs, Wq, Ws, m, n, k, Y, dev, st);
   }
 }

@@ -14,8 +14,8 @@ hipError_t fp8_launch_add_rmsnorm_quantize(const uint16_t* X, int64_t M, int64_t
                                            uint16_t* H, uint16_t* Y, hipStream_t stream);
 hipError_t fp8_launch_linear(const uint8_t* Xq, const float* Xs, const uint8_t* Wq, const float* Ws, int64_t M,
                              int64_t N, int64_t K, uint16_t* Y, hipStream_t stream);
-hipError_t fp8_launch_linear_ring(const uint8_t* Xq, const float* Xs, const uint8_t* Wq, const float* Ws, int64_t M,
-                                  int64_t N, int64_t K, uint16_t* Y, int dev, int cus, hipStream_t stream);
+hipError_t fp8_launch_linear_split(int bm, int bn, const uint8_t* Xq, const float* Xs, const uint8_t* Wq, const float* Ws,
+                                   int64_t M, int64_t N, int64_t K, uint16_t* Y, int dev, hipStream_t stream);
 
 // Mixture of experts for a few tokens.
 hipError_t fp4_launch_moe_route(const uint16_t* X, int64_t T, int64_t D, int64_t ldx, const uint16_t* Wr, int64_t E, int k,

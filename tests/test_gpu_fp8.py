@@ -185,6 +185,17 @@ def test_linear(M, N, K):
     check_linear(M, N, K)
 
 
+# the small tiles, whose waves split K: 16 x 16 (up to 8 rows, or few features), 16 x 32 and 32 x 32, ragged, with
+# fewer blocks of K than waves, and rows of W and X that end inside a tile of several
+SPLIT = [(8, 4101, 8320), (7, 31, 256), (8, 33, 384), (9, 8, 640), (40, 15, 8448), (250, 13, 1152), (9, 4100, 128), (17, 4101, 4224),
+         (33, 2047, 640), (60, 4000, 640), (64, 4090, 8320), (33, 4096, 128), (50, 4095, 256), (200, 2050, 1408)]
+
+
+@pytest.mark.parametrize("M,N,K", SPLIT)
+def test_linear_small_tiles(M, N, K):
+    check_linear(M, N, K)
+
+
 def test_linear_non_finite_stay_in_their_rows():
     xq, xs, wq, ws = random_operands(np.random.default_rng(5), 20, 200, 384)
     xs[3, 1] = float("nan")
