@@ -61,6 +61,15 @@ __device__ __forceinline__ void widen8(v4u w, float* v) {
   }
 }
 
+// Four.
+__device__ __forceinline__ void widen4(v2u w, float v[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    v[2 * i] = bf16_lo(w[i]);
+    v[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+
 // Eight float32 values -> bf16 (round to nearest even).
 __device__ __forceinline__ v4u narrow8(const float* v) {
   v4u w;

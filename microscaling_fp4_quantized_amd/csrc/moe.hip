@@ -197,47 +197,80 @@ __device__ __forceinline__ int term_offset(int step, int half, int g, int c) {
   return ((step * 2 + half) * 4 + g) * (kCols * 16) + c * 16;
 }
 
-// Rotate chunk `at` of 32 values of a row (part of its Hadamard block, see fwht) and write its terms and its E8M0
-// code. The code puts the chunk's largest magnitude into (224, 448], and is at least 12, so that the columns'
-// codes, 4 less each, stay codes. A chunk that is not finite gets NaN terms.
+// The value of lane l ^ X, X = 1, 2, 4, 8 or 16.
+template <int X>
+__device__ __forceinline__ unsigned lane_xor(unsigned v) {
+  if constexpr (X == 1) return __builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false);  // quad_perm 1 0 3 2
+  if constexpr (X == 2) return __builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false);  // quad_perm 2 3 0 1
+  if constexpr (X == 4) {  // ^ 7, then ^ 3
+    const int w = __builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false);  // row_half_mirror
+    return __builtin_amdgcn_update_dpp(0, w, 0x1B, 0xF, 0xF, false);               // quad_perm 3 2 1 0
+  }
+  if constexpr (X == 8) return __builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, false);  // row_ror:8
+  return __builtin_amdgcn_ds_swizzle((int)v, 0x401F);
+}
+
+// A butterfly stage over lanes: the lower lane keeps the sum, the upper one the lower's value minus its own.
+template <int X>
+__device__ __forceinline__ void butterfly(float v[4], int lane) {
+  const unsigned flip = lane & X ? 0x80000000u : 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = __uint_as_float(lane_xor<X>(__float_as_uint(v[i]))) + __uint_as_float(__float_as_uint(v[i]) ^ flip);
+}
+
+// Rotate 256 values, 4 l .. 4 l + 3 of them in lane l, and split them: lane l returns the 16 bytes of term l % 4 (zeros
+// for the fourth) of values 16 (l / 4) .. + 15, which belong at byte 16 l of the 1 KB that term_offset gives them, and
+// the E8M0 code of its chunk of 32 values. The code puts the chunk's largest magnitude into (224, 448], and is at
+// least 12, so that the columns' codes, 4 less each, stay codes. A chunk that is not finite gets NaN terms.
+// Four values a lane keep all 64 lanes at work where a wave has one such piece (a chunk of 32 a lane, eight lanes
+// of 64, took 31.8 us for 4 tokens of 8 of 128 experts of 2048 x 768, this 25.1).
+// The lanes of a half wave (128 values) take part together.
 template <int B>
-__device__ __forceinline__ void split_chunk(float v[32], uint8_t* row, int at, uint8_t* scale) {
-  fwht<B>(v);
+__device__ __forceinline__ v4u split_terms(float v[4], int lane, uint8_t& scale) {
+  const float s0 = v[0] + v[1], s1 = v[0] - v[1], s2 = v[2] + v[3], s3 = v[2] - v[3];
+  v[0] = s0 + s2, v[1] = s1 + s3, v[2] = s0 - s2, v[3] = s1 - s3;
+  butterfly<1>(v, lane);
+  butterfly<2>(v, lane);
+  if constexpr (B >= 32) butterfly<4>(v, lane);
+  if constexpr (B >= 64) butterfly<8>(v, lane);
+  if constexpr (B >= 128) butterfly<16>(v, lane);
   const float c = __uint_as_float(hadamard_constant_bits(B));
   unsigned m = 0;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
+  for (int i = 0; i < 4; ++i) {
     v[i] *= c;
     m = max(m, abs_bits(v[i]));
   }
+  m = max(m, lane_xor<1>(m));
+  m = max(m, lane_xor<2>(m));
+  m = max(m, lane_xor<4>(m));
   // |max| = 1.f * 2^(e - 127); 448 = 1.75 * 2^8
   const int e = (int)(m >> 23) - 8 + ((m & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   const int code = e < 12 ? 12 : e;
   const bool finite = m < 0x7F800000u;
   const float inv = __uint_as_float((unsigned)(254 - code) << 23);  // 2^(127 - code), code <= 247
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] *= inv;
-  const int step = at >> 2, half = (at >> 1) & 1, g = 2 * (at & 1);
+  for (int i = 0; i < 4; ++i) v[i] *= inv;
+  unsigned w[kCols] = {0, 0, 0, 0};
 #pragma unroll
-  for (int t = 0; t < kCols; ++t) {
-    unsigned w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (t < kTerms) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        int b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i], v[4 * i + 1], 0, false);
-        b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2], v[4 * i + 3], b, true);
-        const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8(b, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(b, true);
-        v[4 * i] = (v[4 * i] - lo[0]) * 16.f;
-        v[4 * i + 1] = (v[4 * i + 1] - lo[1]) * 16.f;
-        v[4 * i + 2] = (v[4 * i + 2] - hi[0]) * 16.f;
-        v[4 * i + 3] = (v[4 * i + 3] - hi[1]) * 16.f;
-        w[i] = finite ? (unsigned)b : 0x7F7F7F7Fu;
-      }
-    }
-    *reinterpret_cast<v4u*>(row + term_offset(step, half, g, t)) = v4u{w[0], w[1], w[2], w[3]};
-    *reinterpret_cast<v4u*>(row + term_offset(step, half, g + 1, t)) = v4u{w[4], w[5], w[6], w[7]};
+  for (int t = 0; t < kTerms; ++t) {
+    int b = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+    b = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], b, true);
+    const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8(b, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(b, true);
+    v[0] = (v[0] - lo[0]) * 16.f;
+    v[1] = (v[1] - lo[1]) * 16.f;
+    v[2] = (v[2] - hi[0]) * 16.f;
+    v[3] = (v[3] - hi[1]) * 16.f;
+    w[t] = finite ? (unsigned)b : 0x7F7F7F7Fu;
   }
-  *scale = (uint8_t)(finite ? code : 127);
+  scale = (uint8_t)(finite ? code : 127);
+  // transpose over the quad: lane q has word t of its four values, and wants term q of the quad's sixteen
+  const bool odd = lane & 1, upper = lane & 2;
+  const unsigned r0 = lane_xor<1>(odd ? w[0] : w[1]), r1 = lane_xor<1>(odd ? w[2] : w[3]);
+  const unsigned a0 = odd ? r0 : w[0], a1 = odd ? w[1] : r0, b0 = odd ? r1 : w[2], b1 = odd ? w[3] : r1;
+  const unsigned c0 = lane_xor<2>(upper ? a0 : b0), c1 = lane_xor<2>(upper ? a1 : b1);
+  return upper ? v4u{c0, c1, b0, b1} : v4u{a0, a1, c0, c1};
 }
 
 // Sort the pairs by expert: one workgroup of 256 threads. Ids outside [0, E) name no expert. The order of an
@@ -307,34 +340,30 @@ struct PlanArgs {
   int* list;
 };
 
-// Rows of `cpr` chunks of 32 values -> terms (4 * 32 cpr bytes a row) and scales [row][cpr]; one lane a chunk. The
-// 2 or 4 chunks of a Hadamard block of 64 or 128 sit in adjacent lanes (cpr % 4 == 0). With PLAN, the first
-// workgroup sorts the pairs instead.
+// Rows of `quads` groups of 4 values -> terms (16 bytes a group) and scales [row][quads / 8], a group a lane. A row is
+// whole half waves (K % 128 == 0). With PLAN, the first workgroup sorts the pairs instead.
 template <int B, bool PLAN>
-__global__ __launch_bounds__(256) void split_rows(const void* __restrict__ V, int64_t ld, int rows, int cpr,
+__global__ __launch_bounds__(256) void split_rows(const void* __restrict__ V, int64_t ld, int rows, int quads,
                                                   uint8_t* __restrict__ q, uint8_t* __restrict__ scales, PlanArgs P) {
   if (PLAN && blockIdx.x == 0) {
     plan_experts(P.ids, P.pairs, P.E, P.slots, P.slot, P.list);
     return;
   }
-  const int c = (blockIdx.x - (PLAN ? 1 : 0)) * 256 + threadIdx.x;
-  if (c >= rows * cpr) return;  // whole quads: rows * cpr % 4 == 0
-  const int row = c / cpr, at = c - row * cpr;
-  float v[32];
+  const unsigned c = (blockIdx.x - (PLAN ? 1 : 0)) * 256 + threadIdx.x;
+  if (c >= (unsigned)rows * quads) return;
+  const unsigned row = c / quads, at = c - row * quads;
+  float v[4];
   if constexpr (!PLAN) {  // h, float32
-    const v4f* p = reinterpret_cast<const v4f*>(reinterpret_cast<const float*>(V) + row * ld + at * 32);
+    const v4f w = *reinterpret_cast<const v4f*>(reinterpret_cast<const float*>(V) + row * ld + at * 4);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const v4f w = p[i];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[4 * i + j] = w[j];
-    }
+    for (int i = 0; i < 4; ++i) v[i] = w[i];
   } else {  // x, bf16
-    const v4u* p = reinterpret_cast<const v4u*>(reinterpret_cast<const uint16_t*>(V) + row * ld + at * 32);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) widen8(p[i], v + 8 * i);
+    widen4(*reinterpret_cast<const v2u*>(reinterpret_cast<const uint16_t*>(V) + row * ld + at * 4), v);
   }
-  split_chunk<B>(v, q + (size_t)row * cpr * (32 * kCols), at, scales + c);
+  uint8_t scale;
+  const v4u terms = split_terms<B>(v, threadIdx.x & 63, scale);
+  *reinterpret_cast<v4u*>(q + (size_t)c * 16) = terms;
+  if (threadIdx.x % 8 == 0) scales[c / 8] = scale;
 }
 
 // The three terms of token j are columns 4 j .. 4 j + 2 of a DPP row: lane (4 j, g) ends with their sums for features
@@ -625,10 +654,10 @@ hipError_t launch_experts(const ExpertArgs& A, int slots, hipStream_t st) {
 // the second launch takes all of a token's experts, so that their weighted sum is y.
 //   UP      workgroup (pair, 16 features of h): item = half slice (256 elements) of D, of the gate and the up rows
 //   not UP  workgroup (token, 16 output features): item = (slot, half slice of I), its product times the slot's weight
-// Items go to the waves in turn. A wave splits the vectors of two or four items at once, 8 lanes (chunks of 32) an item,
+// Items go to the waves in turn. A wave splits the vectors of two or four items at a time
 // into its own LDS, and streams each item's 32 or 16 rows x 128 bytes of W through its own ring; a single token's columns
 // are repeated over the instruction's 16. 8 of 128 experts of 2048 x 768, one token: 25 us
-// in five launches, 16 in two; four tokens 41 and 32, eight tokens 56 and 64.
+// in five launches, 15 in two; four tokens 41 and 25, eight tokens 47 and 50. 16 waves for the second launch: no faster.
 constexpr int kFewWaves = 8;
 constexpr int kHalfTerms = 256 * kCols;  // bytes of the terms of a half slice
 template <bool UP>
@@ -702,34 +731,34 @@ __device__ __forceinline__ void few_items(uint8_t* lds, const FewArgs& A, int ti
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
   for (int m0 = 0; m0 < mine; m0 += kItems) {
-    // This lane's chunk: chunk lane % 8 of item m0 + lane / 8. It is requested before the ids are known; the values of
-    // an unused slot's h (whatever lies there) are split too, and go nowhere.
-    const int mi = m0 + (lane >> 3), c = lane & 7;
-    const bool any = (lane >> 3) < kItems && mi < mine;
-    const int pair = pair_of(any ? mi : m0), at = 8 * half_of(any ? mi : m0) + c;
-    const bool split = any && 32 * at < K;  // whole Hadamard blocks: K % 128 == 0
-    float v[32];
-    if (split) {
-      if constexpr (UP) {
-        const v4u* src = reinterpret_cast<const v4u*>(static_cast<const uint16_t*>(A.v) + (pair / A.k) * A.ld + at * 32);
+    // The items' values are requested before the ids are known; those of an unused slot's h (whatever lies there) and
+    // those past K (of an odd number of steps; the row's last) are split too, and go nowhere.
+    typename std::conditional<UP, v2u, v4f>::type raw[kItems];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) widen8(src[i], v + 8 * i);
-      } else {
-        const v4f* src = reinterpret_cast<const v4f*>(static_cast<const float*>(A.v) + (size_t)pair * K + at * 32);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const v4f w = src[i];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[4 * i + j] = w[j];
-        }
-      }
+    for (int n = 0; n < kItems; ++n) {
+      const int m = min(m0 + n, mine - 1), pair = pair_of(m), at = min(256 * half_of(m) + 4 * lane, K - 4);
+      if constexpr (UP) raw[n] = *reinterpret_cast<const v2u*>(static_cast<const uint16_t*>(A.v) + (pair / A.k) * A.ld + at);
+      else raw[n] = *reinterpret_cast<const v4f*>(static_cast<const float*>(A.v) + (size_t)pair * K + at);
     }
     if (m0 == 0) {
       if (UP && !used(A.ids[who])) return;  // the whole workgroup
       fetch(0, Slot0{});
       if (mine > 1) fetch(1, Slot1{});
     }
-    if (split) split_chunk<B>(v, terms + (lane >> 3) * kHalfTerms, c, tscl + (lane >> 3) * kHalfTerms + c);
+#pragma unroll
+    for (int n = 0; n < kItems; ++n) {
+      if (m0 + n >= mine) break;  // uniform in the wave
+      float v[4];
+      if constexpr (UP) {
+        widen4(raw[n], v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = raw[n][j];
+      }
+      uint8_t scale;
+      *reinterpret_cast<v4u*>(terms + n * kHalfTerms + lane * 16) = split_terms<B>(v, lane, scale);
+      if (lane % 8 == 0) tscl[n * kHalfTerms + lane / 8] = scale;
+    }
     __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the wave's own LDS
     asm volatile("" ::: "memory");
     auto item = [&](auto slot, int n) __attribute__((always_inline)) {  // item n of the group
@@ -846,7 +875,9 @@ hipError_t launch_few(int block, const FewArgs& A, int blocks, hipStream_t st) {
   }
 }
 
-// y[t][d .. d + 3] = sum over the slots in order of p * out; slots without an expert add nothing.
+// y[t][d .. d + 3] = sum over the slots in order of p * out, four slots' loads in flight at once; slots without an expert
+// add nothing.
+constexpr int kCombine = 4;
 __global__ __launch_bounds__(256) void combine(const int* __restrict__ ids, const float* __restrict__ p,
                                                const float* __restrict__ out, int T, int k, int E, int D,
                                                uint16_t* __restrict__ Y) {
@@ -854,13 +885,23 @@ __global__ __launch_bounds__(256) void combine(const int* __restrict__ ids, cons
   if (i >= (int64_t)T * (D / 4)) return;
   const int t = (int)(i / (D / 4)), d = (int)(i % (D / 4)) * 4;
   v4f y = {0.f, 0.f, 0.f, 0.f};
-  for (int j = 0; j < k; ++j) {
-    const int pair = t * k + j, e = ids[pair];
-    if (e < 0 || e >= E) continue;
-    const v4f o = *reinterpret_cast<const v4f*>(out + (size_t)pair * D + d);
-    const float w = p[pair];
+  for (int j0 = 0; j0 < k; j0 += kCombine) {
+    int e[kCombine];
+    float w[kCombine];
+    v4f o[kCombine];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) y[q] = __builtin_fmaf(w, o[q], y[q]);
+    for (int j = 0; j < kCombine; ++j) {
+      const int pair = t * k + min(j0 + j, k - 1);
+      e[j] = ids[pair];
+      w[j] = p[pair];
+      o[j] = *reinterpret_cast<const v4f*>(out + (size_t)pair * D + d);  // of an unused slot: whatever lies there
+    }
+#pragma unroll
+    for (int j = 0; j < kCombine; ++j) {
+      const bool used = j0 + j < k && e[j] >= 0 && e[j] < E;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) y[q] = used ? __builtin_fmaf(w[j], o[j][q], y[q]) : y[q];
+    }
   }
   unsigned b[4];
 #pragma unroll
@@ -871,13 +912,13 @@ __global__ __launch_bounds__(256) void combine(const int* __restrict__ ids, cons
 template <bool PLAN>
 hipError_t launch_split(int block, const void* V, int64_t ld, int rows, int K, uint8_t* q, uint8_t* s, const PlanArgs& P,
                         hipStream_t st) {
-  const int cpr = K / 32;
-  const dim3 grid((unsigned)(((int64_t)rows * cpr + 255) / 256 + (PLAN ? 1 : 0)));
+  const int quads = K / 4;
+  const dim3 grid((unsigned)(((int64_t)rows * quads + 255) / 256 + (PLAN ? 1 : 0)));
   switch (block) {
-    case 16: hipLaunchKernelGGL((split_rows<16, PLAN>), grid, dim3(256), 0, st, V, ld, rows, cpr, q, s, P); break;
-    case 32: hipLaunchKernelGGL((split_rows<32, PLAN>), grid, dim3(256), 0, st, V, ld, rows, cpr, q, s, P); break;
-    case 64: hipLaunchKernelGGL((split_rows<64, PLAN>), grid, dim3(256), 0, st, V, ld, rows, cpr, q, s, P); break;
-    default: hipLaunchKernelGGL((split_rows<128, PLAN>), grid, dim3(256), 0, st, V, ld, rows, cpr, q, s, P);
+    case 16: hipLaunchKernelGGL((split_rows<16, PLAN>), grid, dim3(256), 0, st, V, ld, rows, quads, q, s, P); break;
+    case 32: hipLaunchKernelGGL((split_rows<32, PLAN>), grid, dim3(256), 0, st, V, ld, rows, quads, q, s, P); break;
+    case 64: hipLaunchKernelGGL((split_rows<64, PLAN>), grid, dim3(256), 0, st, V, ld, rows, quads, q, s, P); break;
+    default: hipLaunchKernelGGL((split_rows<128, PLAN>), grid, dim3(256), 0, st, V, ld, rows, quads, q, s, P);
   }
   return hipGetLastError();
 }
@@ -912,12 +953,12 @@ hipError_t fp4_launch_moe_experts(const uint16_t* X, int64_t T, int64_t D, int64
   float* out = reinterpret_cast<float*>(ws + FP4_MOE_WS_OUT(T, k, D, I));
   Slot* slot = reinterpret_cast<Slot*>(ws + FP4_MOE_WS_PLAN(T, k, D, I));
   int* list = reinterpret_cast<int*>(slot + pairs);
-  // Two launches that read a pair's matrices for that pair (2.5 TB/s), or five that read those of the used experts once
-  // (24 us and 4.4 TB/s, as fitted to 8 .. 64 pairs of 2048 x 768 and 7168 x 1408), whichever is sooner; the used
+  // Two launches that read a pair's matrices for that pair (3.1 TB/s), or five that read those of the used experts once
+  // (22 us and 4.4 TB/s, as fitted to 8 .. 64 pairs of 2048 x 768 and 7168 x 1408), whichever is sooner; the used
   // experts are guessed as those of evenly spread ids.
   const double bytes = 1.59 * (double)D * (double)I;  // of an expert
   const double spread = (double)E * (1.0 - std::pow(1.0 - std::min(1.0, (double)k / (double)E), (double)T));
-  if (pairs * bytes / 2.5e6 < 24.0 + std::min((double)pairs, spread) * bytes / 4.4e6) {
+  if (pairs * bytes / 3.1e6 < 22.0 + std::min((double)pairs, spread) * bytes / 4.4e6) {
     const FewArgs up{X, ldx, ids, weights, k, (int)E, (int)D, (int)I, W13q, W13s, h};
     const hipError_t e = launch_few<true>(block, up, pairs, st);
     if (e != hipSuccess) return e;
