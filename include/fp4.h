@@ -1,7 +1,8 @@
 /*
  * fp4.h - C ABI of the MI355X (gfx950) online FP4 inference path.
  *
- * Three calls, matching the method's statement of the problem:
+ * Three calls, matching the method's statement of the problem (the 8-bit and mixture-of-experts calls of a model's other
+ * layers stand at the end):
  *
  *   fp4_rotate_quantize   online: block-wise Hadamard rotation of bf16
  *                         activations fused with microscaled FP4 quantization.
@@ -29,8 +30,9 @@
  *  - All arguments are validated before anything is launched. On a non-OK
  *    status nothing has been launched and no output has been written; the
  *    message is available from fp4_last_error().
- *  - bf16 X / W values must be finite, with |value| <= 2^100 (larger values may
- *    overflow inside the float32 rotation); NaN/Inf are outside the contract.
+ *  - bf16 X / W values of the FP4 calls must be finite, with |value| <= 2^100
+ *    (larger values may overflow inside the float32 rotation); NaN/Inf are outside
+ *    their contract. The 8-bit and mixture-of-experts calls say what becomes of them.
  */
 #ifndef FP4_MI355X_H
 #define FP4_MI355X_H
@@ -321,7 +323,8 @@ FP4_API int fp8_linear(const uint8_t *Xq, const float *Xs, const uint8_t *Wq, co
                        int64_t K, void *Y, void *stream);
 
 /*
- * Mixture of experts for a few tokens, over MXFP4 experts.
+ * Mixture of experts for a few tokens, over MXFP4 experts: a decode batch. (A prompt, with tokens enough for every
+ * expert to fill the matrix cores, takes fp4_linear for each expert's tokens.)
  *
  * fp4_moe_route - the router: p = softmax(X Wr^T) over the E experts in float32, the k of the largest
  * logits of each token in falling order (of equal ones the lowest index first; NaN below every number).
