@@ -15,6 +15,10 @@ namespace fp4 {
 
 typedef unsigned v2u __attribute__((ext_vector_type(2)));
 
+// The same at any even address, as rows of an N that is no multiple of 8 begin: global memory takes wide stores there.
+typedef v2u v2u_any __attribute__((aligned(2)));
+typedef v4u v4u_any __attribute__((aligned(2)));
+
 constexpr int kF8Group = 128;
 constexpr unsigned kF8FloorBits = 0x0D800000u;  // 2^-100
 

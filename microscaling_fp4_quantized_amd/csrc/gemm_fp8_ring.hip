@@ -13,7 +13,8 @@
 //    scales are one number per block and 128 features: lane l holds those of blocks 64 i + l, and a
 //    block's comes from v_readlane.
 //  * The barrier of the ring waits for LDS reads only, so the DMA of the next stage stays in flight.
-//  * Output tiles go through LDS as bf16, so Y is written as whole row segments.
+//  * Output tiles go through LDS as bf16, so Y is written as whole row segments, in 16-byte pieces also where N is no
+//    multiple of 8 (2048 x 14340, K = 4096: 126 us, 155 in elements of two bytes; 2048 x 14336 113-115 beside them).
 //  * Workgroup i runs on XCD i % 8; each XCD takes a contiguous range of tiles, M fastest within groups
 //    of 4 tile rows, so tiles running together share X and W in that XCD's L2.
 //
@@ -256,6 +257,8 @@ __device__ __forceinline__ void ring_tile(uint8_t* smem, const uint8_t* __restri
     uint16_t* dst = Y + (size_t)row * N + col;
     if (vec && col + 8 <= N) {
       __builtin_nontemporal_store(v, reinterpret_cast<v4u*>(dst));
+    } else if (col + 8 <= N) {  // pieces share lines with their neighbours: through the caches
+      *reinterpret_cast<v4u_any*>(dst) = v;
     } else {
 #pragma unroll
       for (int q = 0; q < 8; ++q)
@@ -465,6 +468,8 @@ __global__ __launch_bounds__(512) void gemm_fp8_turns(const uint8_t* __restrict_
     uint16_t* dst = Y + (size_t)row * N + col;
     if (vec && col + 8 <= N) {
       __builtin_nontemporal_store(v, reinterpret_cast<v4u*>(dst));
+    } else if (col + 8 <= N) {  // pieces share lines with their neighbours: through the caches
+      *reinterpret_cast<v4u_any*>(dst) = v;
     } else {
 #pragma unroll
       for (int q = 0; q < 8; ++q)

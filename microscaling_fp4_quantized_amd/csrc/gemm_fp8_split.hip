@@ -137,8 +137,8 @@ __device__ __forceinline__ void split_tile(uint8_t* smem, const uint8_t* __restr
     uint16_t o[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] = __builtin_bit_cast(uint16_t, (__bf16)v[e]);
-    if ((N & 3) == 0 && n + 3 < N) {
-      *reinterpret_cast<v2u*>(dst) = v2u{o[0] | ((unsigned)o[1] << 16), o[2] | ((unsigned)o[3] << 16)};
+    if (n + 3 < N) {
+      *reinterpret_cast<v2u_any*>(dst) = v2u{o[0] | ((unsigned)o[1] << 16), o[2] | ((unsigned)o[3] << 16)};
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
