@@ -958,12 +958,16 @@ hipError_t fp4_launch_moe_experts(const uint16_t* X, int64_t T, int64_t D, int64
   float* out = reinterpret_cast<float*>(ws + FP4_MOE_WS_OUT(T, k, D, I));
   Slot* slot = reinterpret_cast<Slot*>(ws + FP4_MOE_WS_PLAN(T, k, D, I));
   int* list = reinterpret_cast<int*>(slot + pairs);
-  // Two launches that read a pair's matrices for that pair (3.1 TB/s), or five that read those of the used experts once
-  // (22 us and 4.4 TB/s, as fitted to 8 .. 64 pairs of 2048 x 768 and 7168 x 1408), whichever is sooner; the used
-  // experts are guessed as those of evenly spread ids.
+  // Two launches that read a pair's matrices for that pair (6 us, and 3.4 TB/s or 4.7 ns a workgroup, whichever is
+  // longer), or five that read those of the used experts once (22 us and 4.4 TB/s), as fitted to 2 .. 250 pairs of
+  // matrices from 512 x 384 to 7168 x 1408, whichever is sooner; the used experts are guessed as those of evenly
+  // spread ids. (Two launches and five: 8 of 128 experts of 2048 x 768, 4 tokens 25 and 41 us, 16 tokens 98 and 64; 2 of
+  // 128 of 4992 x 128, 51 tokens 88 and 49; 5 of 64 of 512 x 384, 49 tokens 43 and 31.)
   const double bytes = 1.59 * (double)D * (double)I;  // of an expert
   const double spread = (double)E * (1.0 - std::pow(1.0 - std::min(1.0, (double)k / (double)E), (double)T));
-  if (pairs * bytes / 3.1e6 < 22.0 + std::min((double)pairs, spread) * bytes / 4.4e6) {
+  const double groups = (double)pairs * (double)I / 16 + (double)T * (double)D / 16;
+  const double few = 6.0 + std::max((double)pairs * bytes / 3.4e6, groups * 4.7e-3);
+  if (few < 22.0 + std::min((double)pairs, spread) * bytes / 4.4e6) {
     const FewArgs up{X, ldx, ids, weights, k, (int)E, (int)D, (int)I, W13q, W13s, h};
     const hipError_t e = launch_few<true>(block, up, pairs, st);
     if (e != hipSuccess) return e;
