@@ -22,7 +22,7 @@
 //   combine    y_t = sum_j p_tj * down, over the slots in order, rounded once to bf16
 // Few pairs take two launches instead (few_experts below).
 //
-// 64 tokens, 6 of 64 experts of 4096 x 1408 (588 MB of weights): 145 us; up 82 us (4.8 TB/s), down 54 (3.6), the other
+// 64 tokens, 6 of 64 experts of 4096 x 1408 (588 MB of weights): 145 us; up 82 us (4.8 TB/s), down 52 (3.8), the other
 // three 5 each. The same workgroups without products, tokens and scales, streaming W alone, take 69 and 43: what is
 // left to a plain read of the weights (98 us) is mostly the starts and ends of workgroups.
 #include <algorithm>
@@ -628,14 +628,15 @@ __global__ __launch_bounds__(64 * S) __attribute__((amdgpu_waves_per_eu(2, 8))) 
 template <bool UP, int S>
 hipError_t launch_gemm(const ExpertArgs& A, int slots, int tiles, hipStream_t st) {
   static std::atomic<int> ready[64];
-  constexpr int lds = S * kRing * kHalfBytes + kScaleBytes;
+  const int scale_row = (UP ? A.D : A.I) / 32;
+  const int lds = S * kRing * kHalfBytes + (scale_row > kScaleRow ? kScaleBytes : (64 * scale_row + 1023) / 1024 * 1024);
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
   auto kern = expert_gemm<UP, S>;
   const bool cached = dev >= 0 && dev < 64;
   if (!cached || !ready[dev].load(std::memory_order_acquire)) {
-    e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, S * kRing * kHalfBytes + kScaleBytes);
     if (e != hipSuccess) return e;
     if (cached) ready[dev].store(1, std::memory_order_release);
   }
@@ -643,13 +644,17 @@ hipError_t launch_gemm(const ExpertArgs& A, int slots, int tiles, hipStream_t st
   return hipGetLastError();
 }
 
-// Two waves a workgroup where there are workgroups enough for four on every CU, eight where K has to be split
-// further to fill the chip (6 of 64 experts of 4096 x 1408, 64 tokens: 151 us with two, 168 with four, 230 with
-// eight).
+// Eight waves a workgroup where K has to be split to fill the chip, and where there are workgroups enough for four on
+// every CU two, or one for a short K, of which two waves would have little or nothing each: more workgroups on a CU then
+// hide each other's starts. Two waves and one, us a call: 64 tokens, 6 of 64 of 4096 x 1408 (down alone) 145 and 143;
+// 8 of 128 of 2048 x 768 (down) 90 and 86; 4 of 256 of 768 x 512 (both) 42 and 37; 51 tokens, 2 of 128 of 4992 x 128
+// (down) 50 and 43; but up alone, K = 4096, 82 and 85. Four and eight waves at the first: 168 and 230.
+constexpr int kShortK = 1536;
 template <bool UP>
 hipError_t launch_experts(const ExpertArgs& A, int slots, hipStream_t st) {
   const int tiles = UP ? A.I / 32 : A.D / 64;
-  return slots * tiles < 1024 ? launch_gemm<UP, 8>(A, slots, tiles, st) : launch_gemm<UP, 2>(A, slots, tiles, st);
+  if (slots * tiles < 1024) return launch_gemm<UP, 8>(A, slots, tiles, st);
+  return (UP ? A.D : A.I) <= kShortK ? launch_gemm<UP, 1>(A, slots, tiles, st) : launch_gemm<UP, 2>(A, slots, tiles, st);
 }
 
 // ---- a few pairs: two launches ------------------------------------------------------------------------------------------

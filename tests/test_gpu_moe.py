@@ -137,7 +137,7 @@ def test_experts(T, E, D, I, k, block):
 SORTED = [(128, 16, 256, 128, 16, 32), (128, 16, 128, 256, 16, 16), (100, 20, 384, 640, 8, 64),
           (64, 16, 1152, 128, 8, 128), (37, 9, 4224, 128, 7, 32), (19, 5, 128, 4352, 5, 64), (50, 12, 7168, 256, 3, 128),
           (24, 3, 8320, 128, 3, 16), (12, 4, 1408, 1408, 2, 128), (128, 60, 640, 256, 3, 64), (90, 32, 256, 1024, 5, 32),
-          (128, 64, 1024, 128, 4, 64)]
+          (128, 64, 1024, 128, 4, 64), (20, 32, 2048, 1664, 2, 32), (60, 64, 512, 1152, 3, 16)]
 
 
 @pytest.mark.parametrize("T,E,D,I,k,block", SORTED)
