@@ -475,7 +475,9 @@ __device__ __forceinline__ void expert_tile(uint8_t* lds, const ExpertArgs& A, c
       }
     }
   };
-  constexpr int kFetch = 2 * kTiles, kTokenLoads = 6 * MF;  // loads of a fetch, and of a half slice's tokens
+  // DMA loads of a fetch. The counted waits below count these alone: loads return in order, every one of these is issued, and
+  // loads to registers, which the compiler may merge, drop or move, can only make such a wait longer than it has to be.
+  constexpr int kDma = 2 * kTiles;
   fetch_scales(0);
   if (mine > 0) fetch(0);
   const int col = r % kCols;
@@ -509,8 +511,8 @@ __device__ __forceinline__ void expert_tile(uint8_t* lds, const ExpertArgs& A, c
     if constexpr (XB == 2) load_tokens(1, 1);
     fetch(1);
   }
-  // window 0 has landed: it was requested first
-  if (mine > 1) wait_vmcnt<2 * kFetch + XB * kTokenLoads>();
+  // window 0 has landed: it was requested before both fetches
+  if (mine > 1) wait_vmcnt<2 * kDma>();
   else wait_vmcnt<0>();
   __syncthreads();
   v4f acc[kTiles][MF];
@@ -535,8 +537,8 @@ __device__ __forceinline__ void expert_tile(uint8_t* lds, const ExpertArgs& A, c
       for (int h = 0; h < 2; ++h) {
         const int j = jj + h, i = wave + S * j;
         if (j >= mine) break;  // uniform in the wave
-        // the half slice has landed: at least the next one's W (and, two ahead, its tokens) was requested after it
-        if (j + 1 < mine) wait_vmcnt<(XB - 1) * kTokenLoads + kFetch>();
+        // the half slice has landed: the next one's W was requested after it
+        if (j + 1 < mine) wait_vmcnt<kDma>();
         else wait_vmcnt<0>();
         asm volatile("" ::: "memory");
         const uint8_t* wa = ring + (j % kRing) * kHalfBytes + r * kHalf;
@@ -713,8 +715,8 @@ __device__ __forceinline__ void few_items(uint8_t* lds, const FewArgs& A, int ti
   using Slot1 = std::integral_constant<int, 1>;
   static_assert(kRing == 2 && kItems % kRing == 0, "an item's slot goes by its place in the group");
   unsigned sw[kRing][kTiles][2];
-  // W of item m into ring slot m % kRing (`slot`), its scale bytes to registers: 2 + 2 loads a tile, also for an unused slot, which
-  // reads nothing of W.
+  // W of item m into ring slot m % kRing (`slot`), two DMA loads a tile, also for an unused slot, which reads nothing of W;
+  // its scale bytes to registers.
   auto fetch = [&](int m, auto slot) {
     constexpr int b = decltype(slot)::value;
     const int id = A.ids[pair_of(m)], i = half_of(m), e = used(id) ? id : 0;
@@ -735,7 +737,7 @@ __device__ __forceinline__ void few_items(uint8_t* lds, const FewArgs& A, int ti
       }
     }
   };
-  constexpr int kFetch = 4 * kTiles;
+  constexpr int kDma = 2 * kTiles;  // DMA loads of a fetch; as in expert_tile, no counted wait counts others
 
   v4f acc[kTiles];
 #pragma unroll
@@ -775,8 +777,8 @@ __device__ __forceinline__ void few_items(uint8_t* lds, const FewArgs& A, int ti
       constexpr int b = decltype(slot)::value;
       const int m = m0 + n;
       if (m >= mine) return;  // uniform in the wave
-      // the item has landed: at most the next one's loads are younger
-      if (m + 1 < mine) wait_vmcnt<kFetch>();
+      // the item has landed: the next one's DMA is younger
+      if (m + 1 < mine) wait_vmcnt<kDma>();
       else wait_vmcnt<0>();
       asm volatile("" ::: "memory");
       if (used(A.ids[pair_of(m)])) {  // uniform in the wave
