@@ -120,7 +120,9 @@ __global__ __launch_bounds__(NT* ROWS) void add_rmsnorm_quantize(const uint16_t*
   static_assert(ROWS == 1 || NT == 64, "one row per workgroup, or one per wave");
   __shared__ float red[NT / 64];
   const int tid = ROWS > 1 ? threadIdx.x & 63 : threadIdx.x;
-  const int64_t row = ROWS > 1 ? (int64_t)blockIdx.x * ROWS + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
+  // rows of one workgroup each are long, so their number fits the grid's x (fp8_launch_add_rmsnorm_quantize)
+  const int64_t row =
+      ROWS > 1 ? ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * ROWS + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
   if (ROWS > 1 && row >= M) return;
   const uint32_t chunks = K / 8;
   const uint16_t* x = X + row * ldx;
@@ -183,8 +185,9 @@ hipError_t launch_norm(const uint16_t* X, int64_t M, int64_t K, int64_t ldx, con
   const bool stream = M * K * (R ? 4 : 2) > kStreamBytes;
   auto kern = R ? (stream ? add_rmsnorm_quantize<NT, V, ROWS, true, true> : add_rmsnorm_quantize<NT, V, ROWS, true, false>)
                 : (stream ? add_rmsnorm_quantize<NT, V, ROWS, false, true> : add_rmsnorm_quantize<NT, V, ROWS, false, false>);
-  hipLaunchKernelGGL(kern, dim3((unsigned)((M + ROWS - 1) / ROWS)), dim3(NT * ROWS), 0, st, X, ldx, R, ldr, G, eps, M,
-                     (uint32_t)K, codes, scales, H, Y);
+  const Grid grid = grid_of((M + ROWS - 1) / ROWS, NT * ROWS);
+  hipLaunchKernelGGL(kern, dim3(grid.x, grid.y), dim3(NT * ROWS), 0, st, X, ldx, R, ldr, G, eps, M, (uint32_t)K, codes,
+                     scales, H, Y);
   return hipGetLastError();
 }
 
@@ -228,6 +231,7 @@ hipError_t fp8_launch_add_rmsnorm_quantize(const uint16_t* X, int64_t M, int64_t
   typedef integral_constant<int, 64> t64;
   typedef integral_constant<int, 256> t256;
   typedef integral_constant<int, 1024> t1024;
+  // M * K / 8 < 2^31: rows of more than 1024 are so few that 256 or 1024 threads each make less than 2^32
   if (K <= 512) return go(t64{}, i1{}, i4{});
   if (K <= 1024) return go(t64{}, i2{}, i4{});
   if (K <= 2048) return go(t256{}, i1{}, i1{});

@@ -302,7 +302,8 @@ __global__ __launch_bounds__(512) void gemm_fp8_turns(const uint8_t* __restrict_
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   int tm, tn;
   {
-    const int T = tiles_m * tiles_n, b = blockIdx.x;
+    const int T = tiles_m * tiles_n, b = (int)(blockIdx.y * gridDim.x + blockIdx.x);
+    if (b >= T) return;
     map_tile(T % 8 == 0 ? (b & 7) * (T >> 3) + (b >> 3) : b, tiles_m, tiles_n, tm, tn);
   }
   const int m0 = tm * PBM, n0 = tn * PBN;
@@ -484,7 +485,8 @@ __global__ __launch_bounds__(C::NT) void gemm_fp8_ring(const uint8_t* __restrict
                                                     uint16_t* __restrict__ Y, int M, int N, int K, int tiles_m,
                                                     int tiles_n) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-  const int T = tiles_m * tiles_n, b = blockIdx.x;
+  const int T = tiles_m * tiles_n, b = (int)(blockIdx.y * gridDim.x + blockIdx.x);
+  if (b >= T) return;
   const int L = T % 8 == 0 ? (b & 7) * (T >> 3) + (b >> 3) : b;
   int tm, tn;
   map_tile(L, tiles_m, tiles_n, tm, tn);
@@ -503,8 +505,8 @@ hipError_t launch(const uint8_t* Xq, const float* Xs, const uint8_t* Wq, const f
     if (cached) ready[dev].store(1, std::memory_order_release);
   }
   const int tiles_m = (M - 1) / C::BM + 1, tiles_n = (N - 1) / C::BN + 1;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(tiles_m * tiles_n)), dim3(C::NT), C::LDS, st, Xq, Xs, Wq, Ws, Y, M, N, K,
-                     tiles_m, tiles_n);
+  const Grid grid = grid_of((int64_t)tiles_m * tiles_n, C::NT);
+  hipLaunchKernelGGL(kern, dim3(grid.x, grid.y), dim3(C::NT), C::LDS, st, Xq, Xs, Wq, Ws, Y, M, N, K, tiles_m, tiles_n);
   return hipGetLastError();
 }
 
@@ -519,8 +521,9 @@ hipError_t launch_turns(const uint8_t* Xq, const float* Xs, const uint8_t* Wq, c
     if (cached) ready[dev].store(1, std::memory_order_release);
   }
   const int tiles_m = (M - 1) / PBM + 1, tiles_n = (N - 1) / PBN + 1;
-  hipLaunchKernelGGL(gemm_fp8_turns, dim3((unsigned)(tiles_m * tiles_n)), dim3(512), P_LDS, st, Xq, Xs, Wq, Ws, Y, M, N, K,
-                     tiles_m, tiles_n);
+  const Grid grid = grid_of((int64_t)tiles_m * tiles_n, 512);
+  hipLaunchKernelGGL(gemm_fp8_turns, dim3(grid.x, grid.y), dim3(512), P_LDS, st, Xq, Xs, Wq, Ws, Y, M, N, K, tiles_m,
+                     tiles_n);
   return hipGetLastError();
 }
 

@@ -151,12 +151,13 @@ template <int MF, int NF>
 __global__ __launch_bounds__(64 * WAVES) void gemm_fp8_split(const uint8_t* __restrict__ Xq, const float* __restrict__ Xs,
                                                              const uint8_t* __restrict__ Wq,
                                                              const float* __restrict__ Ws, uint16_t* __restrict__ Y,
-                                                             int M, int N, int K, int tiles_m) {
+                                                             int M, int N, int K, int tiles_m, unsigned T) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   // workgroup i runs on XCD i % 8; each takes a contiguous range of tiles, X's fastest, so that tiles of the same W
   // share it in that XCD's L2
-  const unsigned T = gridDim.x, xcd = blockIdx.x & 7;
-  const unsigned L = xcd * (T >> 3) + min(xcd, T & 7) + (blockIdx.x >> 3);
+  const unsigned b = blockIdx.y * gridDim.x + blockIdx.x, xcd = b & 7;
+  if (b >= T) return;
+  const unsigned L = xcd * (T >> 3) + min(xcd, T & 7) + (b >> 3);
   split_tile<MF, NF>(smem, Xq, Xs, Wq, Ws, Y, M, N, K, (int)(L % tiles_m) * 16 * MF, (int)(L / tiles_m) * 16 * NF);
 }
 
@@ -173,8 +174,9 @@ hipError_t launch(const uint8_t* Xq, const float* Xs, const uint8_t* Wq, const f
     if (cached) ready[dev].store(1, std::memory_order_release);
   }
   const int tiles_m = (M - 1) / C::BM + 1, tiles_n = (N - 1) / C::BN + 1;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(tiles_m * tiles_n)), dim3(64 * WAVES), C::LDS, st, Xq, Xs, Wq, Ws, Y, M, N, K,
-                     tiles_m);
+  const Grid grid = grid_of((int64_t)tiles_m * tiles_n, 64 * WAVES);
+  hipLaunchKernelGGL(kern, dim3(grid.x, grid.y), dim3(64 * WAVES), C::LDS, st, Xq, Xs, Wq, Ws, Y, M, N, K, tiles_m,
+                     (unsigned)(tiles_m * tiles_n));
   return hipGetLastError();
 }
 

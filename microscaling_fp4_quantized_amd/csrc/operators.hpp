@@ -2,6 +2,7 @@
 // common.hpp, which every FP4 kernel is compiled with: what was measured on those sources stays valid.
 #pragma once
 
+#include "choices.hpp"
 #include "common.hpp"
 
 // 8-bit (E4M3, one float32 scale for 128 values along K) operators.
