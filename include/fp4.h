@@ -275,7 +275,7 @@ FP4_API int fp4_rotate_quantize_linear_noalloc(const void *X, int64_t M, int64_t
  *  X       device bf16 [M, ldx], 16-byte aligned, ldx >= K, ldx % 8 == 0.
  *  codes   device uint8 [M, K], 16-byte aligned.
  *  scales  device float [M, K / 128].
- *  M >= 1, M * K / 8 < 2^31.
+ *  M >= 1, M * K / 8 < 2^31, ldx <= 2^40.
  * fp8_quantize_weights - weights, one scale for 128 x 128 values (fewer rows in the last block of an
  * N that is no multiple of 128): scales is float [ceil(N / 128), K / 128].
  * Errors: FP4_E_NULLPTR, FP4_E_SHAPE, FP4_E_ALIGN.
@@ -297,7 +297,7 @@ FP4_API int fp8_quantize_weights(const void *W, int64_t N, int64_t K, int64_t ld
  *  residual_out  device bf16 [M, K]: h rounded. Non-NULL exactly when residual is. It may be the
  *                residual's own buffer (ldr == K); no other overlap of buffers is allowed.
  *  normed        device bf16 [M, K], or NULL: n rounded, for the layers that take bf16.
- *  M >= 1; K <= 65536. Matrices 16-byte aligned, ldx, ldr >= K and multiples of 8.
+ *  M >= 1, M * K / 8 < 2^31; K <= 65536. Matrices 16-byte aligned, ldx, ldr >= K, multiples of 8, at most 2^40.
  * Errors: FP4_E_NULLPTR, FP4_E_SHAPE (also eps), FP4_E_ALIGN.
  */
 FP4_API int fp8_add_rmsnorm_quantize(const void *X, int64_t M, int64_t K, int64_t ldx, const void *residual,
@@ -314,7 +314,7 @@ FP4_API int fp8_add_rmsnorm_quantize(const void *X, int64_t M, int64_t K, int64_
  *  Xq, Xs  device uint8 [M, K], float [M, K / 128]               (fp8_quantize, fp8_add_rmsnorm_quantize)
  *  Wq, Ws  device uint8 [N, K], float [ceil(N / 128), K / 128]   (fp8_quantize_weights)
  *  Y       device bf16 [M, N] row-major.
- *  M, N >= 1, at most 2^31 - 1; K <= 2^23; M * K and N * K <= 2^40.
+ *  M, N >= 1, at most 2^31 - 1; K <= 2^23; M * K and N * K <= 2^40; ceil(M / 128) * ceil(N / 64) <= 2^31 - 1.
  *  Xq, Wq and Y 16-byte aligned, Xs and Ws 4-byte aligned.
  * Results do not depend on timing: partial sums meet in a fixed order.
  * Errors: FP4_E_NULLPTR, FP4_E_SHAPE, FP4_E_ALIGN.
@@ -329,17 +329,17 @@ FP4_API int fp8_linear(const uint8_t *Xq, const float *Xs, const uint8_t *Wq, co
  * fp4_moe_route - the router: p = softmax(X Wr^T) over the E experts in float32, the k of the largest
  * logits of each token in falling order (of equal ones the lowest index first; NaN below every number).
  *  X        device bf16 [T, ldx], ldx >= D, ldx % 8 == 0.   Wr  device bf16 [E, D].
- *  T >= 1, T * E < 2^31; D a positive multiple of 128, at most 2^24; 1 <= E <= 1024; 1 <= k <= min(E, 16).
+ *  1 <= T <= FP4_MOE_ROUTE_MAX_TOKENS; D a positive multiple of 128, at most 2^24; 1 <= E <= 1024; 1 <= k <= min(E, 16).
  *  renormalize  non-zero: the k weights of a token are divided by their sum.
  *  ids      device int [T, k].   weights  device float [T, k].
  *  workspace, workspace_bytes  device buffer of at least FP4_MOE_ROUTE_WORKSPACE_BYTES(T, E) bytes.
- * X, Wr and workspace 16-byte aligned, ids and weights 4-byte aligned. Two launches on `stream`.
+ * X, Wr and workspace 16-byte aligned, ldx at most 2^40, ids and weights 4-byte aligned. Two launches on `stream`.
  *
  * fp4_moe_experts - Y[t] = sum_j weights[t, j] * W2[e] H (silu(G[e] H X[t]) * (U[e] H X[t])), e = ids[t, j], silu(a) =
  * a / (1 + exp(-a)), H the block Hadamard rotation of fp4_rotate_quantize. The weights are MXFP4 as
  * fp4_quantize_weights makes them (in the rotated basis); the activations are not quantized to 4 bits: they
  * enter as sums of three E4M3 numbers (12 bits and more), all sums are float32, and Y is rounded once.
- *  X            device bf16 [T, ldx], ldx >= D, ldx % 8 == 0; 1 <= T <= FP4_MOE_MAX_TOKENS.
+ *  X            device bf16 [T, ldx], ldx >= D, ldx % 8 == 0, ldx <= 2^40; 1 <= T <= FP4_MOE_MAX_TOKENS.
  *  ids          device int [T, k], weights device float [T, k], 1 <= k <= FP4_MOE_MAX_TOPK. A slot whose id is
  *               outside [0, E) (-1, say) is unused and adds nothing; a token without a used slot gets zeros.
  *               An expert may stand in several slots of a token.
@@ -353,6 +353,7 @@ FP4_API int fp8_linear(const uint8_t *Xq, const float *Xs, const uint8_t *Wq, co
  * A NaN or infinity in X[t] makes Y[t] NaN and no other row.
  * Errors of both: FP4_E_BLOCK, FP4_E_NULLPTR, FP4_E_SHAPE (also a short workspace), FP4_E_ALIGN.
  */
+#define FP4_MOE_ROUTE_MAX_TOKENS 1048560 /* 16 tokens times what a grid's second dimension holds */
 #define FP4_MOE_MAX_TOKENS 128
 #define FP4_MOE_MAX_TOPK 16
 #define FP4_MOE_WS_PLAN_PAIR 84

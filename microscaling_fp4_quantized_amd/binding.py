@@ -518,7 +518,7 @@ def _workspace(workspace, need, name, dev):
 def fp4_moe_route(x: torch.Tensor, router: torch.Tensor, k: int, renormalize: bool = True, out=None, workspace="auto"):
     """softmax(x router^T) in float32 and its k largest of each token: (ids [T, k] int32, weights [T, k] float32).
 
-    x bf16 [T, D], router bf16 [E, D]. Of equal weights the lowest expert comes first. ``out`` may pass
+    x bf16 [T, D], T at most 1048560, router bf16 [E, D]. Of equal weights the lowest expert comes first. ``out`` may pass
     preallocated (ids, weights); workspace: "auto", or a uint8 CUDA tensor of at least 16 T E bytes."""
     name = "fp4_moe_route"
     if not isinstance(router, torch.Tensor) or router.dim() != 2:

@@ -253,7 +253,7 @@ int fp8_add_rmsnorm_quantize(const void* X, int64_t M, int64_t K, int64_t ldx, c
                 (long long)K);
   if (residual && residual == residual_out && ldr != K)
     return fail(FP4_E_SHAPE, "%s: a residual written in place needs ldr == K", who);
-  if (!(eps >= 0.f) || eps > 3.0e38f) return fail(FP4_E_SHAPE, "%s: eps must be finite and not negative", who);
+  if (!(eps >= 0.f) || !__builtin_isfinite(eps)) return fail(FP4_E_SHAPE, "%s: eps must be finite and not negative", who);
   if (!aligned(weight, 16) || (residual && (!aligned(residual, 16) || ldr % 8 || !aligned(residual_out, 16))) ||
       (normed && !aligned(normed, 16)))
     return fail(FP4_E_ALIGN, "%s: weight, residual and outputs must be 16-byte aligned, ldr %% 8 == 0", who);
@@ -284,9 +284,9 @@ int fp4_moe_route(const void* X, int64_t T, int64_t D, int64_t ldx, const void* 
                   int* ids, float* weights, void* workspace, size_t workspace_bytes, void* stream) {
   const char* who = "fp4_moe_route";
   if (!X || !Wr || !ids || !weights || !workspace) return fail(FP4_E_NULLPTR, "%s: pointers must be non-NULL", who);
-  if (T < 1 || D < 128 || D % 128 || D > (1 << 24) || E < 1 || E > 1024 || T > 0x7FFFFFFFLL / E || (T + 15) / 16 > 65535)
-    return fail(FP4_E_SHAPE, "%s: need T >= 1, D a positive multiple of 128, 1 <= E <= 1024 (T=%lld D=%lld E=%lld)", who,
-                (long long)T, (long long)D, (long long)E);
+  if (T < 1 || T > FP4_MOE_ROUTE_MAX_TOKENS || D < 128 || D % 128 || D > (1 << 24) || E < 1 || E > 1024)
+    return fail(FP4_E_SHAPE, "%s: need 1 <= T <= %d, D a positive multiple of 128 up to %d, 1 <= E <= 1024 (T=%lld D=%lld E=%lld)",
+                who, FP4_MOE_ROUTE_MAX_TOKENS, 1 << 24, (long long)T, (long long)D, (long long)E);
   if (k < 1 || k > FP4_MOE_MAX_TOPK || k > E)
     return fail(FP4_E_SHAPE, "%s: k=%d not in 1 .. min(E, %d)", who, k, FP4_MOE_MAX_TOPK);
   if (ldx < D || ldx > (int64_t)1 << 40) return fail(FP4_E_SHAPE, "%s: leading dimension %lld < D", who, (long long)ldx);
