@@ -380,7 +380,8 @@ FP4_API int fp4_moe_experts(const void *X, int64_t T, int64_t D, int64_t ldx, co
 /* Message for the last non-OK status returned on this thread ("" if none). */
 FP4_API const char *fp4_last_error(void);
 
-/* ABI version of this header (major * 100 + minor). */
+/* ABI version of this header (major * 100 + minor); fp4_abi_version gives the one that the library was built with. */
+#define FP4_ABI_VERSION 130
 FP4_API int fp4_abi_version(void);
 
 #ifdef __cplusplus

@@ -141,6 +141,17 @@ class _Fast:
         self.experts = bind(module.experts, "fp4_moe_experts")
 
 
+def _compiled(lib):
+    """The compiled calls for this library, or False: not built, built for another ABI, or no raw stream handles."""
+    try:
+        from . import _torch_calls
+    except ImportError:
+        return False
+    if getattr(_torch_calls, "ABI_VERSION", None) != lib.fp4_abi_version() or _RAW_STREAM is None:
+        return False
+    return _Fast(_torch_calls, lib)
+
+
 def _fast(t):
     """The compiled calls (_torch_calls.so) for calls with given outputs on the GPU, where the interpreter's share of
     a small call counts; None without them. They return a status, or None for operands that they leave to the checks
@@ -149,13 +160,7 @@ def _fast(t):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         return None
     if _FAST is None:
-        lib = load_library()
-        try:
-            from . import _torch_calls
-        except ImportError:
-            _FAST = False
-        else:
-            _FAST = _Fast(_torch_calls, lib) if _RAW_STREAM is not None else False
+        _FAST = _compiled(load_library())
     return _FAST or None
 
 

@@ -330,6 +330,6 @@ int fp4_moe_experts(const void* X, int64_t T, int64_t D, int64_t ldx, const int*
 
 const char* fp4_last_error(void) { return g_err; }
 
-int fp4_abi_version(void) { return 130; }
+int fp4_abi_version(void) { return FP4_ABI_VERSION; }
 
 }  // extern "C"

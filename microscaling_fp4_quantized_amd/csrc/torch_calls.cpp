@@ -10,6 +10,9 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
+#include <type_traits>
+
+#include "../../include/fp4.h"
 
 namespace {
 
@@ -111,7 +114,8 @@ constexpr int64_t kGroup = 128;
 // quantize(entry, device, stream, x, rows per scale, codes, scales)
 PyObject* quantize(PyObject*, PyObject* const* args, Py_ssize_t n) {
   Args a{args, n};
-  auto entry = reinterpret_cast<int (*)(const void*, int64_t, int64_t, int64_t, uint8_t*, float*, void*)>(a.address());
+  auto entry = reinterpret_cast<decltype(&fp8_quantize)>(a.address());
+  static_assert(std::is_same<decltype(&fp8_quantize), decltype(&fp8_quantize_weights)>::value, "one call for both");
   a.device = a.integer();
   void* stream = a.address();
   const auto x = a.bf16_rows();
@@ -126,8 +130,7 @@ PyObject* quantize(PyObject*, PyObject* const* args, Py_ssize_t n) {
 // norm(entry, device, stream, x, weight, residual, eps, codes, scales, sum, normed)
 PyObject* norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
   Args a{args, n};
-  auto entry = reinterpret_cast<int (*)(const void*, int64_t, int64_t, int64_t, const void*, int64_t, const void*, float,
-                                        uint8_t*, float*, void*, void*, void*)>(a.address());
+  auto entry = reinterpret_cast<decltype(&fp8_add_rmsnorm_quantize)>(a.address());
   a.device = a.integer();
   void* stream = a.address();
   const auto x = a.bf16_rows();
@@ -148,8 +151,7 @@ PyObject* norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
 // linear(entry, device, stream, xq, xs, wq, ws, y)
 PyObject* linear(PyObject*, PyObject* const* args, Py_ssize_t n) {
   Args a{args, n};
-  auto entry = reinterpret_cast<int (*)(const uint8_t*, const float*, const uint8_t*, const float*, int64_t, int64_t, int64_t,
-                                        void*, void*)>(a.address());
+  auto entry = reinterpret_cast<decltype(&fp8_linear)>(a.address());
   a.device = a.integer();
   void* stream = a.address();
   const Tensor* xq = a.tensor(ScalarType::Float8_e4m3fn, 2);
@@ -170,8 +172,7 @@ PyObject* linear(PyObject*, PyObject* const* args, Py_ssize_t n) {
 // route(entry, device, stream, x, router, k, renormalize, ids, weights, workspace)
 PyObject* route(PyObject*, PyObject* const* args, Py_ssize_t n) {
   Args a{args, n};
-  auto entry = reinterpret_cast<int (*)(const void*, int64_t, int64_t, int64_t, const void*, int64_t, int, int, int*, float*,
-                                        void*, size_t, void*)>(a.address());
+  auto entry = reinterpret_cast<decltype(&fp4_moe_route)>(a.address());
   a.device = a.integer();
   void* stream = a.address();
   const auto x = a.bf16_rows();
@@ -190,9 +191,7 @@ PyObject* route(PyObject*, PyObject* const* args, Py_ssize_t n) {
 // experts(entry, device, stream, x, ids, weights, w13q, w13s, w2q, w2s, block, y, workspace)
 PyObject* experts(PyObject*, PyObject* const* args, Py_ssize_t n) {
   Args a{args, n};
-  auto entry = reinterpret_cast<int (*)(const void*, int64_t, int64_t, int64_t, const int*, const float*, int, int64_t, int64_t,
-                                        int, const uint8_t*, const uint8_t*, const uint8_t*, const uint8_t*, void*, void*,
-                                        size_t, void*)>(a.address());
+  auto entry = reinterpret_cast<decltype(&fp4_moe_experts)>(a.address());
   a.device = a.integer();
   void* stream = a.address();
   const auto x = a.bf16_rows();
@@ -238,4 +237,9 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, kMeth
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__torch_calls(void) { return PyModule_Create(&kModule); }
+// ABI_VERSION: the header that the calls above were compiled against; binding.py enters no library of another.
+PyMODINIT_FUNC PyInit__torch_calls(void) {
+  PyObject* module = PyModule_Create(&kModule);
+  if (module != nullptr && PyModule_AddIntConstant(module, "ABI_VERSION", FP4_ABI_VERSION) != 0) Py_CLEAR(module);
+  return module;
+}
