@@ -527,45 +527,6 @@ hipError_t launch_turns(const uint8_t* Xq, const float* Xs, const uint8_t* Wq, c
   return hipGetLastError();
 }
 
-// The tile shapes: rows of X, rows of W, workgroups that run at once on a CU, and the time of one scale block of K in us
-// (one round of workgroups at K = 4096, the launch taken off). The least rounds times a round's time is taken; up
-// to 8 rows of X, which cost little beside W, go to 16 x 16. The first three split K over the waves of a workgroup
-// (gemm_fp8_split.hip); several of their workgroups run on a CU, sharing what it reads.
-//   rows x N (K 4096)   16 x 16   16 x 32   32 x 32   64 x 64   128 x 64   128 x 128   the same, two a CU   256 x 256   (us)
-//   1 x 14336              10.7      10.6      10.9      12.1
-//   16 x 4096               5.2       5.3       5.9
-//   37 x 4100               8.0       7.2       8.7      12.1
-//   64 x 4096               8.6       7.4       6.5      11.6       15.2        20.6                 24.7        37
-//   128 x 4096             14.1      11.4       9.5      11.8
-//   64 x 14336                       24.7      16.3      12.8       16.3        21.5                 25.6        37
-//   100 x 14336                                          21.8       16.5        23.7                 28.4        39
-//   200 x 14336                                          40.2       31.0        24.5                 28.9        39
-//   300 x 14336                                          51.3       43.4        42.3                 32.1        41
-//   1024 x 14336                                          137        108        93.4                 71.4        53
-//   K 8192: 1 x 28672      40.5      43.3      41.3
-//   8 x 28672              41.9      45.1      43.4
-//   16 x 28672             48.3      44.9      43.7
-struct Shape {
-  int bm, bn, per_cu;
-  float cost;
-};
-constexpr Shape kShapes[] = {{16, 16, 1, 0.047f}, {16, 32, 1, 0.061f}, {32, 32, 1, 0.095f}, {64, 64, 1, 0.26f},
-                             {128, 64, 1, 0.41f}, {128, 128, 1, 0.65f}, {128, 128, 2, 1.16f}, {256, 256, 1, 1.27f}};
-
-int best_shape(int64_t M, int64_t N, int64_t K, int cus) {
-  int best = 0;
-  double least = 0;
-  if (M <= 8) return 0;
-  for (int i = 0; i < (int)(sizeof kShapes / sizeof kShapes[0]); ++i) {
-    const Shape& s = kShapes[i];
-    if (s.bm == PBM && K < 512) break;
-    const int64_t tiles = ((M + s.bm - 1) / s.bm) * ((N + s.bn - 1) / s.bn), slots = (int64_t)s.per_cu * cus;
-    const double t = (double)((tiles + slots - 1) / slots) * s.cost;
-    if (i == 0 || t < least) best = i, least = t;
-  }
-  return best;
-}
-
 }  // namespace
 }  // namespace fp4
 

@@ -25,9 +25,7 @@
 // 64 tokens, 6 of 64 experts of 4096 x 1408 (588 MB of weights): 145 us; up 82 us (4.8 TB/s), down 52 (3.8), the other
 // three 5 each. The same workgroups without products, tokens and scales, streaming W alone, take 69 and 43: what is
 // left to a plain read of the weights (98 us) is mostly the starts and ends of workgroups.
-#include <algorithm>
 #include <atomic>
-#include <cmath>
 #include <type_traits>
 
 #include "fp8_device.hpp"
@@ -646,17 +644,14 @@ hipError_t launch_gemm(const ExpertArgs& A, int slots, int tiles, hipStream_t st
   return hipGetLastError();
 }
 
-// Eight waves a workgroup where K has to be split to fill the chip, and where there are workgroups enough for four on
-// every CU two, or one for a short K, of which two waves would have little or nothing each: more workgroups on a CU then
-// hide each other's starts. Two waves and one, us a call: 64 tokens, 6 of 64 of 4096 x 1408 (down alone) 145 and 143;
-// 8 of 128 of 2048 x 768 (down) 90 and 86; 4 of 256 of 768 x 512 (both) 42 and 37; 51 tokens, 2 of 128 of 4992 x 128
-// (down) 50 and 43; but up alone, K = 4096, 82 and 85. Four and eight waves at the first: 168 and 230.
-constexpr int kShortK = 1536;
 template <bool UP>
 hipError_t launch_experts(const ExpertArgs& A, int slots, hipStream_t st) {
   const int tiles = UP ? A.I / 32 : A.D / 64;
-  if (slots * tiles < 1024) return launch_gemm<UP, 8>(A, slots, tiles, st);
-  return (UP ? A.D : A.I) <= kShortK ? launch_gemm<UP, 1>(A, slots, tiles, st) : launch_gemm<UP, 2>(A, slots, tiles, st);
+  switch (expert_waves(UP ? A.D : A.I, slots * tiles)) {
+    case 1: return launch_gemm<UP, 1>(A, slots, tiles, st);
+    case 2: return launch_gemm<UP, 2>(A, slots, tiles, st);
+    default: return launch_gemm<UP, 8>(A, slots, tiles, st);
+  }
 }
 
 // ---- a few pairs: two launches ------------------------------------------------------------------------------------------
@@ -965,16 +960,7 @@ hipError_t fp4_launch_moe_experts(const uint16_t* X, int64_t T, int64_t D, int64
   float* out = reinterpret_cast<float*>(ws + FP4_MOE_WS_OUT(T, k, D, I));
   Slot* slot = reinterpret_cast<Slot*>(ws + FP4_MOE_WS_PLAN(T, k, D, I));
   int* list = reinterpret_cast<int*>(slot + pairs);
-  // Two launches that read a pair's matrices for that pair (6 us, and 3.4 TB/s or 4.7 ns a workgroup, whichever is
-  // longer), or five that read those of the used experts once (22 us and 4.4 TB/s), as fitted to 2 .. 250 pairs of
-  // matrices from 512 x 384 to 7168 x 1408, whichever is sooner; the used experts are guessed as those of evenly
-  // spread ids. (Two launches and five: 8 of 128 experts of 2048 x 768, 4 tokens 25 and 41 us, 16 tokens 98 and 64; 2 of
-  // 128 of 4992 x 128, 51 tokens 88 and 49; 5 of 64 of 512 x 384, 49 tokens 43 and 31.)
-  const double bytes = 1.59 * (double)D * (double)I;  // of an expert
-  const double spread = (double)E * (1.0 - std::pow(1.0 - std::min(1.0, (double)k / (double)E), (double)T));
-  const double groups = (double)pairs * (double)I / 16 + (double)T * (double)D / 16;
-  const double few = 6.0 + std::max((double)pairs * bytes / 3.4e6, groups * 4.7e-3);
-  if (few < 22.0 + std::min((double)pairs, spread) * bytes / 4.4e6) {
+  if (few_pairs((int)T, k, E, D, I)) {
     const FewArgs up{X, ldx, ids, weights, k, (int)E, (int)D, (int)I, W13q, W13s, h};
     const hipError_t e = launch_few<true>(block, up, pairs, st);
     if (e != hipSuccess) return e;
