@@ -323,8 +323,8 @@ FP4_API int fp8_linear(const uint8_t *Xq, const float *Xs, const uint8_t *Wq, co
                        int64_t K, void *Y, void *stream);
 
 /*
- * Mixture of experts for a few tokens, over MXFP4 experts: a decode batch. (A prompt, with tokens enough for every
- * expert to fill the matrix cores, takes fp4_linear for each expert's tokens.)
+ * Mixture of experts for a few tokens, over MXFP4 experts: a decode batch. The experts take up to FP4_MOE_MAX_TOKENS tokens a call;
+ * rows are independent, so more go in slices of that many, each of which reads the experts it uses.
  *
  * fp4_moe_route - the router: p = softmax(X Wr^T) over the E experts in float32, the k of the largest
  * logits of each token in falling order (of equal ones the lowest index first; NaN below every number).
@@ -350,7 +350,8 @@ FP4_API int fp8_linear(const uint8_t *Xq, const float *Xs, const uint8_t *Wq, co
  *  Y            device bf16 [T, D].
  *  workspace, workspace_bytes  device buffer of at least FP4_MOE_WORKSPACE_BYTES(T, k, D, I) bytes.
  * Device buffers 16-byte aligned, ids and weights 4-byte aligned. Results do not depend on timing.
- * A NaN or infinity in X[t] makes Y[t] NaN and no other row.
+ * A NaN or infinity in X[t], or sums past float32's range, make Y[t] NaN and no other row; a token without a used slot gets zeros
+ * whatever it holds.
  * Errors of both: FP4_E_BLOCK, FP4_E_NULLPTR, FP4_E_SHAPE (also a short workspace), FP4_E_ALIGN.
  */
 #define FP4_MOE_ROUTE_MAX_TOKENS 1048560 /* 16 tokens times what a grid's second dimension holds */

@@ -565,7 +565,7 @@ def moe_workspace_bytes(T: int, k: int, D: int, I: int) -> int:
 def fp4_moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13q, w13s, w2q, w2s, block: int,
                     out=None, workspace="auto"):
     """y_t = sum_j weights[t, j] W2[e] H (silu(G[e] H x_t) * (U[e] H x_t)), e = ids[t, j]: the experts of a
-    mixture-of-experts layer for up to 128 tokens, [T, D] in bf16.
+    mixture-of-experts layer for up to 128 tokens (more go in slices of 128), [T, D] in bf16.
 
     x bf16 [T, D]; ids int32 and weights float32 [T, k] (fp4_moe_route); an id outside [0, E) leaves its slot out.
     The experts' matrices are MXFP4 from fp4_quantize_weights with this ``block``: w13q uint8 [E, 2I, D/2] and w13s

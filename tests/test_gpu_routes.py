@@ -109,3 +109,22 @@ def test_route_of_many_tokens(T, E, D, k):
     assert bool((chosen >= z.topk(k, dim=1)[0] - 2 * d[:, None]).all())
     want = torch.softmax(z, 1).gather(1, at)
     assert bool(((p.double() - want).abs() <= (2 * d[:, None] + 1e-6) * want).all())
+
+
+@pytest.mark.parametrize("T,E,k", [(3, 8, 2), (96, 8, 6)])
+def test_experts_token_without_a_used_slot_gets_zeros_whatever_it_holds(T, E, k):
+    """In two launches and in five."""
+    D, I = 1024, 256
+    say(f"experts T {T}: no slot of a NaN token used")
+    gen = torch.Generator(DEV).manual_seed(T)
+    w = [torch.randint(0, 256, (E, 2 * I, D // 2), dtype=torch.uint8, device=DEV, generator=gen),
+         torch.randint(118, 126, (E, 2 * I, D // 32), dtype=torch.uint8, device=DEV, generator=gen),
+         torch.randint(0, 256, (E, D, I // 2), dtype=torch.uint8, device=DEV, generator=gen),
+         torch.randint(118, 126, (E, D, I // 32), dtype=torch.uint8, device=DEV, generator=gen)]
+    x, p = torch.randn(T, D, device=DEV, generator=gen).bfloat16(), torch.rand(T, k, device=DEV, generator=gen)
+    ids = torch.randint(0, E, (T, k), dtype=torch.int32, device=DEV, generator=gen)
+    ids[1] = -1
+    want = F.fp4_moe_experts(x, ids, p, *w, 32)
+    x[1] = float("nan")
+    y = F.fp4_moe_experts(x, ids, p, *w, 32)
+    assert bool((y[1] == 0).all()) and torch.equal(y.view(torch.int16), want.view(torch.int16))
