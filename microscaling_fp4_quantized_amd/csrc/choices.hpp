@@ -22,7 +22,8 @@ inline Grid grid_of(int64_t groups, int threads) {
 // ---- 8-bit GEMM --------------------------------------------------------------------------------------------------------
 
 // The tile shapes: rows of X, rows of W, workgroups that run at once on a CU, and the time of one scale block of K in us
-// (one round of workgroups at K = 4096, the launch taken off). The least rounds times a round's time is taken; up
+// (one round of workgroups at K = 4096, the launch taken off; at a short K the start and end of a tile, which grow with it, count
+// for more than this says, and nothing was fitted there). The least rounds times a round's time is taken; up
 // to 8 rows of X, which cost little beside W, go to 16 x 16. The first three split K over the waves of a workgroup
 // (gemm_fp8_split.hip); several of their workgroups run on a CU, sharing what it reads.
 //   rows x N (K 4096)   16 x 16   16 x 32   32 x 32   64 x 64   128 x 64   128 x 128   the same, two a CU   256 x 256   (us)
@@ -83,6 +84,10 @@ inline bool few_pairs(int T, int k, int64_t E, int64_t D, int64_t I) {
 // hide each other's starts. Two waves and one, us a call: 64 tokens, 6 of 64 of 4096 x 1408 (down alone) 145 and 143;
 // 8 of 128 of 2048 x 768 (down) 90 and 86; 4 of 256 of 768 x 512 (both) 42 and 37; 51 tokens, 2 of 128 of 4992 x 128
 // (down) 50 and 43; but up alone, K = 4096, 82 and 85. Four and eight waves at the first: 168 and 230.
+// Where the two meet (6 of 64 experts, one / two waves in the product of that K, us a call): K of the first 1536 56.4 / 58.4, 2048
+// 66.0 / 68.8, 2560 86.0 / 82.4, 4096 124 / 111 for 64 tokens, and 41.9 / 44.3, 49.2 / 51.4, 55.2 / 57.8, 91.9 / 82.8 for 16;
+// of the second, 64 tokens, 1536 91.7 / 93.4, 2048 112 / 112, 2560 138 / 130. So from 1536 to about 2048 one wave would be up to 4%
+// sooner than the two that are taken.
 constexpr int kShortK = 1536;
 inline int expert_waves(int64_t K, int64_t workgroups) { return workgroups < 1024 ? 8 : K <= kShortK ? 1 : 2; }
 

@@ -10,8 +10,8 @@
 // cross-lane steps without LDS. The norm keeps its row in registers between the sum of squares and
 // the scaling. The sum of squares, the mean and the normalised row are float32.
 //
-// Measured: norm with residual 16384 x 8192 157 us (944 MB, 6.0 TB/s: a copy's rate), 1 x 4096 4.6 us a call (launch
-// and host); activations 2047 x 4096 6.0 us, weights 14336 x 4096 30.5 us (176 MB, 5.8 TB/s).
+// Measured, us of a call among others: norm with residual 16384 x 8192 155 (944 MB, 6.1 TB/s: a copy's rate), 1 x 4096 3.9-4.7
+// (launch and host; 2.4 on the GPU); activations 2047 x 4096 6.0, weights 14336 x 4096 30.3 (176 MB, 5.8 TB/s).
 #include <type_traits>
 
 #include "fp8_device.hpp"

@@ -18,8 +18,8 @@
 //  * Workgroup i runs on XCD i % 8; each XCD takes a contiguous range of tiles, M fastest within groups
 //    of 4 tile rows, so tiles running together share X and W in that XCD's L2.
 //
-// Measured: 2048 x 14336, K = 4096: 106 us (2.26 PFLOP/s); 8192 x 28672, K = 8192: 1565 us (2.46 PFLOP/s; the library's
-// product with ONE scale for each operand, so without the FMAs, 1294 us, and 103 us at the first size).
+// Measured, us of a call among others: 2048 x 14336, K = 4096: 104 (2.31 PFLOP/s); 8192 x 28672, K = 8192: 1533 (2.51
+// PFLOP/s; the library's product with ONE scale for each operand, so without the FMAs, 1185, and 97 at the first size).
 #include <atomic>
 #include <type_traits>
 
@@ -283,9 +283,10 @@ __device__ __forceinline__ void map_tile(int L, int tiles_m, int tiles_n, int& t
 // multiplies it; group 1 multiplies the second half of stage s - 1, whose fragments it has in registers, then
 // reads stage s and multiplies its first half. By the barrier every fragment of stage s has been read, so its
 // buffer is refilled with stage s + 2 after it. Needs K >= 512.
-// With all eight waves reading, then multiplying, between the same barriers (ring_tile's order) the matrix pipe was busy
-// 58% of the time: 2048 x 14336 x 4096 115 us and 8192 x 28672 x 8192 1780 us, against 106 and 1570 (65% busy, at the
-// 1.77 GHz that the power limit leaves; without any DMA 1180, without the scales' FMAs 1455).
+// With all eight waves reading, then multiplying, between the same barriers (ring_tile's order): 2048 x 14336 x 4096 115 us and
+// 8192 x 28672 x 8192 1780, against 106 and 1570 at that time; without any DMA the latter took 1180, without the scales' FMAs
+// 1455. At the large size the matrix pipe is busy 63% of the time at 1.88 GHz, the clock that power leaves
+// (profiles/gemm_fp8_turns_sq_counters.txt).
 // (Covering what is left after whole rounds of tiles with 192-wide ones, so that the last round is full, changed nothing
 // at 2048 x 14336: with fewer CUs at work the others' clock rises.)
 constexpr int PBM = 256, PBN = 256, PWM = 64, PWN = 128, PFM = PWM / 16, PFN = PWN / 16;

@@ -11,9 +11,9 @@
 //    and its result gives each lane 4 features of ONE token: acc += p * (xs * ws) is four float32 FMAs.
 //  * The waves' float32 sums meet once, through LDS, in the order of the waves: the result does not depend on timing.
 //  * Rows past M and N read as zero and are not stored.
-// Bound by W's bytes from HBM where N is large (K = 4096, N = 14336: 1 row 10.7 us, 16 rows 10.6, 58.7 MB, 5.5 TB/s; K =
-// 8192, N = 28672: 1 row 40.5 us, 5.8 TB/s), by what a CU reads from L2 and by latency where it is small (K = 4096, N =
-// 4096: 1 row 4.9 us, 64 rows 6.5 us; 37 x 4100 7.2 us, and 12.1 through 32 x 32 tiles of the ring, a stage at
+// Bound by W's bytes from HBM where N is large (K = 4096, N = 14336: 1 row 10.7 us, 16 rows 10.6, 58.7 MB, 5.5 TB/s, and 10.1 a
+// call among others; K = 8192, N = 28672: 1 row 40.5 us, 5.8 TB/s), by what a CU reads from L2 and by latency where it is small (K = 4096, N =
+// 4096: 1 row 4.9 us, 64 rows 6.5 us; 37 x 4100 7.2 us (6.6 among others), and 12.1 through 32 x 32 tiles of the ring, a stage at
 // a time). Eight waves a tile 5.3, 16 waves 5.7 us at 16 x 4096 (four 5.2); three slots a wave no faster.
 #include <atomic>
 

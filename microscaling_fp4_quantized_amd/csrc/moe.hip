@@ -22,7 +22,7 @@
 //   combine    y_t = sum_j p_tj * down, over the slots in order, rounded once to bf16
 // Few pairs take two launches instead (few_experts below).
 //
-// 64 tokens, 6 of 64 experts of 4096 x 1408 (588 MB of weights): 145 us; up 82 us (4.8 TB/s), down 52 (3.8), the other
+// 64 tokens, 6 of 64 experts of 4096 x 1408 (588 MB of weights): 143 us; up 79 us (5.0 TB/s), down 52 (3.8), the other
 // three 5 each. The same workgroups without products, tokens and scales, streaming W alone, take 69 and 43: what is
 // left to a plain read of the weights (98 us) is mostly the starts and ends of workgroups.
 #include <atomic>
@@ -664,7 +664,7 @@ hipError_t launch_experts(const ExpertArgs& A, int slots, hipStream_t st) {
 // Items go to the waves in turn. A wave splits the vectors of two or four items at a time
 // into its own LDS, and streams each item's 32 or 16 rows x 128 bytes of W through its own ring; a single token's columns
 // are repeated over the instruction's 16. 8 of 128 experts of 2048 x 768, one token: 25 us
-// in five launches, 15 in two; four tokens 41 and 25, eight tokens 47 and 50. 16 waves for the second launch: no faster.
+// in five launches, 13 in two; four tokens 41 and 25, eight tokens 47 and 50. 16 waves for the second launch: no faster.
 constexpr int kFewWaves = 8;
 constexpr int kHalfTerms = 256 * kCols;  // bytes of the terms of a half slice
 template <bool UP>
