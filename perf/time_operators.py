@@ -79,7 +79,7 @@ def counters(path, kernel):
     found = collections.defaultdict(list)
     with open(path) as f:
         for r in csv.DictReader(f):
-            if "fp4::" in r["Kernel_Name"] and kernel in r["Kernel_Name"]:
+            if "fp4::" in r["Kernel_Name"] and kernel in short(r["Kernel_Name"]):
                 found[short(r["Kernel_Name"]), int(r["Grid_Size"]), r["Counter_Name"]].append(float(r["Counter_Value"]))
     for (name, grid, counter), v in found.items():
         print(f"{name:44s} {grid:10d} {counter:28s} {statistics.mean(v):16.0f}  over {len(v)} dispatches")

@@ -33,5 +33,5 @@ def test_counters(tool, tmp_path, capsys):
         f"void fp4::(anonymous namespace)::{k}(int),64,SQ_WAVES,{v}\n" for k, v in (("a", 1), ("a", 3), ("b", 100))))
     tool.counters(str(path), "a")
     lines = [line.split() for line in capsys.readouterr().out.splitlines()]
-    assert [line[0] for line in lines if line[0] == "a"] == ["a"]
+    assert [line[0] for line in lines] == ["a"]
     assert lines[0][1:4] == ["64", "SQ_WAVES", "2"] and lines[0][-2:] == ["2", "dispatches"]
