@@ -1,8 +1,8 @@
 /*
  * fp4.h - C ABI of the MI355X (gfx950) online FP4 inference path.
  *
- * Three calls, matching the method's statement of the problem (the 8-bit and mixture-of-experts calls of a model's other
- * layers stand at the end):
+ * Three calls, matching the method's statement of the problem (the 8-bit, mixture-of-experts and attention calls of a
+ * model's other layers stand at the end):
  *
  *   fp4_rotate_quantize   online: block-wise Hadamard rotation of bf16
  *                         activations fused with microscaled FP4 quantization.
@@ -377,6 +377,96 @@ FP4_API int fp4_moe_experts(const void *X, int64_t T, int64_t D, int64_t ldx, co
                             int k, int64_t E, int64_t I, int block, const uint8_t *W13q, const uint8_t *W13s,
                             const uint8_t *W2q, const uint8_t *W2s, void *Y, void *workspace,
                             size_t workspace_bytes, void *stream);
+
+/*
+ * Attention over a paged key-value cache, and the call that fills it.
+ *
+ * The cache: pages of page_size tokens, for every token `heads` keys and values of `dim` numbers each, in bf16 or as E4M3
+ * codes with one float32 scale for a token's key (value) of a head: scale = fl32(a' * fl32(1 / 448)), code = e4m3(fl32(x *
+ * fl32(448 / a'))), a' = max(largest magnitude, 2^-100), as above for groups of 128. Token i of sequence b lies at place
+ * i % page_size of page table[b, i / page_size]; lengths[b] says how many tokens the sequence has, those that a call brings
+ * among them. Both are read on the device, so a captured graph follows them.
+ * Whatever lies in places that no visible token has (NaN too) changes nothing.
+ *
+ *  dtype       FP4_KV_BF16 or FP4_KV_E4M3.   heads 1..1024.   dim 64, 128 or 256.
+ *  page_size   a power of two, 16..1024.   pages 1..2^31 - 1.
+ *  k, v        device, 16-byte aligned. Strides in elements for both, >= dim, at most 2^40 and multiples of 8 (E4M3:
+ *              16): pages of [heads, page_size, dim], of [page_size, heads, dim], keys and values page by page in
+ *              one buffer, or any other order. The dims of a token's head lie together.
+ *  k_scales, v_scales  device float, 4-byte aligned, strides >= 1 and at most 2^40; NULL exactly with FP4_KV_BF16.
+ *  table       device int [batch, cols], row stride table_stride >= cols. A page id outside [0, pages) (-1, say) is no page: its
+ *              tokens are not visible and nothing is written for them.
+ *  cols        >= 1, cols * page_size <= 2^30: tokens past that are as tokens of no page.
+ *  lengths     device int [batch]; below 0 counts as 0, above 2^30 as 2^30.
+ *  batch       1..65535, batch * query heads <= 2^22.
+ */
+enum { FP4_KV_BF16 = 0, FP4_KV_E4M3 = 1 };
+typedef struct fp4_kv_cache {
+  void *k, *v;
+  float *k_scales, *v_scales;
+  int64_t pages, page_stride, head_stride, token_stride;
+  int64_t scale_page_stride, scale_head_stride, scale_token_stride;
+  const int *table;
+  int64_t table_stride, cols;
+  const int *lengths;
+  int64_t batch;
+  int dtype, heads, dim, page_size;
+} fp4_kv_cache;
+
+/*
+ * New tokens stand in rows: those of sequence b in rows starts[b] .. starts[b + 1] - 1, the last of them being the sequence's
+ * last token, so row t is its token lengths[b] - (starts[b + 1] - t). starts is device int [batch + 1], not falling, from 0 to at
+ * most T; rows from starts[batch] on belong to nobody: they are not read, and what they would write is left as it was. starts
+ * NULL: T == batch, one new token each.
+ *
+ * fp4_kv_append - keys and values of T rows into the cache, keys and queries rotated on the way:
+ *   pair (a, b) -> (a cos w - b sin w, a sin w + b cos w),  w = position * freqs[f]
+ * for the first `rotated` dims of every head; pair f is dims (f, rotated / 2 + f), or (2 f, 2 f + 1) if interleaved. The position is
+ * the token's place in its sequence, or positions[axes[f], t]: several axes (time, height, width) each with frequencies of their
+ * own. The angle is taken in float64 before its whole turns are dropped, the rotation is float32, and the result is rounded
+ * once, to bf16 or to E4M3 under its scale.
+ *  K, V         device bf16, rows of cache->heads heads of dim: strides of rows and heads in elements, multiples of 8, at most
+ *               2^40; 16-byte aligned.
+ *  Q, q_heads   device bf16, rows of q_heads heads in the same way, or NULL and 0: Q_out[t, h] is the rotated Q[t, h]. Q_out may be
+ *               Q with the same strides; no other overlap of buffers is allowed.
+ *  freqs        device float [rotated / 2], or NULL with rotated 0: nothing is rotated.   rotated: a multiple of 16 up to dim.
+ *  positions    device int [n_axes, T], or NULL.   axes: device int [rotated / 2], or NULL: axis 0. An axis outside
+ *               [0, n_axes) does not rotate.   n_axes: 1..16 with positions, else 0.
+ *  T            1..2^24, T * (q_heads + 2 * heads) <= 2^30.
+ * Two rows of one cache place (a page that stands twice in the table) leave either's values there.
+ * One launch on `stream`. Errors: FP4_E_NULLPTR, FP4_E_SHAPE, FP4_E_FORMAT (dtype), FP4_E_ALIGN.
+ */
+FP4_API int fp4_kv_append(const fp4_kv_cache *cache, const int *starts, int64_t T, const void *K, int64_t k_row, int64_t k_head,
+                          const void *V, int64_t v_row, int64_t v_head, const void *Q, int64_t q_row, int64_t q_head,
+                          int q_heads, void *Q_out, int64_t out_row, int64_t out_head, const float *freqs, int rotated,
+                          int interleaved, const int *positions, const int *axes, int n_axes, void *stream);
+
+/*
+ * fp4_attention_decode, fp4_attention_prompt - for row t, the token i of its sequence, and query head h:
+ *   Out[t, h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q_h . k_j - max),  key-value head h / (q_heads / heads),
+ * over the visible tokens j of the sequence: j <= i and (window == 0 or i - j < window or j < sinks).
+ * fp4_attention_decode is for one new token of each sequence (row b belongs to sequence b); fp4_attention_prompt for many.
+ * Rows that see no token get zeros. Scores, p's sum and the output's sum are float32; p is rounded to bf16 for the product with v.
+ * A NaN or infinity in a visible key or value, or in q, gives outputs of that row and head that are not numbers, and
+ * no others.
+ *  Q            device bf16, rows of q_heads heads of dim: strides as above. q_heads a multiple of cache->heads, up to 1024.
+ *  scale        finite and positive.   window, sinks >= 0 (above 2^30 they count as 2^30).
+ *  Out          device bf16 [T, q_heads, dim], 16-byte aligned.
+ *  T            1..2^24, T * q_heads <= 2^30.
+ *  workspace, workspace_bytes  device buffer of at least FP4_ATTENTION_WORKSPACE_BYTES(T, batch, q_heads, heads, dim) bytes, 16-byte
+ *               aligned, the call's alone while it runs (T = batch for the decode call).
+ * Two launches at most, on `stream`. Results do not depend on timing: partial sums meet in a fixed order.
+ * Errors: FP4_E_NULLPTR, FP4_E_SHAPE (also scale, window, sinks and a short workspace), FP4_E_FORMAT (dtype), FP4_E_ALIGN.
+ */
+#define FP4_ATTENTION_PIECES(blocks) ((blocks) >= 512 ? 1 : 512 / (blocks))
+#define FP4_ATTENTION_WORKSPACE_BYTES(T, batch, q_heads, heads, dim) \
+  (((size_t)FP4_ATTENTION_PIECES((heads) * (((q_heads) / (heads) + 15) / 16)) + (size_t)(batch)) * (size_t)(q_heads) * ((size_t)(dim) + 2) * 4)
+FP4_API int fp4_attention_decode(const fp4_kv_cache *cache, const void *Q, int64_t q_row, int64_t q_head, int q_heads, float scale,
+                                 int64_t window, int64_t sinks, void *Out, void *workspace, size_t workspace_bytes,
+                                 void *stream);
+FP4_API int fp4_attention_prompt(const fp4_kv_cache *cache, const int *starts, int64_t T, const void *Q, int64_t q_row,
+                                 int64_t q_head, int q_heads, float scale, int64_t window, int64_t sinks, void *Out,
+                                 void *workspace, size_t workspace_bytes, void *stream);
 
 /* Message for the last non-OK status returned on this thread ("" if none). */
 FP4_API const char *fp4_last_error(void);

@@ -14,7 +14,8 @@ def __getattr__(name):
     if name in ("fp4_rotate_quantize", "fp4_quantize_weights", "fp4_linear", "fp4_rotate_quantize_linear",
                 "fp4_abi_version", "Fp4Error", "load_library", "library_path", "group_size", "FP4_MXFP4",
                 "FP4_NVFP4", "fp8_quantize", "fp8_quantize_weights", "fp8_add_rmsnorm_quantize", "fp8_linear",
-                "fp4_moe_route", "fp4_moe_experts", "moe_workspace_bytes"):
+                "fp4_moe_route", "fp4_moe_experts", "moe_workspace_bytes", "fp4_kv_append", "fp4_attention_decode",
+                "fp4_attention_prompt", "attention_workspace_bytes"):
         from . import binding
         value = globals()[name] = getattr(binding, name)  # found at once from now on
         return value

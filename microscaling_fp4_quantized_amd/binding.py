@@ -31,6 +31,10 @@ __all__ = [
     "fp4_moe_route",
     "fp4_moe_experts",
     "moe_workspace_bytes",
+    "fp4_kv_append",
+    "fp4_attention_decode",
+    "fp4_attention_prompt",
+    "attention_workspace_bytes",
     "fp4_abi_version",
     "group_size",
 ]
@@ -48,6 +52,16 @@ class Fp4Error(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"[{_STATUS.get(status, status)}] {message}")
         self.status = status
+
+
+class _KvCache(ctypes.Structure):
+    """fp4_kv_cache of include/fp4.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scales", "v_scales")] + \
+        [(n, ctypes.c_int64) for n in ("pages", "page_stride", "head_stride", "token_stride", "scale_page_stride",
+                                       "scale_head_stride", "scale_token_stride")] + \
+        [("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("cols", ctypes.c_int64),
+         ("lengths", ctypes.c_void_p), ("batch", ctypes.c_int64)] + \
+        [(n, ctypes.c_int) for n in ("dtype", "heads", "dim", "page_size")]
 
 
 def library_path() -> str:
@@ -94,6 +108,14 @@ def load_library() -> ctypes.CDLL:
     lib.fp4_moe_experts.argtypes = [vp, i64, i64, i64, vp, vp, i32, i64, i64, i32, vp, vp, vp, vp, vp, vp,
                                     ctypes.c_size_t, vp]
     lib.fp4_moe_experts.restype = i32
+    cache = ctypes.POINTER(_KvCache)
+    lib.fp4_kv_append.argtypes = [cache, vp, i64, vp, i64, i64, vp, i64, i64, vp, i64, i64, i32, vp, i64, i64, vp, i32, i32, vp,
+                                  vp, i32, vp]
+    lib.fp4_kv_append.restype = i32
+    lib.fp4_attention_decode.argtypes = [cache, vp, i64, i64, i32, ctypes.c_float, i64, i64, vp, vp, ctypes.c_size_t, vp]
+    lib.fp4_attention_decode.restype = i32
+    lib.fp4_attention_prompt.argtypes = [cache, vp, i64, vp, i64, i64, i32, ctypes.c_float, i64, i64, vp, vp, ctypes.c_size_t, vp]
+    lib.fp4_attention_prompt.restype = i32
     lib.fp4_last_error.argtypes = []
     lib.fp4_last_error.restype = ctypes.c_char_p
     lib.fp4_abi_version.argtypes = []
@@ -604,6 +626,173 @@ def fp4_moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w
              int(block), w13q.data_ptr(), w13s.data_ptr(), w2q.data_ptr(), w2s.data_ptr(), out.data_ptr(),
              ws.data_ptr(), ws.numel())
     return out
+
+
+def _head_rows(t, name, what):
+    """A 3-D bf16 CUDA tensor [rows, heads, dim] whose heads lie together: its shape, then its strides of rows and heads."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.dtype != torch.bfloat16 or not t.is_cuda or t.stride(2) != 1:
+        raise ValueError(f"{name}: {what} must be a 3-D bf16 CUDA tensor with unit stride in its last dimension")
+    T, H, D = t.shape
+    # the stride of a dimension of one says nothing: torch may give any
+    return T, H, D, t.stride(0) if T > 1 else H * D, t.stride(1) if H > 1 else D
+
+
+def _strides(t, least):
+    """Strides of pages, heads and tokens of a cache tensor; one of a dimension of one is any that suits."""
+    return [s if n > 1 else max(least, 1) for n, s in zip(t.shape[:3], t.stride()[:3])]
+
+
+def _kv_cache(name, k_pages, v_pages, table, lengths, k_scales, v_scales):
+    """The cache's description, and its device."""
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4 or not k_pages.is_cuda or \
+            k_pages.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise ValueError(f"{name}: k_pages must be a 4-D bf16 or float8_e4m3fn CUDA tensor [pages, heads, page size, dim]")
+    P, H, S, D = k_pages.shape
+    strides = _strides(k_pages, D)
+    if not isinstance(v_pages, torch.Tensor) or v_pages.dtype != k_pages.dtype or v_pages.shape != k_pages.shape or \
+            _strides(v_pages, D) != strides or k_pages.stride(3) != 1 or v_pages.stride(3) != 1:
+        raise ValueError(f"{name}: v_pages must be like k_pages, {k_pages.dtype} {tuple(k_pages.shape)} with its strides, and the "
+                         "dims of a token's head together in both")
+    e4m3 = k_pages.dtype == torch.float8_e4m3fn
+    scale_strides = [0, 0, 0]
+    if e4m3:
+        for t, what in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+            if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.shape != (P, H, S):
+                raise ValueError(f"{name}: {what} must be a float32 CUDA tensor of shape {(P, H, S)} with an 8-bit cache")
+        scale_strides = _strides(k_scales, 1)
+        if _strides(v_scales, 1) != scale_strides:
+            raise ValueError(f"{name}: k_scales and v_scales must have the same strides")
+    elif k_scales is not None or v_scales is not None:
+        raise ValueError(f"{name}: a bf16 cache has no scales")
+    if not isinstance(table, torch.Tensor) or table.dim() != 2 or table.dtype != torch.int32 or not table.is_cuda or \
+            (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"{name}: table must be a 2-D int32 CUDA tensor with unit column stride")
+    B, cols = table.shape
+    _expect(lengths, (B,), torch.int32, name, "lengths")
+    _same_device(name, k_pages.device, v_pages, k_scales, v_scales, table, lengths)
+    return _KvCache(k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr() if e4m3 else None,
+                    v_scales.data_ptr() if e4m3 else None, P, *strides, *scale_strides, table.data_ptr(),
+                    table.stride(0) if B > 1 else cols, cols, lengths.data_ptr(), B, int(e4m3), H, D, S)
+
+
+def fp4_kv_append(k: torch.Tensor, v: torch.Tensor, k_pages, v_pages, table, lengths, starts=None, q=None, freqs=None,
+                  positions=None, axes=None, interleaved: bool = False, k_scales=None, v_scales=None, out=None):
+    """Keys and values of new tokens into a paged cache, keys and queries rotated on the way; the rotated queries, or None.
+
+    k, v bf16 [T, heads, dim], q bf16 [T, query heads, dim] or None: rows of any strides, slices of one projection's output, say.
+    k_pages, v_pages bf16 or float8_e4m3fn [pages, heads, page size, dim] in any order of memory, 8-bit ones with k_scales
+    and v_scales float32 [pages, heads, page size]; table int32 [B, columns] the pages of each sequence (-1: none); lengths
+    int32 [B] its tokens, the new ones among them; starts int32 [B + 1] the rows of each sequence, or None for one each.
+    freqs float32 [n / 2]: the first n dims of a head are rotated by position * freqs, pairs (f, n / 2 + f), or (2 f, 2 f + 1) with
+    ``interleaved``; None: nothing is. positions int32 [T] or [axes, T] in place of the tokens' places, axes int32 [n / 2] the axis
+    of each frequency. ``out`` may pass the rotated queries' buffer, any strides, q itself too."""
+    name = "fp4_kv_append"
+    lib = load_library()
+    T, H, D, k_row, k_head = _head_rows(k, name, "k")
+    dev = k.device
+    cache = _kv_cache(name, k_pages, v_pages, table, lengths, k_scales, v_scales)
+    Tv, Hv, Dv, v_row, v_head = _head_rows(v, name, "v")
+    if (H, D) != (cache.heads, cache.dim) or (Tv, Hv, Dv) != (T, H, D):
+        raise ValueError(f"{name}: k and v must both be [T, {cache.heads}, {cache.dim}] as the cache, got {tuple(k.shape)} and "
+                         f"{tuple(v.shape)}")
+    if starts is not None:
+        _expect(starts, (cache.batch + 1,), torch.int32, name, "starts")
+    elif T != cache.batch:
+        raise ValueError(f"{name}: without starts there must be one row for each of {cache.batch} sequences, got {T}")
+    half = n_axes = 0
+    if freqs is not None:
+        if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
+            raise ValueError(f"{name}: freqs must be a 1-D tensor")
+        half = freqs.shape[0]
+        _expect(freqs, (half,), torch.float32, name, "freqs")
+        if positions is not None:
+            if not isinstance(positions, torch.Tensor) or positions.dim() not in (1, 2):
+                raise ValueError(f"{name}: positions must be a tensor [T] or [axes, T]")
+            n_axes = positions.shape[0] if positions.dim() == 2 else 1
+            _expect(positions, (n_axes, T) if positions.dim() == 2 else (T,), torch.int32, name, "positions")
+        if axes is not None:
+            if positions is None:
+                raise ValueError(f"{name}: axes need positions")
+            _expect(axes, (half,), torch.int32, name, "axes")
+    elif q is not None or positions is not None or axes is not None:
+        raise ValueError(f"{name}: q, positions and axes need freqs")
+    Hq = q_row = q_head = out_row = out_head = 0
+    if q is not None:
+        Tq, Hq, Dq, q_row, q_head = _head_rows(q, name, "q")
+        if (Tq, Dq) != (T, D):
+            raise ValueError(f"{name}: q must be [{T}, heads, {D}], got {tuple(q.shape)}")
+        if out is None:
+            out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+        To, Ho, Do, out_row, out_head = _head_rows(out, name, "out")
+        if (To, Ho, Do) != (T, Hq, D):
+            raise ValueError(f"{name}: out must have the shape of q, {(T, Hq, D)}, got {tuple(out.shape)}")
+        if out.data_ptr() == q.data_ptr():  # in place: strides that say nothing are the same ones
+            out_row, out_head = (q_row if T == 1 else out_row), (q_head if Hq == 1 else out_head)
+    elif out is not None:
+        raise ValueError(f"{name}: out is for the rotated queries, and there are none")
+    _same_device(name, dev, k_pages, v, starts, q, freqs, positions, axes, out)
+    _enqueue(lib.fp4_kv_append, dev, ctypes.byref(cache), _data(starts), T, k.data_ptr(), k_row, k_head, v.data_ptr(), v_row, v_head,
+             _data(q), q_row, q_head, Hq, _data(out), out_row, out_head, _data(freqs), 2 * half, int(bool(interleaved)),
+             _data(positions), _data(axes), n_axes)
+    return out
+
+
+def _data(t):
+    return None if t is None else t.data_ptr()
+
+
+def attention_workspace_bytes(T: int, B: int, q_heads: int, heads: int, dim: int) -> int:
+    """FP4_ATTENTION_WORKSPACE_BYTES(T, B, q_heads, heads, dim) of include/fp4.h."""
+    blocks = heads * ((q_heads // heads + 15) // 16)
+    return ((1 if blocks >= 512 else 512 // blocks) + B) * q_heads * (dim + 2) * 4
+
+
+def _attention(name, q, cache, scale, window, sinks, starts, out, workspace):
+    T, Hq, D, q_row, q_head = _head_rows(q, name, "q")
+    dev = q.device
+    c = _kv_cache(name, *cache)
+    if D != c.dim or Hq % c.heads or not Hq:
+        raise ValueError(f"{name}: q must have a multiple of the cache's {c.heads} heads of {c.dim}, got {tuple(q.shape)}")
+    if starts is None:
+        if T != c.batch:
+            raise ValueError(f"{name}: there must be one row for each of {c.batch} sequences, got {T}")
+    else:
+        _expect(starts, (c.batch + 1,), torch.int32, name, "starts")
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+    else:
+        _expect(out, (T, Hq, D), torch.bfloat16, name, "out")
+    ws = _workspace(workspace, attention_workspace_bytes(T, c.batch, Hq, c.heads, D), name, dev)
+    _same_device(name, dev, cache[0], starts, out, ws)
+    rows = () if starts is None else (starts.data_ptr(), T)
+    _enqueue(getattr(load_library(), name), dev, ctypes.byref(c), *rows, q.data_ptr(), q_row, q_head, Hq,
+             D ** -0.5 if scale is None else scale, int(window), int(sinks), out.data_ptr(), ws.data_ptr(), ws.numel())
+    return out
+
+
+def fp4_attention_decode(q: torch.Tensor, k_pages, v_pages, table, lengths, scale=None, window: int = 0, sinks: int = 0,
+                         k_scales=None, v_scales=None, out=None, workspace="auto"):
+    """Attention of one new token of each sequence over a paged cache: bf16 [B, query heads, dim].
+
+    q bf16 [B, query heads, dim], a multiple of the cache's heads; the cache as in fp4_kv_append, the new tokens in it. scale
+    defaults to dim ** -0.5. A sequence's last token sees all of its tokens, or with ``window`` the last ``window`` of them and the first
+    ``sinks``; one of no tokens gets zeros. workspace: "auto", or a uint8 CUDA tensor of at least
+    attention_workspace_bytes(B, B, query heads, heads, dim) that no other call uses meanwhile."""
+    return _attention("fp4_attention_decode", q, (k_pages, v_pages, table, lengths, k_scales, v_scales), scale, window, sinks, None,
+                      out, workspace)
+
+
+def fp4_attention_prompt(q: torch.Tensor, k_pages, v_pages, table, lengths, starts, scale=None, window: int = 0, sinks: int = 0,
+                         k_scales=None, v_scales=None, out=None, workspace="auto"):
+    """Attention of many new tokens of each sequence over a paged cache, [T, query heads, dim] in bf16: as
+    fp4_attention_decode, for each token over those up to itself.
+
+    The rows starts[b] .. starts[b + 1] of q (starts int32 [B + 1]) are the last tokens of sequence b; rows from starts[B] on
+    are left as they were. workspace: at least attention_workspace_bytes(T, B, query heads, heads, dim)."""
+    if starts is None:
+        raise ValueError("fp4_attention_prompt: starts is needed")
+    return _attention("fp4_attention_prompt", q, (k_pages, v_pages, table, lengths, k_scales, v_scales), scale, window, sinks, starts,
+                      out, workspace)
 
 
 def fp4_abi_version() -> int:

@@ -35,6 +35,9 @@ SOURCES = [
     "gemm_fp8_split.hip",
     "gemm_fp8_ring.hip",
     "moe.hip",
+    "kv_append.hip",
+    "attention_decode.hip",
+    "attention_prompt.hip",
     "fp4_abi.cpp",
 ]
 

@@ -1,0 +1,52 @@
+// Device helpers that the attention kernels share: matrix operands from cache values, and maxima and sums across a wave.
+#pragma once
+
+#include "paged.hpp"
+
+namespace fp4 {
+
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kNever = -__builtin_inff();  // the score of a token that a row does not see
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Both halves of the wave (lane ^ 32), and both halves of each half (lane ^ 16), side by side.
+template <int X>
+__device__ __forceinline__ void lane_swap(unsigned v, unsigned& a, unsigned& b) {
+  static_assert(X == 16 || X == 32, "the two swaps there are");
+  const auto r = X == 32 ? __builtin_amdgcn_permlane32_swap(v, v, false, false) : __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  a = r[0];
+  b = r[1];
+}
+template <int X>
+__device__ __forceinline__ float max_across(float v) {
+  unsigned a, b;
+  lane_swap<X>(__float_as_uint(v), a, b);
+  return fmaxf(__uint_as_float(a), __uint_as_float(b));
+}
+template <int X>
+__device__ __forceinline__ float sum_across(float v) {
+  unsigned a, b;
+  lane_swap<X>(__float_as_uint(v), a, b);
+  return __uint_as_float(a) + __uint_as_float(b);
+}
+
+// Four E4M3 codes -> two words of bf16 (exact).
+__device__ __forceinline__ v2u bf16_of_codes(unsigned c) {
+  const v2bf lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, false), hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, true);
+  return v2u{__builtin_bit_cast(unsigned, lo), __builtin_bit_cast(unsigned, hi)};
+}
+
+// Two floats -> a word of bf16, a in the low half (to nearest even).
+__device__ __forceinline__ unsigned bf16_pair(float a, float b) {
+  const v2bf v{(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(unsigned, v);
+}
+
+// The low or the high halves of two words, a's in the low half.
+__device__ __forceinline__ unsigned low_halves(unsigned a, unsigned b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
+__device__ __forceinline__ unsigned high_halves(unsigned a, unsigned b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
+
+}  // namespace fp4

@@ -10,6 +10,7 @@
 #include "../../include/fp4.h"
 #include "common.hpp"
 #include "operators.hpp"
+#include "paged.hpp"
 
 namespace {
 
@@ -131,6 +132,90 @@ int check_fp8_rows(const char* who, const void* X, int64_t M, int64_t K, int64_t
   if (!aligned(codes, 16) || !aligned(scales, 4))
     return fail(FP4_E_ALIGN, "%s: codes must be 16-byte aligned, scales 4-byte aligned", who);
   return FP4_OK;
+}
+
+// The cache of the attention calls and the shapes that go with it, as the kernels take them.
+int check_cache(const char* who, const fp4_kv_cache* c, int64_t q_heads, fp4::Paged* out) {
+  if (!c || !c->k || !c->v || !c->table || !c->lengths) return fail(FP4_E_NULLPTR, "%s: cache pointers must be non-NULL", who);
+  if (c->dtype != FP4_KV_BF16 && c->dtype != FP4_KV_E4M3) return fail(FP4_E_FORMAT, "%s: unknown cache dtype %d", who, c->dtype);
+  const bool e4m3 = c->dtype == FP4_KV_E4M3;
+  if ((c->k_scales != nullptr) != e4m3 || (c->v_scales != nullptr) != e4m3)
+    return fail(FP4_E_NULLPTR, "%s: k_scales and v_scales belong to an E4M3 cache, and only there", who);
+  if (c->heads < 1 || c->heads > 1024 || (c->dim != 64 && c->dim != 128 && c->dim != 256))
+    return fail(FP4_E_SHAPE, "%s: need 1 to 1024 heads of 64, 128 or 256 (heads=%d dim=%d)", who, c->heads, c->dim);
+  if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)))
+    return fail(FP4_E_SHAPE, "%s: page_size=%d is no power of two from 16 to 1024", who, c->page_size);
+  if (c->pages < 1 || c->pages > 0x7FFFFFFF) return fail(FP4_E_SHAPE, "%s: pages=%lld not in 1 .. 2^31 - 1", who, (long long)c->pages);
+  const int64_t far = (int64_t)1 << 40;
+  for (const int64_t s : {c->page_stride, c->head_stride, c->token_stride})
+    if (s < c->dim || s > far) return fail(FP4_E_SHAPE, "%s: cache stride %lld below dim or too large", who, (long long)s);
+  if (e4m3)
+    for (const int64_t s : {c->scale_page_stride, c->scale_head_stride, c->scale_token_stride})
+      if (s < 1 || s > far) return fail(FP4_E_SHAPE, "%s: scale stride %lld not positive or too large", who, (long long)s);
+  if (c->cols < 1 || c->cols > ((int64_t)1 << 30) / c->page_size || c->table_stride < c->cols || c->table_stride > far)
+    return fail(FP4_E_SHAPE, "%s: need cols >= 1, cols * page_size <= 2^30 and table_stride >= cols (cols=%lld stride=%lld)", who,
+                (long long)c->cols, (long long)c->table_stride);
+  if (c->batch < 1 || c->batch > 65535 || c->batch * q_heads > (1 << 22))
+    return fail(FP4_E_SHAPE, "%s: need 1 <= batch <= 65535 and batch * query heads <= 2^22 (batch=%lld)", who, (long long)c->batch);
+  const int64_t unit = e4m3 ? 16 : 8;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || c->page_stride % unit || c->head_stride % unit || c->token_stride % unit)
+    return fail(FP4_E_ALIGN, "%s: pages must be 16-byte aligned, their strides multiples of %d", who, (int)unit);
+  if (!aligned(c->table, 4) || !aligned(c->lengths, 4) || (e4m3 && (!aligned(c->k_scales, 4) || !aligned(c->v_scales, 4))))
+    return fail(FP4_E_ALIGN, "%s: table, lengths and scales must be 4-byte aligned", who);
+  const int64_t bytes = e4m3 ? 1 : 2;
+  int shift = 4;
+  while ((1 << shift) < c->page_size) ++shift;
+  *out = fp4::Paged{static_cast<const uint8_t*>(c->k), static_cast<const uint8_t*>(c->v), c->k_scales, c->v_scales,
+                    c->page_stride * bytes, c->head_stride * bytes, c->token_stride * bytes, c->scale_page_stride,
+                    c->scale_head_stride, c->scale_token_stride, c->table, c->table_stride, c->lengths, (int)c->pages, shift,
+                    (int)c->cols, (int)c->batch, c->heads};
+  return FP4_OK;
+}
+
+// Rows of heads of dim bf16 numbers.
+int check_heads(const char* who, const char* what, const void* X, int64_t row, int64_t head, int dim) {
+  if (row < dim || head < dim || row > (int64_t)1 << 40 || head > (int64_t)1 << 40)
+    return fail(FP4_E_SHAPE, "%s: strides of %s (rows %lld, heads %lld) below dim or too large", who, what, (long long)row, (long long)head);
+  if (!aligned(X, 16) || row % 8 || head % 8)
+    return fail(FP4_E_ALIGN, "%s: %s must be 16-byte aligned, its strides multiples of 8", who, what);
+  return FP4_OK;
+}
+
+int attention(const char* who, const fp4_kv_cache* cache, const int* starts, int64_t T, const void* Q, int64_t q_row, int64_t q_head,
+              int q_heads, float scale, int64_t window, int64_t sinks, void* Out, void* workspace, size_t workspace_bytes,
+              bool decode, void* stream) {
+  if (!Q || !Out || !workspace || (!decode && !starts)) return fail(FP4_E_NULLPTR, "%s: pointers must be non-NULL", who);
+  Fp4AttentionArgs a{};
+  int st = check_cache(who, cache, q_heads, &a.cache);
+  if (st != FP4_OK) return st;
+  if (decode) T = cache->batch;
+  if (q_heads < 1 || q_heads > 1024 || q_heads % cache->heads)
+    return fail(FP4_E_SHAPE, "%s: q_heads=%d is no multiple of the cache's %d heads up to 1024", who, q_heads, cache->heads);
+  if (T < 1 || T > (1 << 24) || T * q_heads > (1 << 30))
+    return fail(FP4_E_SHAPE, "%s: need 1 <= T <= 2^24 and T * q_heads <= 2^30 (T=%lld)", who, (long long)T);
+  if (!(scale > 0.f) || !__builtin_isfinite(scale)) return fail(FP4_E_SHAPE, "%s: scale must be finite and positive", who);
+  if (window < 0 || sinks < 0) return fail(FP4_E_SHAPE, "%s: window and sinks must not be negative", who);
+  const size_t need = FP4_ATTENTION_WORKSPACE_BYTES(T, cache->batch, q_heads, cache->heads, cache->dim);
+  if (workspace_bytes < need) return fail(FP4_E_SHAPE, "%s: workspace of %zu bytes, %zu needed", who, workspace_bytes, need);
+  st = check_heads(who, "Q", Q, q_row, q_head, cache->dim);
+  if (st != FP4_OK) return st;
+  if (!aligned(Out, 16) || !aligned(workspace, 16) || !aligned(starts, 4))
+    return fail(FP4_E_ALIGN, "%s: Out and workspace must be 16-byte aligned, starts 4-byte aligned", who);
+  const int64_t most = (int64_t)1 << 30;
+  a.starts = starts;
+  a.q = static_cast<const uint16_t*>(Q);
+  a.out = static_cast<uint16_t*>(Out);
+  a.q_token = q_row;
+  a.q_head = q_head;
+  a.scale = scale;
+  a.T = (int)T;
+  a.q_heads = q_heads;
+  a.window = (int)(window < most ? window : most);
+  a.sinks = (int)(sinks < most ? sinks : most);
+  a.workspace = workspace;
+  const bool e4m3 = cache->dtype == FP4_KV_E4M3;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return launched(who, decode ? fp4_launch_attention_decode(a, cache->dim, e4m3, s) : fp4_launch_attention_prompt(a, cache->dim, e4m3, s));
 }
 
 }  // namespace
@@ -326,6 +411,74 @@ int fp4_moe_experts(const void* X, int64_t T, int64_t D, int64_t ldx, const int*
   return launched(who, fp4_launch_moe_experts(static_cast<const uint16_t*>(X), T, D, ldx, ids, weights, k, E, I, block,
                                               W13q, W13s, W2q, W2s, static_cast<uint16_t*>(Y),
                                               static_cast<uint8_t*>(workspace), static_cast<hipStream_t>(stream)));
+}
+
+int fp4_kv_append(const fp4_kv_cache* cache, const int* starts, int64_t T, const void* K, int64_t k_row, int64_t k_head,
+                  const void* V, int64_t v_row, int64_t v_head, const void* Q, int64_t q_row, int64_t q_head, int q_heads,
+                  void* Q_out, int64_t out_row, int64_t out_head, const float* freqs, int rotated, int interleaved,
+                  const int* positions, const int* axes, int n_axes, void* stream) {
+  const char* who = "fp4_kv_append";
+  if (!K || !V) return fail(FP4_E_NULLPTR, "%s: K and V must be non-NULL", who);
+  if ((Q != nullptr) != (Q_out != nullptr)) return fail(FP4_E_NULLPTR, "%s: Q and Q_out go together", who);
+  if (!freqs && (rotated || positions || axes || Q))
+    return fail(FP4_E_NULLPTR, "%s: rotated, positions, axes and Q need freqs", who);
+  if (axes && !positions) return fail(FP4_E_NULLPTR, "%s: axes need positions", who);
+  Fp4AppendArgs a{};
+  int st = check_cache(who, cache, Q ? q_heads : 1, &a.cache);
+  if (st != FP4_OK) return st;
+  if (Q ? q_heads < 1 || q_heads > 1024 : q_heads != 0) return fail(FP4_E_SHAPE, "%s: q_heads=%d not in 1 .. 1024, or 0 without Q", who, q_heads);
+  if (T < 1 || T > (1 << 24) || T * (q_heads + 2 * cache->heads) > (1 << 30))
+    return fail(FP4_E_SHAPE, "%s: need 1 <= T <= 2^24 and T * (q_heads + 2 * heads) <= 2^30 (T=%lld)", who, (long long)T);
+  if (!starts && T != cache->batch)
+    return fail(FP4_E_SHAPE, "%s: without starts T must be the batch, got %lld and %lld", who, (long long)T, (long long)cache->batch);
+  if (rotated < 0 || rotated > cache->dim || rotated % 16 || (freqs && !rotated))
+    return fail(FP4_E_SHAPE, "%s: rotated=%d is no positive multiple of 16 up to dim (0 without freqs)", who, rotated);
+  if (positions ? n_axes < 1 || n_axes > 16 : n_axes != 0)
+    return fail(FP4_E_SHAPE, "%s: n_axes=%d not in 1 .. 16, or 0 without positions", who, n_axes);
+  st = check_heads(who, "K", K, k_row, k_head, cache->dim);
+  if (st == FP4_OK) st = check_heads(who, "V", V, v_row, v_head, cache->dim);
+  if (st == FP4_OK && Q) st = check_heads(who, "Q", Q, q_row, q_head, cache->dim);
+  if (st == FP4_OK && Q) st = check_heads(who, "Q_out", Q_out, out_row, out_head, cache->dim);
+  if (st != FP4_OK) return st;
+  if (Q && Q == Q_out && (q_row != out_row || q_head != out_head))
+    return fail(FP4_E_SHAPE, "%s: queries rotated in place need the same strides", who);
+  if (!aligned(starts, 4) || !aligned(freqs, 4) || !aligned(positions, 4) || !aligned(axes, 4))
+    return fail(FP4_E_ALIGN, "%s: starts, freqs, positions and axes must be 4-byte aligned", who);
+  a.starts = starts;
+  a.q = static_cast<const uint16_t*>(Q);
+  a.k = static_cast<const uint16_t*>(K);
+  a.v = static_cast<const uint16_t*>(V);
+  a.q_out = static_cast<uint16_t*>(Q_out);
+  a.q_token = q_row;
+  a.q_head = q_head;
+  a.k_token = k_row;
+  a.k_head = k_head;
+  a.v_token = v_row;
+  a.v_head = v_head;
+  a.out_token = out_row;
+  a.out_head = out_head;
+  a.freqs = freqs;
+  a.positions = positions;
+  a.axes = axes;
+  a.T = (int)T;
+  a.q_heads = q_heads;
+  a.half = rotated / 2;
+  a.naxes = n_axes;
+  a.interleaved = interleaved != 0;
+  return launched(who, fp4_launch_kv_append(a, cache->dim, cache->dtype == FP4_KV_E4M3, static_cast<hipStream_t>(stream)));
+}
+
+int fp4_attention_decode(const fp4_kv_cache* cache, const void* Q, int64_t q_row, int64_t q_head, int q_heads, float scale,
+                         int64_t window, int64_t sinks, void* Out, void* workspace, size_t workspace_bytes, void* stream) {
+  return attention("fp4_attention_decode", cache, nullptr, 0, Q, q_row, q_head, q_heads, scale, window, sinks, Out, workspace,
+                   workspace_bytes, true, stream);
+}
+
+int fp4_attention_prompt(const fp4_kv_cache* cache, const int* starts, int64_t T, const void* Q, int64_t q_row, int64_t q_head,
+                         int q_heads, float scale, int64_t window, int64_t sinks, void* Out, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  return attention("fp4_attention_prompt", cache, starts, T, Q, q_row, q_head, q_heads, scale, window, sinks, Out, workspace,
+                   workspace_bytes, false, stream);
 }
 
 const char* fp4_last_error(void) { return g_err; }

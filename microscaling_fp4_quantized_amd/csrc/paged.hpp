@@ -1,0 +1,83 @@
+// The paged key-value cache as the kernels see it, and its launchers. A page holds page_size = 1 << shift tokens of every head;
+// table[b, i >> shift] names the page of token i of sequence b. Page sizes are powers of two from 16 on, so 16 consecutive tokens
+// from a multiple of 16 lie in one page: a "granule", for which one look into the table is enough.
+#pragma once
+
+#include "fp8_device.hpp"
+
+namespace fp4 {
+
+struct Paged {
+  const uint8_t *k, *v;               // bf16, or E4M3 codes
+  const float *k_scales, *v_scales;   // E4M3: one for a token's values of a head
+  int64_t page_stride, head_stride, token_stride;     // bytes
+  int64_t spage_stride, shead_stride, stoken_stride;  // scales, elements
+  const int* table;
+  int64_t table_stride;
+  const int* lengths;
+  int pages, shift, cols, batch, heads;
+};
+
+constexpr int kGranule = 16;
+
+// Tokens that the table has room for.
+__device__ __forceinline__ int paged_room(const Paged& p) { return p.cols << p.shift; }
+
+// Tokens of sequence b, those that the table has no room for included; no more than 2^30 count, so that places and their
+// differences from a window (at most 2^30 too) stay within 32 bits.
+__device__ __forceinline__ int length_of(const Paged& p, int b) { return min(max(p.lengths[b], 0), 1 << 30); }
+
+// Sum over the 64 lanes, and over the lanes up to this one.
+__device__ __forceinline__ int wave_total(int v) {
+#pragma unroll
+  for (int h = 1; h < 64; h <<= 1) v += __shfl_xor(v, h);
+  return v;
+}
+__device__ __forceinline__ int wave_prefix(int v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int h = 1; h < 64; h <<= 1) {
+    const int o = __shfl_up(v, h);
+    if (lane >= h) v += o;
+  }
+  return v;
+}
+
+// The sequence of row t of a batch of rows, or -1 where it belongs to none. starts is NULL for one row each.
+__device__ __forceinline__ int sequence_of(const int* starts, int batch, int t) {
+  if (starts == nullptr) return t < batch ? t : -1;
+  int n = 0;
+  for (int b = 0; b < batch; b += 64) {
+    const int at = b + (threadIdx.x & 63);
+    n += __popcll(__ballot(at < batch && starts[at + 1] <= t));
+  }
+  return n < batch && starts[n] <= t ? n : -1;
+}
+
+}  // namespace fp4
+
+struct Fp4AppendArgs {
+  fp4::Paged cache;
+  const int* starts;
+  const uint16_t *q, *k, *v;
+  uint16_t* q_out;
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head, out_token, out_head;  // strides, elements
+  const float* freqs;
+  const int *positions, *axes;  // positions [naxes, T]
+  int T, q_heads, half, naxes;
+  bool interleaved;
+};
+hipError_t fp4_launch_kv_append(const Fp4AppendArgs& a, int dim, bool e4m3, hipStream_t stream);
+
+struct Fp4AttentionArgs {
+  fp4::Paged cache;
+  const int* starts;  // prompt only
+  const uint16_t* q;
+  uint16_t* out;  // contiguous [T, q_heads, dim]
+  int64_t q_token, q_head;
+  float scale;
+  int T, q_heads, window, sinks;
+  void* workspace;
+};
+hipError_t fp4_launch_attention_decode(const Fp4AttentionArgs& a, int dim, bool e4m3, hipStream_t stream);
+hipError_t fp4_launch_attention_prompt(const Fp4AttentionArgs& a, int dim, bool e4m3, hipStream_t stream);
