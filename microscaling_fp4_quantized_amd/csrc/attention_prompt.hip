@@ -256,33 +256,36 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void prompt(Fp4Atten
     if (tid == 0) lds.odd[(it + 2) & 3] = 0;  // read two tiles ago, next written behind the next barrier
     const bool hidden = j > w1 || (a.window && j + kTokens - 1 <= w0 - a.window && j >= a.sinks);
     if (!hidden) {
-      v16f s[2];
+      // scores as plain floats: changing elements of a matrix register under a branch was compiled wrongly (D = 256, one
+      // element copied over all others, by the clang of ROCm 7.2)
+      float s[2][16];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
+        v16f acc;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[u][i] = 0.f;
+        for (int i = 0; i < 16; ++i) acc[i] = 0.f;
         const int r = lane & 31, t = 32 * u + ((r & 0x13) | ((r & 4) << 1) | ((r & 8) >> 1));
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           const v8bf k = __builtin_bit_cast(v8bf, *reinterpret_cast<const v4u*>(&lds.k[buf][t][16 * i + 8 * half]));
-          s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[i], s[u], 0, 0, 0);
+          acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[i], acc, 0, 0, 0);
         }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          s[u][i] = acc[i] * (E4M3 ? lds.scales[buf][0][32 * u + 16 * (i / 8) + 8 * half + i % 8] : factor);
       }
       const bool all = whole(id, j, w0, w1);
+      if (!all) {
+        const int from = a.window ? place - a.window : -1, to = min(place, range.n - 1);
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int t = 32 * u + 16 * (i / 8) + 8 * half + i % 8;
-          if constexpr (E4M3) s[u][i] *= lds.scales[buf][0][t];
-          else s[u][i] *= factor;
-          if (!all) {
-            const int at = j + t;
-            const bool on = at <= place && at < range.n && (a.window == 0 || at > place - a.window || at < a.sinks) &&
-                            id.page[2 * u + i / 8] >= 0;
+          for (int i = 0; i < 16; ++i) {
+            const int at = j + 32 * u + 16 * (i / 8) + 8 * half + i % 8;
+            const bool on = (at <= to) & ((at > from) | (at < a.sinks)) & (id.page[2 * u + i / 8] >= 0);
             s[u][i] = on ? s[u][i] : kNever;
           }
-        }
+      }
       float z = s[0][0];
 #pragma unroll
       for (int u = 0; u < 2; ++u)
