@@ -161,6 +161,10 @@ class _Fast:
         self.linear = bind(module.linear, "fp8_linear")
         self.route = bind(module.route, "fp4_moe_route")
         self.experts = bind(module.experts, "fp4_moe_experts")
+        # a module built before these calls were there serves the others
+        self.append, self.decode, self.prompt = (
+            bind(getattr(module, name), entry) if hasattr(module, name) else None
+            for name, entry in (("append", "fp4_kv_append"), ("decode", "fp4_attention_decode"), ("prompt", "fp4_attention_prompt")))
 
 
 def _compiled(lib):
@@ -687,6 +691,14 @@ def fp4_kv_append(k: torch.Tensor, v: torch.Tensor, k_pages, v_pages, table, len
     ``interleaved``; None: nothing is. positions int32 [T] or [axes, T] in place of the tokens' places, axes int32 [n / 2] the axis
     of each frequency. ``out`` may pass the rotated queries' buffer, any strides, q itself too."""
     name = "fp4_kv_append"
+    fast = _fast(k) if (q is None) == (out is None) else None
+    if fast and fast.append:
+        status = fast.append(k, v, k_pages, v_pages, table, lengths, k_scales, v_scales, starts, q, freqs, positions, axes,
+                             bool(interleaved), out)
+        if status is not None:
+            if status:
+                _check(status)
+            return out
     lib = load_library()
     T, H, D, k_row, k_head = _head_rows(k, name, "k")
     dev = k.device
@@ -747,7 +759,26 @@ def attention_workspace_bytes(T: int, B: int, q_heads: int, heads: int, dim: int
     return ((1 if blocks >= 512 else 512 // blocks) + B) * q_heads * (dim + 2) * 4
 
 
+_SHORT = -2  # FP4_E_SHAPE
+
+
+def _attention_bytes(q, cache):
+    return attention_workspace_bytes(q.shape[0], cache[2].shape[0], q.shape[1], cache[0].shape[1], q.shape[2])
+
+
 def _attention(name, q, cache, scale, window, sinks, starts, out, workspace):
+    fast = _fast(q) if out is not None else None
+    call = fast and (fast.decode if starts is None else fast.prompt)
+    if call and isinstance(workspace, torch.Tensor):
+        rows = () if starts is None else (starts,)
+        # the library knows what the workspace has to hold
+        status = call(q, *cache, *rows, q.shape[-1] ** -0.5 if scale is None else scale, window, sinks, out, workspace)
+        if status == _SHORT and workspace.numel() < _attention_bytes(q, cache):
+            status = None
+        if status is not None:
+            if status:
+                _check(status)
+            return out
     T, Hq, D, q_row, q_head = _head_rows(q, name, "q")
     dev = q.device
     c = _kv_cache(name, *cache)

@@ -1,6 +1,7 @@
-"""Times of the operators' listed cases (perf/operators.py), and summaries of rocprofv3's output on them.
+"""Times of the operators' listed cases (perf/operators.py, or with --more perf/more_operators.py), and summaries of rocprofv3's
+output on them.
 
-    python perf/time_operators.py [--plain] [--only NAME,NAME]        us of a call among others, Python included
+    python perf/time_operators.py [--more] [--plain] [--only NAME,NAME]  us of a call among others, Python included
     python perf/time_operators.py --calls 30 [--only NAME,NAME]       that many calls of each case and nothing else: the program to profile
     python perf/time_operators.py --trace CSV                         summary of a kernel trace
     python perf/time_operators.py --counters CSV [--kernel NAME]      mean counters of a kernel's grids
@@ -21,10 +22,10 @@ sys.path.insert(0, os.path.dirname(HERE))
 SETS = 3
 
 
-def cases(own, only):
+def cases(own, only, file="operators"):
     import torch
 
-    spec = importlib.util.spec_from_file_location("operators", os.path.join(HERE, "operators.py"))
+    spec = importlib.util.spec_from_file_location(file, os.path.join(HERE, file + ".py"))
     ops = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(ops)
     ops.own = own
@@ -87,6 +88,7 @@ def counters(path, kernel):
 
 def main():
     p = argparse.ArgumentParser(description=__doc__.split("\n")[0])
+    p.add_argument("--more", action="store_true", help="the cases of more_operators.py")
     p.add_argument("--plain", action="store_true", help="the plain forms in place of the kernels")
     p.add_argument("--only", default="")
     p.add_argument("--calls", type=int, default=0)
@@ -100,7 +102,8 @@ def main():
         return counters(a.counters, a.kernel)
     if not a.calls:
         print(f"{'case':20s} {'median us':>10s} {'least':>10s} {'longest':>10s}")
-    for name, call in cases(not a.plain, set(filter(None, a.only.split(",")))):
+    for name, call in cases(not a.plain, set(filter(None, a.only.split(","))),
+                            "more_operators" if a.more else "operators"):
         if a.calls:
             for i in range(a.calls):
                 call(i)
