@@ -390,8 +390,8 @@ FP4_API int fp4_moe_experts(const void *X, int64_t T, int64_t D, int64_t ldx, co
  *
  *  dtype       FP4_KV_BF16 or FP4_KV_E4M3.   heads 1..1024.   dim 64, 128 or 256.
  *  page_size   a power of two, 16..1024.   pages 1..2^31 - 1.
- *  k, v        device, 16-byte aligned. Strides in elements for both, >= dim, at most 2^40 and multiples of 8 (E4M3:
- *              16): pages of [heads, page_size, dim], of [page_size, heads, dim], keys and values page by page in
+ *  k, v        device, 16-byte aligned. Strides in elements for both, >= dim, at most 2^40 (tokens: 2^25) and multiples of 8
+ *              (E4M3: 16): pages of [heads, page_size, dim], of [page_size, heads, dim], keys and values page by page in
  *              one buffer, or any other order. The dims of a token's head lie together.
  *  k_scales, v_scales  device float, 4-byte aligned, strides >= 1 and at most 2^40; NULL exactly with FP4_KV_BF16.
  *  table       device int [batch, cols], row stride table_stride >= cols. A page id outside [0, pages) (-1, say) is no page: its

@@ -45,6 +45,16 @@ __device__ __forceinline__ unsigned bf16_pair(float a, float b) {
   return __builtin_bit_cast(unsigned, v);
 }
 
+// Both halves of a word of bf16 and c, in float32.
+__device__ __forceinline__ float add_pair(unsigned w, float c) {
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2bf, w), v2bf{(__bf16)1.f, (__bf16)1.f}, c, false);
+}
+
+// A word that all lanes read alike and that no kernel running now writes, into scalar registers.
+__device__ __forceinline__ int uniform_load(const int* p) {
+  return *(const __attribute__((address_space(4))) int*)(reinterpret_cast<uintptr_t>(p));
+}
+
 // The low or the high halves of two words, a's in the low half.
 __device__ __forceinline__ unsigned low_halves(unsigned a, unsigned b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
 __device__ __forceinline__ unsigned high_halves(unsigned a, unsigned b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }

@@ -48,23 +48,23 @@ struct Staged {
   float scale;
 };
 
-struct Ids {
-  int page[4];
-};
-
 // What a workgroup looks at: tiles of 64 tokens, ta of them from token 0 on, then more from tile tb on.
 struct Range {
   int n, ta, tb, tiles;
   __device__ int first_of(int t) const { return (t < ta ? t : t - ta + tb) * kTokens; }
 };
 
+// A tile's pages, -1 for those that are none and past the end: one for each of its granules, the same for the whole workgroup.
+struct Ids {
+  int page[4];
+};
 __device__ __forceinline__ Ids ids_of(const Paged& c, const int* row, const Range& r, int tile) {
   Ids x;
   const int j = tile < r.tiles ? r.first_of(tile) : r.n;
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     const int at = j + g * kGranule;
-    const int page = at < r.n ? row[at >> c.shift] : -1;
+    const int page = at < r.n ? uniform_load(row + (at >> c.shift)) : -1;
     x.page[g] = (unsigned)page < (unsigned)c.pages ? page : -1;
   }
   return x;
@@ -74,30 +74,43 @@ __device__ __forceinline__ int pick(const Ids& x, int g) {
   return (g & 2) ? b : a;
 }
 
+// A thread's loads of a tile: a granule's place is the same for a wave (scalar registers), the offset within it stays the thread's.
 template <int D, bool E4M3>
-__device__ __forceinline__ void fetch(Staged<D, E4M3>& x, const Paged& c, int head, const Ids& id, int j, int tid) {
+struct Fetch {
   typedef Staged<D, E4M3> S;
-  constexpr int LANES = D * (E4M3 ? 1 : 2) / 16, STEP = 64 * kWaves / LANES;  // threads of a K row, rows of a pass
-  const int mask = (1 << c.shift) - 1;
-#pragma unroll
-  for (int i = 0; i < S::KL; ++i) {
-    const int t = tid / LANES + i * STEP, page = max(pick(id, t >> 4), 0);
-    x.k[i] = *reinterpret_cast<const v4u*>(c.k + page * c.page_stride + head * c.head_stride + ((j + t) & mask) * c.token_stride +
-                                           16 * (tid % LANES));
+  static constexpr int LANES = D * (E4M3 ? 1 : 2) / 16, STEP = 64 * kWaves / LANES;  // threads of a K row, rows of a pass
+  unsigned k, v, token;
+
+  __device__ __forceinline__ Fetch(const Paged& c, int tid) {
+    token = (unsigned)c.token_stride;  // at most 2^26 bytes
+    k = (tid / LANES % kGranule) * token + 16 * (tid % LANES);
+    v = (4 * (tid >> 4) % kGranule) * token + 4 * S::VW * (tid & 15);
   }
-  const int t = 4 * (tid >> 4), page = max(pick(id, t >> 4), 0);
-  const uint8_t* v = c.v + page * c.page_stride + head * c.head_stride + ((j + t) & mask) * c.token_stride + 4 * S::VW * (tid & 15);
+  static __device__ __forceinline__ int64_t place(const Paged& c, int head, int page, int j) {
+    return max(page, 0) * c.page_stride + head * c.head_stride + (j & ((1 << c.shift) - 1)) * c.token_stride;
+  }
+  __device__ __forceinline__ void operator()(S& x, const Paged& c, int head, const Ids& id, int j, int wave, int tid) const {
 #pragma unroll
-  for (int u = 0; u < S::VU; ++u)
+    for (int i = 0; i < S::KL; ++i) {
+      const int t = wave * (64 / LANES) / kGranule * kGranule + i * STEP;  // the wave's rows are in this one's granule
+      const int g = t / kGranule, more = STEP < kGranule ? i * STEP % kGranule : 0;
+      const uint8_t* at = c.k + place(c, head, pick(id, g), j + g * kGranule);
+      x.k[i] = *reinterpret_cast<const v4u*>(at + (k + more * token));
+    }
+    const uint8_t* at = c.v + place(c, head, pick(id, wave), j + wave * kGranule);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      x.v[u][i] = *reinterpret_cast<const typename S::VWord*>(v + i * c.token_stride + u * (64 * S::VW));
-  if constexpr (E4M3) {
-    const int ts = tid & 63, ps = max(pick(id, ts >> 4), 0);
-    if (tid < 128)
-      x.scale = (tid < 64 ? c.k_scales : c.v_scales)[ps * c.spage_stride + head * c.shead_stride + ((j + ts) & mask) * c.stoken_stride];
+#pragma unroll
+      for (int u = 0; u < S::VU; ++u)
+        x.v[u][i] = *reinterpret_cast<const typename S::VWord*>(at + (v + i * token) + u * (64 * S::VW));
+    if constexpr (E4M3) {
+      const int ts = tid & 63, ps = max(pick(id, ts >> 4), 0);
+      if (tid < 128)
+        x.scale = (tid < 64 ? c.k_scales : c.v_scales)[ps * c.spage_stride + head * c.shead_stride +
+                                                       ((j + ts) & ((1 << c.shift) - 1)) * c.stoken_stride];
+    }
   }
-}
+};
 
 // bf16 pairs with an exponent of all ones, in either half.
 __device__ __forceinline__ bool odd_pair(unsigned w) { return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u; }
@@ -106,7 +119,7 @@ __device__ __forceinline__ bool odd_pair(unsigned w) { return (w & 0x7F80u) == 0
 // `some` (not all rows see all tokens) values that are no numbers are 0 and their tokens noted.
 template <int D, bool E4M3>
 __device__ __forceinline__ void store(Lds<D, E4M3>& lds, const Staged<D, E4M3>& x, int buf, const Ids& id, int j, int n, float factor,
-                                      bool some, unsigned long long* odd, int tid) {
+                                      bool some, unsigned long long* odd, int wave, int tid) {
   typedef Staged<D, E4M3> S;
   constexpr int LANES = D * (E4M3 ? 1 : 2) / 16, STEP = 64 * kWaves / LANES;
 #pragma unroll
@@ -122,7 +135,7 @@ __device__ __forceinline__ void store(Lds<D, E4M3>& lds, const Staged<D, E4M3>& 
     }
   }
   const int t = 4 * (tid >> 4);
-  const bool held = pick(id, t >> 4) >= 0;
+  const bool held = pick(id, wave) >= 0;
 #pragma unroll
   for (int u = 0; u < S::VU; ++u) {
     unsigned w[4][S::VDIM / 2];
@@ -231,7 +244,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void prompt(Fp4Atten
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[m][i] = 0.f;
   float top = kNever, sum = 0.f;
-  const float factor = a.scale * kLog2e;
+  const float factor = a.scale * kLog2e, unit = E4M3 ? 1.f : factor;  // 8 bits: the factor is in the keys' scales
   // does everything in the tile from j on count for all rows of places from i0 to i1?
   auto whole = [&](const Ids& id, int j, int i0, int i1) {
     return j + kTokens <= range.n && j + kTokens - 1 <= i0 && (a.window == 0 || j > i1 - a.window || j + kTokens <= a.sinks) &&
@@ -239,19 +252,22 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void prompt(Fp4Atten
   };
 
   Staged<D, E4M3> next;
+  const Fetch<D, E4M3> fetch(c, tid);
   Ids id = ids_of(c, pages, range, 0), ahead = ids_of(c, pages, range, 1);
+  bool some = false;  // not all rows see all of the tile that lies in LDS
   if (tid < 4) lds.odd[tid] = 0;
   __syncthreads();
   if (range.tiles > 0) {
     const int j = range.first_of(0);
-    fetch<D, E4M3>(next, c, head, id, j, tid);
-    store<D, E4M3>(lds, next, 0, id, j, range.n, factor, !whole(id, j, g0, g1), &lds.odd[0], tid);
+    fetch(next, c, head, id, j, wave, tid);
+    some = !whole(id, j, g0, g1);
+    store<D, E4M3>(lds, next, 0, id, j, range.n, factor, some, &lds.odd[0], wave, tid);
   }
   __syncthreads();
   for (int it = 0; it < range.tiles; ++it) {
     const int buf = it & 1, j = range.first_of(it), jn = range.first_of(it + 1);
     const bool more = it + 1 < range.tiles;
-    if (more) fetch<D, E4M3>(next, c, head, ahead, jn, tid);
+    if (more) fetch(next, c, head, ahead, jn, wave, tid);
     const Ids after = ids_of(c, pages, range, it + 2);
     if (tid == 0) lds.odd[(it + 2) & 3] = 0;  // read two tiles ago, next written behind the next barrier
     const bool hidden = j > w1 || (a.window && j + kTokens - 1 <= w0 - a.window && j >= a.sinks);
@@ -271,8 +287,10 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void prompt(Fp4Atten
           acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[i], acc, 0, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          s[u][i] = acc[i] * (E4M3 ? lds.scales[buf][0][32 * u + 16 * (i / 8) + 8 * half + i % 8] : factor);
+        for (int i = 0; i < 16; ++i) {
+          s[u][i] = acc[i];
+          if (E4M3) s[u][i] *= lds.scales[buf][0][32 * u + 16 * (i / 8) + 8 * half + i % 8];
+        }
       }
       const bool all = whole(id, j, w0, w1);
       if (!all) {
@@ -286,12 +304,10 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void prompt(Fp4Atten
             s[u][i] = on ? s[u][i] : kNever;
           }
       }
-      float z = s[0][0];
+      float z = fmaxf(s[0][0], s[1][0]);
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) z = fmaxf(z, s[u][i]);
-      z = max_across<32>(z);
+      for (int i = 1; i < 16; ++i) z = fmaxf(fmaxf(z, s[0][i]), s[1][i]);
+      z = max_across<32>(z) * unit;
       if (__any(z > top + kSlack)) {
         const float m = fmaxf(top, z), keep = m == top ? 1.f : exp2_hw(top - m);
         top = m;
@@ -302,13 +318,14 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void prompt(Fp4Atten
           for (int i = 0; i < 16; ++i) o[m2][i] *= keep;
       }
       const float m = top == kNever ? 0.f : top;
-      float part = 0.f;
-      if (const unsigned long long odd = lds.odd[it & 3]) {  // a row that sees such a token is none of numbers
+      if (some) {
+        if (const unsigned long long odd = lds.odd[it & 3]) {  // a row that sees such a token is none of numbers
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (((odd >> (32 * u + 16 * (i / 8) + 8 * half + i % 8)) & 1) && s[u][i] != kNever) part = __builtin_nanf("");
+            for (int i = 0; i < 16; ++i)
+              if (((odd >> (32 * u + 16 * (i / 8) + 8 * half + i % 8)) & 1) && s[u][i] != kNever) sum = __builtin_nanf("");
+        }
       }
       v8bf p[2][2];
 #pragma unroll
@@ -320,17 +337,20 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void prompt(Fp4Atten
           for (int i = 0; i < 8; i += 2) {
             float x[2];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float y = s[u][8 * e + i + k];
-              x[k] = exp2_hw(y - m);
-              part += x[k];
-              if constexpr (E4M3) x[k] = !all && y == kNever ? 0.f : x[k] * lds.scales[buf][1][32 * u + 16 * e + 8 * half + i + k];
+            for (int k = 0; k < 2; ++k) x[k] = exp2_hw(__builtin_fmaf(s[u][8 * e + i + k], unit, -m));
+            if constexpr (E4M3) {
+              sum += x[0] + x[1];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const float y = x[k] * lds.scales[buf][1][32 * u + 16 * e + 8 * half + i + k];
+                x[k] = s[u][8 * e + i + k] == kNever ? 0.f : y;  // a hidden token's scale may be anything
+              }
             }
             w[i / 2] = bf16_pair(x[0], x[1]);
+            if (!E4M3) sum = add_pair(w[i / 2], sum);
           }
           p[u][e] = __builtin_bit_cast(v8bf, w);
         }
-      sum += part;
 #pragma unroll
       for (int m2 = 0; m2 < D / 32; ++m2)
 #pragma unroll
@@ -342,8 +362,10 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void prompt(Fp4Atten
             o[m2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[u][e], o[m2], 0, 0, 0);
           }
     }
-    if (more)
-      store<D, E4M3>(lds, next, buf ^ 1, ahead, jn, range.n, factor, !whole(ahead, jn, g0, g1), &lds.odd[(it + 1) & 3], tid);
+    if (more) {
+      some = !whole(ahead, jn, g0, g1);
+      store<D, E4M3>(lds, next, buf ^ 1, ahead, jn, range.n, factor, some, &lds.odd[(it + 1) & 3], wave, tid);
+    }
     id = ahead;
     ahead = after;
     __syncthreads();

@@ -149,6 +149,8 @@ int check_cache(const char* who, const fp4_kv_cache* c, int64_t q_heads, fp4::Pa
   const int64_t far = (int64_t)1 << 40;
   for (const int64_t s : {c->page_stride, c->head_stride, c->token_stride})
     if (s < c->dim || s > far) return fail(FP4_E_SHAPE, "%s: cache stride %lld below dim or too large", who, (long long)s);
+  // a granule's tokens are addressed by 32-bit offsets from its first
+  if (c->token_stride > (1 << 25)) return fail(FP4_E_SHAPE, "%s: token stride %lld above 2^25", who, (long long)c->token_stride);
   if (e4m3)
     for (const int64_t s : {c->scale_page_stride, c->scale_head_stride, c->scale_token_stride})
       if (s < 1 || s > far) return fail(FP4_E_SHAPE, "%s: scale stride %lld not positive or too large", who, (long long)s);

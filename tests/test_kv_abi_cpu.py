@@ -59,6 +59,7 @@ def test_the_caches_validation(lib, call, late):
     assert c(heads=0) == c(heads=-4) == c(heads=1025) == c(dim=0) == c(dim=96) == c(dim=512) == SHAPE
     assert c(page_size=8) == c(page_size=0) == c(page_size=48) == c(page_size=2048) == SHAPE
     assert c(pages=0) == c(pages=1 << 31) == c(page_stride=64) == c(head_stride=0) == c(token_stride=FAR) == SHAPE
+    assert c(token_stride=(1 << 25) + 16) == c(head_stride=FAR) == SHAPE and c(token_stride=1 << 25) == ALIGN
     assert c(dtype=1, scale_page_stride=0) == c(dtype=1, scale_token_stride=-1) == c(dtype=1, scale_head_stride=FAR) == SHAPE
     assert c(cols=0) == c(cols=6) == c(cols=(1 << 26) + 1, table_stride=1 << 27) == c(table_stride=FAR) == SHAPE
     assert c(batch=0) == c(batch=65536) == SHAPE
