@@ -306,6 +306,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode(Fp4Atten
   if (tile < end) {
     load<D, E4M3>(x0, c, head, span, id, lane);
     id = ids_of(c, row, span, tile + kWaves, lane);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) arrived(st.q[i]);
     while (true) {
       if (tile + kWaves < end) load<D, E4M3>(x1, c, head, span, id, lane);
       id = ids_of(c, row, span, tile + 2 * kWaves, lane);

@@ -50,6 +50,14 @@ __device__ __forceinline__ float add_pair(unsigned w, float c) {
   return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2bf, w), v2bf{(__bf16)1.f, (__bf16)1.f}, c, false);
 }
 
+// What a load brought, waited for here: its first use inside a loop would wait there in every round, and for all loads since.
+template <class T>
+__device__ __forceinline__ void arrived(T& x) {
+  v4u w = __builtin_bit_cast(v4u, x);
+  asm volatile("" : "+v"(w));
+  x = __builtin_bit_cast(T, w);
+}
+
 // A word that all lanes read alike and that no kernel running now writes, into scalar registers.
 __device__ __forceinline__ int uniform_load(const int* p) {
   return *(const __attribute__((address_space(4))) int*)(reinterpret_cast<uintptr_t>(p));

@@ -21,8 +21,6 @@
 namespace fp4 {
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kRows = 128;   // of a workgroup
 constexpr int kTokens = 64;  // of a tile
 constexpr float kSlack = 8.f;
 
@@ -33,19 +31,20 @@ struct Lds {
   static constexpr int KP = D + 8, VP = kTokens + 8;  // elements of a row
   uint16_t k[2][kTokens][KP];
   uint16_t v[2][D][VP];
-  float scales[2][2][kTokens];
+  float scales[4][2][kTokens];
   unsigned long long odd[4];  // tokens of a tile whose V has an infinity or NaN, where not all rows see all tokens
 };
 
+// A wave's part of a tile on its way: a granule's keys as 16-byte loads, or its values as 4 tokens x VDIM dims of a thread.
 template <int D, bool E4M3>
-struct Staged {
-  static constexpr int KL = kTokens * D * (E4M3 ? 1 : 2) / (64 * kWaves * 16);  // 16-byte loads of K of a thread
-  static constexpr int VDIM = D == 64 ? 4 : 8, VU = D == 256 ? 2 : 1;           // dims of a unit of V, units of a thread
-  static constexpr int VW = E4M3 ? VDIM / 4 : VDIM / 2;
+struct Part {
+  static constexpr int LANES = D * (E4M3 ? 1 : 2) / 16, KL = LANES / 4;  // threads of a key, loads of a granule
+  static constexpr int VDIM = D == 64 ? 4 : 8, VU = D == 256 ? 2 : 1;    // dims of a unit of V, units of a thread
+  static constexpr int VW = E4M3 ? VDIM / 4 : VDIM / 2;                  // words of a token and unit
   typedef unsigned VWord __attribute__((ext_vector_type(VW)));
-  v4u k[KL];
-  VWord v[VU][4];
+  unsigned w[4 * KL];
   float scale;
+  static_assert(4 * KL == VU * 4 * VW, "as many bytes of keys as of values");
 };
 
 // What a workgroup looks at: tiles of 64 tokens, ta of them from token 0 on, then more from tile tb on.
@@ -74,81 +73,92 @@ __device__ __forceinline__ int pick(const Ids& x, int g) {
   return (g & 2) ? b : a;
 }
 
-// A thread's loads of a tile: a granule's place is the same for a wave (scalar registers), the offset within it stays the thread's.
+// A granule's place is the same for a wave (scalar registers), the offset within it stays the thread's.
 template <int D, bool E4M3>
 struct Fetch {
-  typedef Staged<D, E4M3> S;
-  static constexpr int LANES = D * (E4M3 ? 1 : 2) / 16, STEP = 64 * kWaves / LANES;  // threads of a K row, rows of a pass
+  typedef Part<D, E4M3> P;
   unsigned k, v, token;
 
-  __device__ __forceinline__ Fetch(const Paged& c, int tid) {
+  __device__ __forceinline__ Fetch(const Paged& c, int lane) {
     token = (unsigned)c.token_stride;  // at most 2^26 bytes
-    k = (tid / LANES % kGranule) * token + 16 * (tid % LANES);
-    v = (4 * (tid >> 4) % kGranule) * token + 4 * S::VW * (tid & 15);
+    k = (lane / P::LANES) * token + 16 * (lane % P::LANES);
+    v = 4 * (lane >> 4) * token + 4 * P::VW * (lane & 15);
   }
   static __device__ __forceinline__ int64_t place(const Paged& c, int head, int page, int j) {
     return max(page, 0) * c.page_stride + head * c.head_stride + (j & ((1 << c.shift) - 1)) * c.token_stride;
   }
-  __device__ __forceinline__ void operator()(S& x, const Paged& c, int head, const Ids& id, int j, int wave, int tid) const {
+  static __device__ __forceinline__ float scale(const Paged& c, const float* scales, int head, const Ids& id, int j, int lane) {
+    const int ps = max(pick(id, lane >> 4), 0);
+    return scales[ps * c.spage_stride + head * c.shead_stride + ((j + lane) & ((1 << c.shift) - 1)) * c.stoken_stride];
+  }
+  __device__ __forceinline__ void keys(P& x, const Paged& c, int head, const Ids& id, int j, int g, int lane) const {
+    const uint8_t* at = c.k + place(c, head, pick(id, g), j + g * kGranule);
 #pragma unroll
-    for (int i = 0; i < S::KL; ++i) {
-      const int t = wave * (64 / LANES) / kGranule * kGranule + i * STEP;  // the wave's rows are in this one's granule
-      const int g = t / kGranule, more = STEP < kGranule ? i * STEP % kGranule : 0;
-      const uint8_t* at = c.k + place(c, head, pick(id, g), j + g * kGranule);
-      x.k[i] = *reinterpret_cast<const v4u*>(at + (k + more * token));
+    for (int i = 0; i < P::KL; ++i) {
+      const v4u y = *reinterpret_cast<const v4u*>(at + (k + i * (64 / P::LANES) * token));
+#pragma unroll
+      for (int n = 0; n < 4; ++n) x.w[4 * i + n] = y[n];
     }
-    const uint8_t* at = c.v + place(c, head, pick(id, wave), j + wave * kGranule);
+    if (E4M3 && g == 0) x.scale = scale(c, c.k_scales, head, id, j, lane);
+  }
+  __device__ __forceinline__ void values(P& x, const Paged& c, int head, const Ids& id, int j, int g, int lane) const {
+    const uint8_t* at = c.v + place(c, head, pick(id, g), j + g * kGranule);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int u = 0; u < S::VU; ++u)
-        x.v[u][i] = *reinterpret_cast<const typename S::VWord*>(at + (v + i * token) + u * (64 * S::VW));
-    if constexpr (E4M3) {
-      const int ts = tid & 63, ps = max(pick(id, ts >> 4), 0);
-      if (tid < 128)
-        x.scale = (tid < 64 ? c.k_scales : c.v_scales)[ps * c.spage_stride + head * c.shead_stride +
-                                                       ((j + ts) & ((1 << c.shift) - 1)) * c.stoken_stride];
-    }
+      for (int u = 0; u < P::VU; ++u) {
+        const typename P::VWord y = *reinterpret_cast<const typename P::VWord*>(at + (v + i * token) + u * (64 * P::VW));
+#pragma unroll
+        for (int n = 0; n < P::VW; ++n) x.w[(u * 4 + i) * P::VW + n] = y[n];
+      }
+    if (E4M3 && g == 0) x.scale = scale(c, c.v_scales, head, id, j, lane);
   }
 };
 
 // bf16 pairs with an exponent of all ones, in either half.
 __device__ __forceinline__ bool odd_pair(unsigned w) { return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u; }
 
-// The fetched tile into LDS: K as rows of bf16, V turned. Tokens from `n` on and of pages that are none have values of 0. With
-// `some` (not all rows see all tokens) values that are no numbers are 0 and their tokens noted.
+// Fetched keys into LDS, as rows of bf16.
 template <int D, bool E4M3>
-__device__ __forceinline__ void store(Lds<D, E4M3>& lds, const Staged<D, E4M3>& x, int buf, const Ids& id, int j, int n, float factor,
-                                      bool some, unsigned long long* odd, int wave, int tid) {
-  typedef Staged<D, E4M3> S;
-  constexpr int LANES = D * (E4M3 ? 1 : 2) / 16, STEP = 64 * kWaves / LANES;
+__device__ __forceinline__ void store_keys(Lds<D, E4M3>& lds, const Part<D, E4M3>& x, int tile, float factor, int g, int lane) {
+  typedef Part<D, E4M3> P;
 #pragma unroll
-  for (int i = 0; i < S::KL; ++i) {
-    const int t = tid / LANES + i * STEP;
-    uint16_t* to = &lds.k[buf][t][(E4M3 ? 16 : 8) * (tid % LANES)];
+  for (int i = 0; i < P::KL; ++i) {
+    uint16_t* to = &lds.k[tile & 1][g * kGranule + lane / P::LANES + i * (64 / P::LANES)][(E4M3 ? 16 : 8) * (lane % P::LANES)];
+    const unsigned* w = x.w + 4 * i;
     if constexpr (E4M3) {
-      const v2u a = bf16_of_codes(x.k[i][0]), b = bf16_of_codes(x.k[i][1]), e = bf16_of_codes(x.k[i][2]), f = bf16_of_codes(x.k[i][3]);
+      const v2u a = bf16_of_codes(w[0]), b = bf16_of_codes(w[1]), e = bf16_of_codes(w[2]), f = bf16_of_codes(w[3]);
       *reinterpret_cast<v4u*>(to) = v4u{a[0], a[1], b[0], b[1]};
       *reinterpret_cast<v4u*>(to + 8) = v4u{e[0], e[1], f[0], f[1]};
     } else {
-      *reinterpret_cast<v4u*>(to) = x.k[i];
+      *reinterpret_cast<v4u*>(to) = v4u{w[0], w[1], w[2], w[3]};
     }
   }
-  const int t = 4 * (tid >> 4);
-  const bool held = pick(id, wave) >= 0;
+  if (E4M3 && g == 0) lds.scales[tile & 3][0][lane] = x.scale * factor;
+}
+
+// Fetched values into LDS, turned. With `some` (not all rows see all of the tile's tokens) values from token n on, of pages that
+// are none and those that are no numbers are 0, and the tokens of the last are noted.
+template <int D, bool E4M3>
+__device__ __forceinline__ void store_values(Lds<D, E4M3>& lds, const Part<D, E4M3>& x, int tile, const Ids& id, int j, int n, bool some,
+                                             int g, int lane) {
+  typedef Part<D, E4M3> P;
+  const int t = g * kGranule + 4 * (lane >> 4);
+  const bool held = pick(id, g) >= 0;
 #pragma unroll
-  for (int u = 0; u < S::VU; ++u) {
-    unsigned w[4][S::VDIM / 2];
+  for (int u = 0; u < P::VU; ++u) {
+    unsigned w[4][P::VDIM / 2];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int k = 0; k < S::VW; ++k) {
+      for (int k = 0; k < P::VW; ++k) {
+        const unsigned raw = x.w[(u * 4 + i) * P::VW + k];
         if constexpr (E4M3) {
-          const v2u p = bf16_of_codes(x.v[u][i][k]);
+          const v2u p = bf16_of_codes(raw);
           w[i][2 * k] = p[0];
           w[i][2 * k + 1] = p[1];
         } else {
-          w[i][k] = x.v[u][i][k];
+          w[i][k] = raw;
         }
       }
     if (some) {
@@ -157,22 +167,20 @@ __device__ __forceinline__ void store(Lds<D, E4M3>& lds, const Staged<D, E4M3>& 
         const bool on = held && j + t + i < n;
         bool bad = false;
 #pragma unroll
-        for (int k = 0; k < S::VDIM / 2; ++k) bad |= odd_pair(w[i][k]);
-        if (on && bad) atomicOr(odd, 1ull << (t + i));
+        for (int k = 0; k < P::VDIM / 2; ++k) bad |= odd_pair(w[i][k]);
+        if (on && bad) atomicOr(&lds.odd[tile & 3], 1ull << (t + i));
 #pragma unroll
-        for (int k = 0; k < S::VDIM / 2; ++k) w[i][k] = on && !bad ? w[i][k] : 0u;
+        for (int k = 0; k < P::VDIM / 2; ++k) w[i][k] = on && !bad ? w[i][k] : 0u;
       }
     }
 #pragma unroll
-    for (int k = 0; k < S::VDIM / 2; ++k) {
-      const int row = u * 128 + 32 * k + (tid & 15);  // dim 128 u + VDIM (row % 16) + row / 16
-      *reinterpret_cast<v2u*>(&lds.v[buf][row][t]) = v2u{low_halves(w[0][k], w[1][k]), low_halves(w[2][k], w[3][k])};
-      *reinterpret_cast<v2u*>(&lds.v[buf][row + 16][t]) = v2u{high_halves(w[0][k], w[1][k]), high_halves(w[2][k], w[3][k])};
+    for (int k = 0; k < P::VDIM / 2; ++k) {
+      const int row = u * 128 + 32 * k + (lane & 15);  // dim 128 u + VDIM (row % 16) + row / 16
+      *reinterpret_cast<v2u*>(&lds.v[tile & 1][row][t]) = v2u{low_halves(w[0][k], w[1][k]), low_halves(w[2][k], w[3][k])};
+      *reinterpret_cast<v2u*>(&lds.v[tile & 1][row + 16][t]) = v2u{high_halves(w[0][k], w[1][k]), high_halves(w[2][k], w[3][k])};
     }
   }
-  if constexpr (E4M3) {
-    if (tid < 128) lds.scales[buf][tid >> 6][tid & 63] = tid < 64 ? x.scale * factor : x.scale;
-  }
+  if (E4M3 && g == 0) lds.scales[tile & 3][1][lane] = x.scale;
 }
 
 // Rows of a sequence: new tokens times the heads of a group.
@@ -184,10 +192,12 @@ __device__ __forceinline__ Rows rows_of(const int* starts, int b, int T) {
   return {t0, t1 - t0};
 }
 
-template <int D, bool E4M3>
-__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void prompt(Fp4AttentionArgs a, int group, int tiles) {
+template <int D, bool E4M3, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt(Fp4AttentionArgs a, int group, int tiles) {
   extern __shared__ __align__(16) uint8_t memory[];
   typedef Lds<D, E4M3> L;
+  constexpr int kRows = 32 * WAVES;
+  static_assert(sizeof(L) >= (size_t)kRows * (D + 8) * 2, "the rows of out pass through the same memory");
   L& lds = *reinterpret_cast<L*>(memory);
   const Paged& c = a.cache;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -227,10 +237,6 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void prompt(Fp4Atten
     if (range.tb <= range.ta) range.ta = range.tb = end;
     range.tiles = range.ta + max(end - range.tb, 0);
   }
-  // the wave's first and last places
-  const int w0 = base + min(tile * kRows + wave * 32, last) / group, w1 = base + min(tile * kRows + wave * 32 + 31, last) / group;
-  const int g0 = base + tile * kRows / group, g1 = base + min(tile * kRows + kRows - 1, last) / group;
-
   const int half = lane >> 5;
   v8bf q[D / 16];
   {
@@ -245,136 +251,175 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void prompt(Fp4Atten
     for (int i = 0; i < 16; ++i) o[m][i] = 0.f;
   float top = kNever, sum = 0.f;
   const float factor = a.scale * kLog2e, unit = E4M3 ? 1.f : factor;  // 8 bits: the factor is in the keys' scales
-  // does everything in the tile from j on count for all rows of places from i0 to i1?
-  auto whole = [&](const Ids& id, int j, int i0, int i1) {
-    return j + kTokens <= range.n && j + kTokens - 1 <= i0 && (a.window == 0 || j > i1 - a.window || j + kTokens <= a.sinks) &&
-           (id.page[0] | id.page[1] | id.page[2] | id.page[3]) >= 0;
+  // A tile of pages that are all there counts whole, for every row from `low` to `high`, if its first token is at most `upto` and, with a
+  // window, at least `from` or one of so few that it ends with the first tokens.
+  struct Whole {
+    int upto, from, ends;
+    __device__ Whole(const Range& r, int low, int high, int window, int sinks) {
+      upto = min(r.n, low + 1) - kTokens;
+      from = window ? high - window + 1 : 0;
+      ends = sinks - kTokens;
+    }
+    __device__ bool operator()(bool held, int j) const { return held & (j <= upto) & ((j >= from) | (j <= ends)); }
+  };
+  const int r0 = tile * kRows, rw = r0 + wave * 32;
+  const Whole for_all(range, base + r0 / group, base + min(r0 + kRows - 1, last) / group, a.window, a.sinks);
+  const Whole for_wave(range, base + min(rw, last) / group, base + min(rw + 31, last) / group, a.window, a.sinks);
+  auto held = [](const Ids& id) { return (id.page[0] | id.page[1] | id.page[2] | id.page[3]) >= 0; };
+  auto scores = [&](int t, v16f (&acc)[2], int u, int i) {  // one product of tile t
+    const int r = lane & 31, row = 32 * u + ((r & 0x13) | ((r & 4) << 1) | ((r & 8) >> 1));
+    const v8bf k = __builtin_bit_cast(v8bf, *reinterpret_cast<const v4u*>(&lds.k[t & 1][row][16 * i + 8 * half]));
+    acc[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[i], acc[u], 0, 0, 0);
   };
 
-  Staged<D, E4M3> next;
-  const Fetch<D, E4M3> fetch(c, tid);
-  Ids id = ids_of(c, pages, range, 0), ahead = ids_of(c, pages, range, 1);
-  bool some = false;  // not all rows see all of the tile that lies in LDS
+  // Tile `it` is worked on while the products of it + 1's scores run, and keys of it + 2 and values of it + 1 are on their way.
+  // Of eight waves four bring the values and four the keys; four waves bring both.
+  Part<D, E4M3> part[WAVES == 8 ? 1 : 2];
+  Part<D, E4M3>&vpart = part[0], &kpart = part[WAVES == 8 ? 0 : 1];
+  const bool brings_v = WAVES == 4 || wave < 4, brings_k = WAVES == 4 || wave >= 4;
+  const int g = wave & 3;
+  const Fetch<D, E4M3> fetch(c, lane);
+  Ids id = ids_of(c, pages, range, 0), id1 = ids_of(c, pages, range, 1), id2 = ids_of(c, pages, range, 2);
   if (tid < 4) lds.odd[tid] = 0;
   __syncthreads();
+  v16f acc[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[u][i] = 0.f;
   if (range.tiles > 0) {
     const int j = range.first_of(0);
-    fetch(next, c, head, id, j, wave, tid);
-    some = !whole(id, j, g0, g1);
-    store<D, E4M3>(lds, next, 0, id, j, range.n, factor, some, &lds.odd[0], wave, tid);
+    if (brings_v) {
+      fetch.values(vpart, c, head, id, j, g, lane);
+      store_values<D, E4M3>(lds, vpart, 0, id, j, range.n, !for_all(held(id), j), g, lane);
+    }
+    if (brings_k) {
+      fetch.keys(kpart, c, head, id, j, g, lane);
+      store_keys<D, E4M3>(lds, kpart, 0, factor, g, lane);
+      fetch.keys(kpart, c, head, id1, range.first_of(1), g, lane);
+      store_keys<D, E4M3>(lds, kpart, 1, factor, g, lane);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) scores(0, acc, u, i);
   }
-  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) arrived(q[i]);
   for (int it = 0; it < range.tiles; ++it) {
-    const int buf = it & 1, j = range.first_of(it), jn = range.first_of(it + 1);
+    const int j = range.first_of(it), j1 = range.first_of(it + 1);
     const bool more = it + 1 < range.tiles;
-    if (more) fetch(next, c, head, ahead, jn, wave, tid);
-    const Ids after = ids_of(c, pages, range, it + 2);
+    // past the last tile too, from page 0 then: a branch around loads makes every later use of their registers wait for them
+    if (brings_v) fetch.values(vpart, c, head, id1, j1, g, lane);
+    if (brings_k) fetch.keys(kpart, c, head, id2, range.first_of(it + 2), g, lane);
+    const Ids id3 = ids_of(c, pages, range, it + 3);
     if (tid == 0) lds.odd[(it + 2) & 3] = 0;  // read two tiles ago, next written behind the next barrier
-    const bool hidden = j > w1 || (a.window && j + kTokens - 1 <= w0 - a.window && j >= a.sinks);
-    if (!hidden) {
-      // scores as plain floats: changing elements of a matrix register under a branch was compiled wrongly (D = 256, one
-      // element copied over all others, by the clang of ROCm 7.2)
-      float s[2][16];
+    // scores as plain floats: changing elements of a matrix register under a branch was compiled wrongly (D = 256, one
+    // element copied over all others, by the clang of ROCm 7.2)
+    float s[2][16];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        v16f acc;
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-        const int r = lane & 31, t = 32 * u + ((r & 0x13) | ((r & 4) << 1) | ((r & 8) >> 1));
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const v8bf k = __builtin_bit_cast(v8bf, *reinterpret_cast<const v4u*>(&lds.k[buf][t][16 * i + 8 * half]));
-          acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[i], acc, 0, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          s[u][i] = acc[i];
-          if (E4M3) s[u][i] *= lds.scales[buf][0][32 * u + 16 * (i / 8) + 8 * half + i % 8];
-        }
+      for (int i = 0; i < 16; ++i) {
+        s[u][i] = acc[u][i];
+        if (E4M3) s[u][i] *= lds.scales[it & 3][0][32 * u + 16 * (i / 8) + 8 * half + i % 8];
       }
-      const bool all = whole(id, j, w0, w1);
-      if (!all) {
-        const int from = a.window ? place - a.window : -1, to = min(place, range.n - 1);
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int at = j + 32 * u + 16 * (i / 8) + 8 * half + i % 8;
-            const bool on = (at <= to) & ((at > from) | (at < a.sinks)) & (id.page[2 * u + i / 8] >= 0);
-            s[u][i] = on ? s[u][i] : kNever;
-          }
-      }
-      float z = fmaxf(s[0][0], s[1][0]);
-#pragma unroll
-      for (int i = 1; i < 16; ++i) z = fmaxf(fmaxf(z, s[0][i]), s[1][i]);
-      z = max_across<32>(z) * unit;
-      if (__any(z > top + kSlack)) {
-        const float m = fmaxf(top, z), keep = m == top ? 1.f : exp2_hw(top - m);
-        top = m;
-        sum *= keep;
-#pragma unroll
-        for (int m2 = 0; m2 < D / 32; ++m2)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[m2][i] *= keep;
-      }
-      const float m = top == kNever ? 0.f : top;
-      if (some) {
-        if (const unsigned long long odd = lds.odd[it & 3]) {  // a row that sees such a token is none of numbers
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (((odd >> (32 * u + 16 * (i / 8) + 8 * half + i % 8)) & 1) && s[u][i] != kNever) sum = __builtin_nanf("");
-        }
-      }
-      v8bf p[2][2];
+    if (!for_wave(held(id), j)) {
+      // the lane's tokens j + 8 half + {0 .. 7, 16 .. 23, 32 .. 39, 48 .. 55} against what its row sees, from that place on
+      const int at = j + 8 * half, to = min(place, range.n - 1) - at, from = (a.window ? place - a.window : -1) - at, first = a.sinks - at;
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          v4u w;
-#pragma unroll
-          for (int i = 0; i < 8; i += 2) {
-            float x[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) x[k] = exp2_hw(__builtin_fmaf(s[u][8 * e + i + k], unit, -m));
-            if constexpr (E4M3) {
-              sum += x[0] + x[1];
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const float y = x[k] * lds.scales[buf][1][32 * u + 16 * e + 8 * half + i + k];
-                x[k] = s[u][8 * e + i + k] == kNever ? 0.f : y;  // a hidden token's scale may be anything
-              }
-            }
-            w[i / 2] = bf16_pair(x[0], x[1]);
-            if (!E4M3) sum = add_pair(w[i / 2], sum);
-          }
-          p[u][e] = __builtin_bit_cast(v8bf, w);
+        for (int i = 0; i < 16; ++i) {
+          const int t = 32 * u + 16 * (i / 8) + i % 8;
+          const bool on = (t <= to) & ((t > from) | (t < first)) & (id.page[2 * u + i / 8] >= 0);
+          s[u][i] = on ? s[u][i] : kNever;
         }
-#pragma unroll
-      for (int m2 = 0; m2 < D / 32; ++m2)
+    }
+    if (!for_all(held(id), j)) {
+      if (const unsigned long long odd = lds.odd[it & 3]) {  // a row that sees such a token is none of numbers
+        const unsigned bits[2] = {(unsigned)(odd >> (8 * half)), (unsigned)(odd >> (32 + 8 * half))};
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const v8bf v = __builtin_bit_cast(
-                v8bf, *reinterpret_cast<const v4u*>(&lds.v[buf][32 * m2 + (lane & 31)][32 * u + 16 * e + 8 * half]));
-            o[m2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[u][e], o[m2], 0, 0, 0);
-          }
+          for (int i = 0; i < 16; ++i)
+            if ((bits[u] & (1u << (16 * (i / 8) + i % 8))) && s[u][i] != kNever) sum = __builtin_nanf("");
+      }
     }
+    float z = fmaxf(s[0][0], s[1][0]);
+#pragma unroll
+    for (int i = 1; i < 16; ++i) z = fmaxf(fmaxf(z, s[0][i]), s[1][i]);
+    z = max_across<32>(z) * unit;
+    if (__any(z > top + kSlack)) {
+      const float m = fmaxf(top, z), keep = m == top ? 1.f : exp2_hw(top - m);
+      top = m;
+      sum *= keep;
+#pragma unroll
+      for (int m2 = 0; m2 < D / 32; ++m2)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[m2][i] *= keep;
+    }
+    const float m = top == kNever ? 0.f : top;
+    unsigned w[16];
+    auto weigh = [&](int n) {  // p of scores 2 n and 2 n + 1
+      float x[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int u = n / 8, i = 2 * (n % 8) + k;
+        x[k] = exp2_hw(__builtin_fmaf(s[u][i], unit, -m));
+        if constexpr (E4M3) {
+          sum += x[k];
+          const float y = x[k] * lds.scales[it & 3][1][32 * u + 16 * (i / 8) + 8 * half + i % 8];
+          x[k] = s[u][i] == kNever ? 0.f : y;  // a hidden token's scale may be anything
+        }
+      }
+      w[n] = bf16_pair(x[0], x[1]);
+      if (!E4M3) sum = add_pair(w[n], sum);
+    };
+    auto add = [&](int n, int m2) {  // 16 tokens' part of 32 dims
+      const v8bf p = __builtin_bit_cast(v8bf, v4u{w[4 * n], w[4 * n + 1], w[4 * n + 2], w[4 * n + 3]});
+      const v8bf v = __builtin_bit_cast(v8bf, *reinterpret_cast<const v4u*>(&lds.v[it & 1][32 * m2 + (lane & 31)][16 * n + 8 * half]));
+      o[m2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p, o[m2], 0, 0, 0);
+    };
     if (more) {
-      some = !whole(ahead, jn, g0, g1);
-      store<D, E4M3>(lds, next, buf ^ 1, ahead, jn, range.n, factor, some, &lds.odd[(it + 1) & 3], wave, tid);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[u][i] = 0.f;
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        scores(it + 1, acc, n / (D / 16), n % (D / 16));
+#pragma unroll
+        for (int k = 12 * n / (D / 8); k < 12 * (n + 1) / (D / 8); ++k) weigh(k);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 12; ++k) weigh(k);
     }
-    id = ahead;
-    ahead = after;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+#pragma unroll
+      for (int m2 = 0; m2 < D / 32; ++m2) {
+        add(n, m2);
+        if (n < 2) {
+#pragma unroll
+          for (int k = 12 + 4 * (n * (D / 32) + m2) / (D / 16); k < 12 + 4 * (n * (D / 32) + m2 + 1) / (D / 16); ++k) weigh(k);
+        }
+      }
+    }
+    if (brings_v) store_values<D, E4M3>(lds, vpart, it + 1, id1, j1, range.n, !for_all(held(id1), j1), g, lane);
+    if (brings_k) store_keys<D, E4M3>(lds, kpart, it + 2, factor, g, lane);
+    id = id1;
+    id1 = id2;
+    id2 = id3;
     __syncthreads();
   }
   sum = sum_across<32>(sum);
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   // rows of out through LDS: a wave's 32 rows, D + 8 elements apart
   uint16_t* mem = reinterpret_cast<uint16_t*>(memory) + wave * 32 * (D + 8);
-  constexpr int VDIM = Staged<D, E4M3>::VDIM;
+  constexpr int VDIM = Part<D, E4M3>::VDIM;
 #pragma unroll
   for (int m2 = 0; m2 < D / 32; ++m2)
 #pragma unroll
@@ -395,24 +440,34 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void prompt(Fp4Atten
   }
 }
 
-template <int D, bool E4M3>
-hipError_t launch(const Fp4AttentionArgs& a, hipStream_t st) {
-  const int group = a.q_heads / a.cache.heads;
-  const int64_t tiles = ((int64_t)a.T * group + kRows - 1) / kRows + a.cache.batch;
+template <int D, bool E4M3, int WAVES>
+hipError_t launch(const Fp4AttentionArgs& a, int dev, hipStream_t st) {
+  const int group = a.q_heads / a.cache.heads, rows = 32 * WAVES;
+  const int64_t tiles = ((int64_t)a.T * group + rows - 1) / rows + a.cache.batch;
   constexpr int bytes = sizeof(Lds<D, E4M3>);
   static std::atomic<int> ready[64];  // by device
-  auto kern = prompt<D, E4M3>;
-  int dev = 0;
-  hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess) return e;
+  auto kern = prompt<D, E4M3, WAVES>;
   const bool cached = dev >= 0 && dev < 64;
   if (!cached || !ready[dev].load(std::memory_order_acquire)) {
-    e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
     if (cached) ready[dev].store(1, std::memory_order_release);
   }
-  hipLaunchKernelGGL(kern, dim3((unsigned)(tiles * a.cache.heads)), dim3(64 * kWaves), bytes, st, a, group, (int)tiles);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(tiles * a.cache.heads)), dim3(64 * WAVES), bytes, st, a, group, (int)tiles);
   return hipGetLastError();
+}
+
+template <int D, bool E4M3>
+hipError_t launch(const Fp4AttentionArgs& a, hipStream_t st) {
+  int dev = 0, cus = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e == hipSuccess) e = fp4_device_cus(dev, &cus);
+  if (e != hipSuccess) return e;
+  if constexpr (D < 256) {
+    // 256 rows share what is brought into LDS, once they fill the CUs
+    if ((int64_t)a.T * a.q_heads >= (int64_t)256 * cus) return launch<D, E4M3, 8>(a, dev, st);
+  }
+  return launch<D, E4M3, 4>(a, dev, st);
 }
 
 }  // namespace

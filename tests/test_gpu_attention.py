@@ -228,6 +228,14 @@ def test_long_decode_is_split():
         run(c, 2, window=9001, sinks=70)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("D,Hq,H,window,sinks", [(64, 64, 4, 0, 0), (64, 66, 2, 150, 20), (128, 64, 64, 0, 0), (128, 64, 8, 333, 0)])
+def test_rows_that_fill_the_gpu(D, Hq, H, window, sinks, e4m3):
+    """More than 256 rows for every CU: the tiles of 256 rows."""
+    c = Cache([900, 70, 520, 1], H, D, 32, e4m3, "tokens").fill()
+    run(c, Hq, [600, 70, 400, 1], window=window, sinks=sinks, pad=2)
+
+
 def test_few_rows_over_a_long_cache():
     c = Cache([9000, 5000], 2, 128, 64, True).fill()
     run(c, 8, [3, 17])
