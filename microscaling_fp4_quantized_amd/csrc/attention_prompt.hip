@@ -137,8 +137,8 @@ __device__ __forceinline__ void store_keys(Lds<D, E4M3>& lds, const Part<D, E4M3
   if (E4M3 && g == 0) lds.scales[tile & 3][0][lane] = x.scale * factor;
 }
 
-// Fetched values into LDS, turned. With `some` (not all rows see all of the tile's tokens) values from token n on, of pages that
-// are none and those that are no numbers are 0, and the tokens of the last are noted.
+// Fetched values into LDS, turned. With `some` (not all rows see all of the tile's tokens) values and scales from token n on,
+// of pages that are none and those that are no numbers are 0, and the tokens of the last are noted.
 template <int D, bool E4M3>
 __device__ __forceinline__ void store_values(Lds<D, E4M3>& lds, const Part<D, E4M3>& x, int tile, const Ids& id, int j, int n, bool some,
                                              int g, int lane) {
@@ -161,7 +161,17 @@ __device__ __forceinline__ void store_values(Lds<D, E4M3>& lds, const Part<D, E4
           w[i][k] = raw;
         }
       }
-    if (some) {
+    auto turn = [&] {
+#pragma unroll
+      for (int k = 0; k < P::VDIM / 2; ++k) {
+        const int row = u * 128 + 32 * k + (lane & 15);  // dim 128 u + VDIM (row % 16) + row / 16
+        *reinterpret_cast<v2u*>(&lds.v[tile & 1][row][t]) = v2u{low_halves(w[0][k], w[1][k]), low_halves(w[2][k], w[3][k])};
+        *reinterpret_cast<v2u*>(&lds.v[tile & 1][row + 16][t]) = v2u{high_halves(w[0][k], w[1][k]), high_halves(w[2][k], w[3][k])};
+      }
+    };
+    if (!some) {
+      turn();
+    } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const bool on = held && j + t + i < n;
@@ -172,15 +182,19 @@ __device__ __forceinline__ void store_values(Lds<D, E4M3>& lds, const Part<D, E4
 #pragma unroll
         for (int k = 0; k < P::VDIM / 2; ++k) w[i][k] = on && !bad ? w[i][k] : 0u;
       }
-    }
-#pragma unroll
-    for (int k = 0; k < P::VDIM / 2; ++k) {
-      const int row = u * 128 + 32 * k + (lane & 15);  // dim 128 u + VDIM (row % 16) + row / 16
-      *reinterpret_cast<v2u*>(&lds.v[tile & 1][row][t]) = v2u{low_halves(w[0][k], w[1][k]), low_halves(w[2][k], w[3][k])};
-      *reinterpret_cast<v2u*>(&lds.v[tile & 1][row + 16][t]) = v2u{high_halves(w[0][k], w[1][k]), high_halves(w[2][k], w[3][k])};
+      turn();
     }
   }
-  if (E4M3 && g == 0) lds.scales[tile & 3][1][lane] = x.scale;
+  if (E4M3 && g == 0) {
+    float scale = x.scale;
+    if (some) {
+      const bool on = j + lane < n && pick(id, lane >> 4) >= 0;
+      const bool bad = !(fabsf(scale) < __builtin_inff());
+      if (on && bad) atomicOr(&lds.odd[tile & 3], 1ull << lane);
+      scale = on && !bad ? scale : 0.f;
+    }
+    lds.scales[tile & 3][1][lane] = scale;
+  }
 }
 
 // Rows of a sequence: new tokens times the heads of a group.
@@ -325,26 +339,31 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt(Fp4Attent
         s[u][i] = acc[u][i];
         if (E4M3) s[u][i] *= lds.scales[it & 3][0][32 * u + 16 * (i / 8) + 8 * half + i % 8];
       }
+    unsigned hidden = 0;  // bit 8 n + k: the lane's token j + 8 half + 16 n + k, which its row does not see
     if (!for_wave(held(id), j)) {
-      // the lane's tokens j + 8 half + {0 .. 7, 16 .. 23, 32 .. 39, 48 .. 55} against what its row sees, from that place on
-      const int at = j + 8 * half, to = min(place, range.n - 1) - at, from = (a.window ? place - a.window : -1) - at, first = a.sinks - at;
+      const int at = j + 8 * half, to = min(place, range.n - 1) - at;
+      const int from = (a.window ? place - a.window : -1) - at, first = a.sinks - at;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        auto below = [&](int t) { return (1u << min(max(t - 16 * n, 0), 8)) - 1; };  // of the 8, those before token t
+        unsigned seen = below(to + 1) & (~below(from + 1) | below(first));
+        if (id.page[n] < 0) seen = 0;
+        hidden |= (~seen & 0xFFu) << (8 * n);
+      }
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int t = 32 * u + 16 * (i / 8) + i % 8;
-          const bool on = (t <= to) & ((t > from) | (t < first)) & (id.page[2 * u + i / 8] >= 0);
-          s[u][i] = on ? s[u][i] : kNever;
+          const unsigned off = (unsigned)((int)(hidden << (31 - 16 * u - i)) >> 31);
+          s[u][i] = __uint_as_float((__float_as_uint(s[u][i]) & ~off) | (__float_as_uint(kNever) & off));
         }
     }
     if (!for_all(held(id), j)) {
       if (const unsigned long long odd = lds.odd[it & 3]) {  // a row that sees such a token is none of numbers
-        const unsigned bits[2] = {(unsigned)(odd >> (8 * half)), (unsigned)(odd >> (32 + 8 * half))};
+        unsigned bits = 0;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if ((bits[u] & (1u << (16 * (i / 8) + i % 8))) && s[u][i] != kNever) sum = __builtin_nanf("");
+        for (int n = 0; n < 4; ++n) bits |= ((unsigned)(odd >> (16 * n + 8 * half)) & 0xFFu) << (8 * n);
+        if (bits & ~hidden) sum = __builtin_nanf("");
       }
     }
     float z = fmaxf(s[0][0], s[1][0]);
@@ -370,8 +389,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt(Fp4Attent
         x[k] = exp2_hw(__builtin_fmaf(s[u][i], unit, -m));
         if constexpr (E4M3) {
           sum += x[k];
-          const float y = x[k] * lds.scales[it & 3][1][32 * u + 16 * (i / 8) + 8 * half + i % 8];
-          x[k] = s[u][i] == kNever ? 0.f : y;  // a hidden token's scale may be anything
+          x[k] *= lds.scales[it & 3][1][32 * u + 16 * (i / 8) + 8 * half + i % 8];
         }
       }
       w[n] = bf16_pair(x[0], x[1]);
