@@ -31,7 +31,7 @@ struct Lds {
   static constexpr int KP = D + 8, VP = kTokens + 8;  // elements of a row
   uint16_t k[2][kTokens][KP];
   uint16_t v[2][D][VP];
-  float scales[4][2][kTokens];
+  float scales[2][2][kTokens];
   unsigned long long odd[4];  // tokens of a tile whose V has an infinity or NaN, where not all rows see all tokens
 };
 
@@ -134,7 +134,7 @@ __device__ __forceinline__ void store_keys(Lds<D, E4M3>& lds, const Part<D, E4M3
       *reinterpret_cast<v4u*>(to) = v4u{w[0], w[1], w[2], w[3]};
     }
   }
-  if (E4M3 && g == 0) lds.scales[tile & 3][0][lane] = x.scale * factor;
+  if (E4M3 && g == 0) lds.scales[tile & 1][0][lane] = x.scale * factor;
 }
 
 // Fetched values into LDS, turned. With `some` (not all rows see all of the tile's tokens) values and scales from token n on,
@@ -193,7 +193,7 @@ __device__ __forceinline__ void store_values(Lds<D, E4M3>& lds, const Part<D, E4
       if (on && bad) atomicOr(&lds.odd[tile & 3], 1ull << lane);
       scale = on && !bad ? scale : 0.f;
     }
-    lds.scales[tile & 3][1][lane] = scale;
+    lds.scales[tile & 1][1][lane] = scale;
   }
 }
 
@@ -207,7 +207,7 @@ __device__ __forceinline__ Rows rows_of(const int* starts, int b, int T) {
 }
 
 template <int D, bool E4M3, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt(Fp4AttentionArgs a, int group, int tiles) {
+__global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 4 : 2) void prompt(Fp4AttentionArgs a, int group, int tiles) {
   extern __shared__ __align__(16) uint8_t memory[];
   typedef Lds<D, E4M3> L;
   constexpr int kRows = 32 * WAVES;
@@ -280,27 +280,16 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt(Fp4Attent
   const Whole for_all(range, base + r0 / group, base + min(r0 + kRows - 1, last) / group, a.window, a.sinks);
   const Whole for_wave(range, base + min(rw, last) / group, base + min(rw + 31, last) / group, a.window, a.sinks);
   auto held = [](const Ids& id) { return (id.page[0] | id.page[1] | id.page[2] | id.page[3]) >= 0; };
-  auto scores = [&](int t, v16f (&acc)[2], int u, int i) {  // one product of tile t
-    const int r = lane & 31, row = 32 * u + ((r & 0x13) | ((r & 4) << 1) | ((r & 8) >> 1));
-    const v8bf k = __builtin_bit_cast(v8bf, *reinterpret_cast<const v4u*>(&lds.k[t & 1][row][16 * i + 8 * half]));
-    acc[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[i], acc[u], 0, 0, 0);
-  };
 
-  // Tile `it` is worked on while the products of it + 1's scores run, and keys of it + 2 and values of it + 1 are on their way.
   // Of eight waves four bring the values and four the keys; four waves bring both.
   Part<D, E4M3> part[WAVES == 8 ? 1 : 2];
   Part<D, E4M3>&vpart = part[0], &kpart = part[WAVES == 8 ? 0 : 1];
   const bool brings_v = WAVES == 4 || wave < 4, brings_k = WAVES == 4 || wave >= 4;
   const int g = wave & 3;
   const Fetch<D, E4M3> fetch(c, lane);
-  Ids id = ids_of(c, pages, range, 0), id1 = ids_of(c, pages, range, 1), id2 = ids_of(c, pages, range, 2);
+  Ids id = ids_of(c, pages, range, 0), id1 = ids_of(c, pages, range, 1);
   if (tid < 4) lds.odd[tid] = 0;
   __syncthreads();
-  v16f acc[2];
-#pragma unroll
-  for (int u = 0; u < 2; ++u)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[u][i] = 0.f;
   if (range.tiles > 0) {
     const int j = range.first_of(0);
     if (brings_v) {
@@ -310,35 +299,38 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt(Fp4Attent
     if (brings_k) {
       fetch.keys(kpart, c, head, id, j, g, lane);
       store_keys<D, E4M3>(lds, kpart, 0, factor, g, lane);
-      fetch.keys(kpart, c, head, id1, range.first_of(1), g, lane);
-      store_keys<D, E4M3>(lds, kpart, 1, factor, g, lane);
     }
     __syncthreads();
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) scores(0, acc, u, i);
   }
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) arrived(q[i]);
   for (int it = 0; it < range.tiles; ++it) {
     const int j = range.first_of(it), j1 = range.first_of(it + 1);
-    const bool more = it + 1 < range.tiles;
     // past the last tile too, from page 0 then: a branch around loads makes every later use of their registers wait for them
     if (brings_v) fetch.values(vpart, c, head, id1, j1, g, lane);
-    if (brings_k) fetch.keys(kpart, c, head, id2, range.first_of(it + 2), g, lane);
-    const Ids id3 = ids_of(c, pages, range, it + 3);
+    if (brings_k) fetch.keys(kpart, c, head, id1, j1, g, lane);
+    const Ids id2 = ids_of(c, pages, range, it + 2);
     if (tid == 0) lds.odd[(it + 2) & 3] = 0;  // read two tiles ago, next written behind the next barrier
     // scores as plain floats: changing elements of a matrix register under a branch was compiled wrongly (D = 256, one
     // element copied over all others, by the clang of ROCm 7.2)
     float s[2][16];
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < 2; ++u) {
+      v16f acc;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+      const int r = lane & 31, key = 32 * u + ((r & 0x13) | ((r & 4) << 1) | ((r & 8) >> 1));
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const v8bf k = __builtin_bit_cast(v8bf, *reinterpret_cast<const v4u*>(&lds.k[it & 1][key][16 * i + 8 * half]));
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[i], acc, 0, 0, 0);
+      }
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        s[u][i] = acc[u][i];
-        if (E4M3) s[u][i] *= lds.scales[it & 3][0][32 * u + 16 * (i / 8) + 8 * half + i % 8];
+        s[u][i] = acc[i];
+        if (E4M3) s[u][i] *= lds.scales[it & 1][0][32 * u + 16 * (i / 8) + 8 * half + i % 8];
       }
+    }
     unsigned hidden = 0;  // bit 8 n + k: the lane's token j + 8 half + 16 n + k, which its row does not see
     if (!for_wave(held(id), j)) {
       const int at = j + 8 * half, to = min(place, range.n - 1) - at;
@@ -389,7 +381,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt(Fp4Attent
         x[k] = exp2_hw(__builtin_fmaf(s[u][i], unit, -m));
         if constexpr (E4M3) {
           sum += x[k];
-          x[k] *= lds.scales[it & 3][1][32 * u + 16 * (i / 8) + 8 * half + i % 8];
+          x[k] *= lds.scales[it & 1][1][32 * u + 16 * (i / 8) + 8 * half + i % 8];
         }
       }
       w[n] = bf16_pair(x[0], x[1]);
@@ -400,37 +392,19 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt(Fp4Attent
       const v8bf v = __builtin_bit_cast(v8bf, *reinterpret_cast<const v4u*>(&lds.v[it & 1][32 * m2 + (lane & 31)][16 * n + 8 * half]));
       o[m2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p, o[m2], 0, 0, 0);
     };
-    if (more) {
+    // ahead of the SIMD's other waves from here on: their loads and products fill in behind (547 -> 538 us at 8192 tokens)
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+    for (int k = 0; k < 16; ++k) weigh(k);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[u][i] = 0.f;
+    for (int n = 0; n < 4; ++n)
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n) {
-        scores(it + 1, acc, n / (D / 16), n % (D / 16));
-#pragma unroll
-        for (int k = 12 * n / (D / 8); k < 12 * (n + 1) / (D / 8); ++k) weigh(k);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 12; ++k) weigh(k);
-    }
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-#pragma unroll
-      for (int m2 = 0; m2 < D / 32; ++m2) {
-        add(n, m2);
-        if (n < 2) {
-#pragma unroll
-          for (int k = 12 + 4 * (n * (D / 32) + m2) / (D / 16); k < 12 + 4 * (n * (D / 32) + m2 + 1) / (D / 16); ++k) weigh(k);
-        }
-      }
-    }
+      for (int m2 = 0; m2 < D / 32; ++m2) add(n, m2);
+    __builtin_amdgcn_s_setprio(0);
     if (brings_v) store_values<D, E4M3>(lds, vpart, it + 1, id1, j1, range.n, !for_all(held(id1), j1), g, lane);
-    if (brings_k) store_keys<D, E4M3>(lds, kpart, it + 2, factor, g, lane);
+    if (brings_k) store_keys<D, E4M3>(lds, kpart, it + 1, factor, g, lane);
     id = id1;
     id1 = id2;
-    id2 = id3;
     __syncthreads();
   }
   sum = sum_across<32>(sum);
