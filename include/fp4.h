@@ -458,9 +458,24 @@ FP4_API int fp4_kv_append(const fp4_kv_cache *cache, const int *starts, int64_t 
  * Two launches at most, on `stream`. Results do not depend on timing: partial sums meet in a fixed order.
  * Errors: FP4_E_NULLPTR, FP4_E_SHAPE (also scale, window, sinks and a short workspace), FP4_E_FORMAT (dtype), FP4_E_ALIGN.
  */
-#define FP4_ATTENTION_PIECES(blocks) ((blocks) >= 512 ? 1 : 512 / (blocks))
-#define FP4_ATTENTION_WORKSPACE_BYTES(T, batch, q_heads, heads, dim) \
-  (((size_t)FP4_ATTENTION_PIECES((heads) * (((q_heads) / (heads) + 15) / 16)) + (size_t)(batch)) * (size_t)(q_heads) * ((size_t)(dim) + 2) * 4)
+/* what the workspace holds: a decode call's pieces (one for each sequence and those below for all together), or as many parts of
+ * every row's tokens as it takes to fill the GPU */
+#define FP4_ATTENTION_PIECES(q_heads, heads) \
+  ((heads) * (((q_heads) / (heads) + 15) / 16) >= 512 ? 1 : 512 / ((heads) * (((q_heads) / (heads) + 15) / 16)))
+#define FP4_ATTENTION_MAX_(a, b) ((a) > (b) ? (a) : (b))
+#define FP4_ATTENTION_TILES_(T, batch, q_heads, heads) \
+  (FP4_ATTENTION_MAX_(((int64_t)(T) * ((q_heads) / (heads)) + 127) / 128, (int64_t)(batch)) * (heads))
+#define FP4_ATTENTION_SPLITS(T, batch, q_heads, heads)                      \
+  (FP4_ATTENTION_TILES_(T, batch, q_heads, heads) > 256 ? 1                  \
+   : FP4_ATTENTION_TILES_(T, batch, q_heads, heads) <= 8 ? 64                \
+                                                        : 512 / FP4_ATTENTION_TILES_(T, batch, q_heads, heads))
+#define FP4_ATTENTION_PARTS_(T, batch, q_heads, heads) \
+  FP4_ATTENTION_MAX_((int64_t)FP4_ATTENTION_PIECES(q_heads, heads) + (batch), FP4_ATTENTION_SPLITS(T, batch, q_heads, heads) * (int64_t)(T))
+#define FP4_ATTENTION_WORKSPACE_BYTES(T, batch, q_heads, heads, dim)                                          \
+  ((size_t)(FP4_ATTENTION_SPLITS(T, batch, q_heads, heads) > 1                                                \
+                ? FP4_ATTENTION_PARTS_(T, batch, q_heads, heads)                                              \
+                : (int64_t)FP4_ATTENTION_PIECES(q_heads, heads) + (batch)) *                                  \
+   (size_t)(q_heads) * ((size_t)(dim) + 2) * 4)
 FP4_API int fp4_attention_decode(const fp4_kv_cache *cache, const void *Q, int64_t q_row, int64_t q_head, int q_heads, float scale,
                                  int64_t window, int64_t sinks, void *Out, void *workspace, size_t workspace_bytes,
                                  void *stream);

@@ -256,16 +256,6 @@ __device__ __forceinline__ void work(State<D, E4M3>& st, Raw<D, E4M3>& x, float 
   }
 }
 
-// Partial results in the workspace: [slot][q_heads][D] outputs over their own maxima, then [slot][q_heads] maxima and sums.
-struct Parts {
-  float* o;
-  v2f* ml;
-};
-__device__ __host__ __forceinline__ Parts parts_of(void* workspace, int slots, int q_heads, int dim) {
-  float* o = static_cast<float*>(workspace);
-  return {o, reinterpret_cast<v2f*>(o + (size_t)slots * q_heads * dim)};
-}
-
 template <int D, bool E4M3>
 __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode(Fp4AttentionArgs a, int group, int blocks, int room, int slots) {
   typedef Raw<D, E4M3> R;
@@ -328,7 +318,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode(Fp4Atten
   }
   __syncthreads();
   const float top = fmaxf(fmaxf(tops[0][r], tops[1][r]), fmaxf(tops[2][r], tops[3][r]));
-  const float keep = st.m == kNever ? (st.l == 0.f ? 0.f : 1.f) : exp2_hw(st.m - top);  // l is NaN where a score was, and no maximum
+  const float keep = share_of(v2f{st.m, st.l}, top);
   if (r < heads) {
 #pragma unroll
     for (int n = 0; n < D / 16; ++n)
@@ -352,7 +342,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode(Fp4Atten
       *reinterpret_cast<v2u*>(a.out + ((int64_t)b * a.q_heads + hq) * D + d) =
           v2u{bf16_pair(o[0] * inv, o[1] * inv), bf16_pair(o[2] * inv, o[3] * inv)};
     } else {
-      const Parts parts = parts_of(a.workspace, slots, a.q_heads, D);
+      const Parts parts = parts_of(a.workspace, (size_t)slots * a.q_heads, D);
       *reinterpret_cast<v4f*>(parts.o + ((size_t)slot * a.q_heads + hq) * D + d) = v4f{o[0], o[1], o[2], o[3]};
       if (d == 0) {
         float m = tops[0][h];
@@ -387,7 +377,7 @@ __global__ __launch_bounds__(256) void join(Fp4AttentionArgs a, int room, int sl
     before += wave_total(i + lane < b ? max(1, (span_of(c, i + lane, a.window, a.sinks).tiles() + per - 1) / per) : 0);
   const int count = max(1, (span_of(c, b, a.window, a.sinks).tiles() + per - 1) / per);
   if (count == 1) return;  // written by its only piece
-  const Parts parts = parts_of(a.workspace, slots, a.q_heads, D);
+  const Parts parts = parts_of(a.workspace, (size_t)slots * a.q_heads, D);
   const v2f* ml = parts.ml + (size_t)before * a.q_heads + hq;
   float m = kNever;
   for (int i = 0; i < count; i += 64)
@@ -400,7 +390,7 @@ __global__ __launch_bounds__(256) void join(Fp4AttentionArgs a, int room, int sl
   float l = 0.f;
   for (int i = g; i < count; i += GROUPS) {
     const v2f x = ml[(size_t)i * a.q_heads];
-    const float keep = x[0] == kNever ? (x[1] == 0.f ? 0.f : 1.f) : exp2_hw(x[0] - mm);
+    const float keep = share_of(x, mm);
     const v4f y = *reinterpret_cast<const v4f*>(parts.o + ((size_t)(before + i) * a.q_heads + hq) * D + 4 * e);
     l = __builtin_fmaf(x[1], keep, l);
 #pragma unroll
@@ -426,7 +416,7 @@ template <int D, bool E4M3>
 hipError_t launch(const Fp4AttentionArgs& a, hipStream_t st) {
   const Paged& c = a.cache;
   const int group = a.q_heads / c.heads, blocks = (group + 15) / 16;
-  const int room = FP4_ATTENTION_PIECES(c.heads * blocks);
+  const int room = FP4_ATTENTION_PIECES(a.q_heads, c.heads);
   // what the longest sequence that the table has room for can be cut into
   int64_t tokens = (int64_t)c.cols << c.shift;
   if (a.window && (int64_t)a.window + a.sinks + 2 * kTile < tokens) tokens = (int64_t)a.window + a.sinks + 2 * kTile;

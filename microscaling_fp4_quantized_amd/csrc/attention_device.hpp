@@ -63,6 +63,18 @@ __device__ __forceinline__ int uniform_load(const int* p) {
   return *(const __attribute__((address_space(4))) int*)(reinterpret_cast<uintptr_t>(p));
 }
 
+// Partial results in the workspace: n outputs of D over their own maxima, then n maxima and sums.
+struct Parts {
+  float* o;
+  v2f* ml;
+};
+__device__ __forceinline__ Parts parts_of(void* workspace, size_t n, int dim) {
+  float* o = static_cast<float*>(workspace);
+  return {o, reinterpret_cast<v2f*>(o + n * dim)};
+}
+// What a partial result counts under the common maximum m. Without a maximum its sum is 0, or NaN where a score was.
+__device__ __forceinline__ float share_of(v2f ml, float m) { return ml[0] == kNever ? (ml[1] == 0.f ? 0.f : 1.f) : exp2_hw(ml[0] - m); }
+
 // The low or the high halves of two words, a's in the low half.
 __device__ __forceinline__ unsigned low_halves(unsigned a, unsigned b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
 __device__ __forceinline__ unsigned high_halves(unsigned a, unsigned b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }

@@ -16,12 +16,14 @@
 // its sum is not. 8-bit caches: codes are exact in bf16, the scales are applied in float32 to scores and p.
 #include <atomic>
 
+#include "../../include/fp4.h"
 #include "attention_device.hpp"
 
 namespace fp4 {
 namespace {
 
 constexpr int kTokens = 64;  // of a tile
+constexpr int kMinTiles = 4;  // of a part, where a row's tokens are split over workgroups
 constexpr float kSlack = 8.f;
 
 typedef float v16f __attribute__((ext_vector_type(16)));
@@ -197,6 +199,20 @@ __device__ __forceinline__ void store_values(Lds<D, E4M3>& lds, const Part<D, E4
   }
 }
 
+// What rows at places i0 to i1 look at.
+__device__ __forceinline__ Range range_of(const Paged& c, int len, int i0, int i1, int window, int sinks) {
+  Range r;
+  r.n = min(min(len, paged_room(c)), i1 + 1);
+  const int end = max((r.n + kTokens - 1) / kTokens, 0);
+  r.ta = max((min(sinks, r.n) + kTokens - 1) / kTokens, 0);
+  r.tb = (window ? max(i0 - window + 1, 0) : 0) / kTokens;
+  if (r.tb <= r.ta) r.ta = r.tb = end;
+  r.tiles = r.ta + max(end - r.tb, 0);
+  return r;
+}
+// Parts that are worth a workgroup each, at most.
+__device__ __forceinline__ int worth(const Range& r) { return max(1, (r.tiles + kMinTiles - 1) / kMinTiles); }
+
 // Rows of a sequence: new tokens times the heads of a group.
 struct Rows {
   int first, count;  // its first row of q, and its new tokens
@@ -206,8 +222,10 @@ __device__ __forceinline__ Rows rows_of(const int* starts, int b, int T) {
   return {t0, t1 - t0};
 }
 
-template <int D, bool E4M3, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 4 : 2) void prompt(Fp4AttentionArgs a, int group, int tiles) {
+// SPLIT: blockIdx.y takes one of `splits` parts of its rows' tokens, at most. A kernel of its own, because what it adds to the registers
+// costs heads of 64 4% (455 -> 468 us with a window).
+template <int D, bool E4M3, int WAVES, bool SPLIT>
+__global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 4 : 2) void prompt(Fp4AttentionArgs a, int group, int tiles, int splits) {
   extern __shared__ __align__(16) uint8_t memory[];
   typedef Lds<D, E4M3> L;
   constexpr int kRows = 32 * WAVES;
@@ -240,17 +258,11 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 4 : 2) void pr
   const int mine = min(row, last), token = mine / group, place = base + token;
   const int* pages = c.table + b * c.table_stride;
 
-  Range range;
-  {
-    const int i0 = base + tile * kRows / group, i1 = base + min(tile * kRows + kRows - 1, last) / group;
-    range.n = min(min(len, paged_room(c)), i1 + 1);
-    const int lo = a.window ? max(i0 - a.window + 1, 0) : 0;
-    const int end = max((range.n + kTokens - 1) / kTokens, 0);
-    range.ta = max((min(a.sinks, range.n) + kTokens - 1) / kTokens, 0);
-    range.tb = lo / kTokens;
-    if (range.tb <= range.ta) range.ta = range.tb = end;
-    range.tiles = range.ta + max(end - range.tb, 0);
-  }
+  const Range range = range_of(c, len, base + tile * kRows / group, base + min(tile * kRows + kRows - 1, last) / group, a.window, a.sinks);
+  const int parts = SPLIT ? min(splits, worth(range)) : 1, part = SPLIT ? blockIdx.y : 0;
+  if (part >= parts) return;
+  const int from = SPLIT ? (int)((int64_t)range.tiles * part / parts) : 0;
+  const int end = SPLIT ? (int)((int64_t)range.tiles * (part + 1) / parts) : range.tiles;
   const int half = lane >> 5;
   v8bf q[D / 16];
   {
@@ -282,29 +294,29 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 4 : 2) void pr
   auto held = [](const Ids& id) { return (id.page[0] | id.page[1] | id.page[2] | id.page[3]) >= 0; };
 
   // Of eight waves four bring the values and four the keys; four waves bring both.
-  Part<D, E4M3> part[WAVES == 8 ? 1 : 2];
-  Part<D, E4M3>&vpart = part[0], &kpart = part[WAVES == 8 ? 0 : 1];
+  Part<D, E4M3> bring[WAVES == 8 ? 1 : 2];
+  Part<D, E4M3>&vpart = bring[0], &kpart = bring[WAVES == 8 ? 0 : 1];
   const bool brings_v = WAVES == 4 || wave < 4, brings_k = WAVES == 4 || wave >= 4;
   const int g = wave & 3;
   const Fetch<D, E4M3> fetch(c, lane);
-  Ids id = ids_of(c, pages, range, 0), id1 = ids_of(c, pages, range, 1);
+  Ids id = ids_of(c, pages, range, from), id1 = ids_of(c, pages, range, from + 1);
   if (tid < 4) lds.odd[tid] = 0;
   __syncthreads();
-  if (range.tiles > 0) {
-    const int j = range.first_of(0);
+  if (from < end) {
+    const int j = range.first_of(from);
     if (brings_v) {
       fetch.values(vpart, c, head, id, j, g, lane);
-      store_values<D, E4M3>(lds, vpart, 0, id, j, range.n, !for_all(held(id), j), g, lane);
+      store_values<D, E4M3>(lds, vpart, from, id, j, range.n, !for_all(held(id), j), g, lane);
     }
     if (brings_k) {
       fetch.keys(kpart, c, head, id, j, g, lane);
-      store_keys<D, E4M3>(lds, kpart, 0, factor, g, lane);
+      store_keys<D, E4M3>(lds, kpart, from, factor, g, lane);
     }
     __syncthreads();
   }
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) arrived(q[i]);
-  for (int it = 0; it < range.tiles; ++it) {
+  for (int it = from; it < end; ++it) {
     const int j = range.first_of(it), j1 = range.first_of(it + 1);
     // past the last tile too, from page 0 then: a branch around loads makes every later use of their registers wait for them
     if (brings_v) fetch.values(vpart, c, head, id1, j1, g, lane);
@@ -408,10 +420,28 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 4 : 2) void pr
     __syncthreads();
   }
   sum = sum_across<32>(sum);
+  constexpr int VDIM = Part<D, E4M3>::VDIM;
+  if (SPLIT && parts > 1) {
+    // a lane has VDIM dims in a row of every eighth: (m2 / 4) 128 + VDIM r + {0 .. VDIM - 1}
+    if (row <= last) {
+      const size_t n = (size_t)a.T * a.q_heads, at = part * n + (size_t)(rows.first + token) * a.q_heads + head * group + (row - token * group);
+      const Parts to = parts_of(a.workspace, splits * n, D);
+#pragma unroll
+      for (int p = 0; p < D / 32; p += VDIM / 2)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int k = 0; k < VDIM / 2; k += 2) {
+            float* y = to.o + at * D + (p / 4) * 128 + VDIM * (8 * (i / 4) + 4 * half + i % 4) + 2 * k;
+            *reinterpret_cast<v4f*>(y) = v4f{o[p + k][i], o[p + k][i + 8], o[p + k + 1][i], o[p + k + 1][i + 8]};
+          }
+      if (half == 0) to.ml[at] = v2f{top, sum};
+    }
+    return;
+  }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   // rows of out through LDS: a wave's 32 rows, D + 8 elements apart
   uint16_t* mem = reinterpret_cast<uint16_t*>(memory) + wave * 32 * (D + 8);
-  constexpr int VDIM = Part<D, E4M3>::VDIM;
 #pragma unroll
   for (int m2 = 0; m2 < D / 32; ++m2)
 #pragma unroll
@@ -432,20 +462,58 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 4 : 2) void pr
   }
 }
 
-template <int D, bool E4M3, int WAVES>
-hipError_t launch(const Fp4AttentionArgs& a, int dev, hipStream_t st) {
+// out = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p over the parts of a row and head, where there is more than one. D / 4 lanes for
+// a head, 1024 / D heads of a token in a workgroup.
+template <int D>
+__global__ __launch_bounds__(256) void join(Fp4AttentionArgs a, int group, int tile_rows, int splits) {
+  constexpr int LANES = D / 4;
+  const Paged& c = a.cache;
+  const int t = blockIdx.x, h = blockIdx.y * (256 / LANES) + threadIdx.x / LANES, e = 4 * (threadIdx.x % LANES);
+  const int b = __builtin_amdgcn_readfirstlane(sequence_of(a.starts, c.batch, t));
+  if (b < 0 || h >= a.q_heads) return;
+  const Rows rows = rows_of(a.starts, b, a.T);
+  const int len = length_of(c, b), base = len - rows.count, last = rows.count * group - 1;
+  const int first = ((t - rows.first) * group + h % group) / tile_rows * tile_rows;
+  const int parts = min(splits, worth(range_of(c, len, base + first / group, base + min(first + tile_rows - 1, last) / group,
+                                                  a.window, a.sinks)));
+  if (parts == 1) return;  // written by its only part
+  const size_t n = (size_t)a.T * a.q_heads, at = (size_t)t * a.q_heads + h;
+  const Parts from = parts_of(a.workspace, splits * n, D);
+  float m = kNever;
+  for (int p = 0; p < parts; ++p) m = fmaxf(m, from.ml[p * n + at][0]);
+  v4f o{0.f, 0.f, 0.f, 0.f};
+  float l = 0.f;
+  for (int p = 0; p < parts; ++p) {
+    const v2f ml = from.ml[p * n + at];
+    const v4f y = *reinterpret_cast<const v4f*>(from.o + (p * n + at) * D + e);
+    const float keep = share_of(ml, m);
+    l = __builtin_fmaf(ml[1], keep, l);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = __builtin_fmaf(y[k], keep, o[k]);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  *reinterpret_cast<v2u*>(a.out + at * D + e) = v2u{bf16_pair(o[0] * inv, o[1] * inv), bf16_pair(o[2] * inv, o[3] * inv)};
+}
+
+template <int D, bool E4M3, int WAVES, bool SPLIT>
+hipError_t launch(const Fp4AttentionArgs& a, int splits, int dev, hipStream_t st) {
   const int group = a.q_heads / a.cache.heads, rows = 32 * WAVES;
   const int64_t tiles = ((int64_t)a.T * group + rows - 1) / rows + a.cache.batch;
   constexpr int bytes = sizeof(Lds<D, E4M3>);
   static std::atomic<int> ready[64];  // by device
-  auto kern = prompt<D, E4M3, WAVES>;
+  auto kern = prompt<D, E4M3, WAVES, SPLIT>;
   const bool cached = dev >= 0 && dev < 64;
+  hipError_t e = hipSuccess;
   if (!cached || !ready[dev].load(std::memory_order_acquire)) {
-    const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
     if (cached) ready[dev].store(1, std::memory_order_release);
   }
-  hipLaunchKernelGGL(kern, dim3((unsigned)(tiles * a.cache.heads)), dim3(64 * WAVES), bytes, st, a, group, (int)tiles);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(tiles * a.cache.heads), splits), dim3(64 * WAVES), bytes, st, a, group, (int)tiles, splits);
+  e = hipGetLastError();
+  if (e != hipSuccess || !SPLIT) return e;
+  constexpr int heads = 1024 / D;
+  hipLaunchKernelGGL((join<D>), dim3((unsigned)a.T, (unsigned)((a.q_heads + heads - 1) / heads)), dim3(256), 0, st, a, group, rows, splits);
   return hipGetLastError();
 }
 
@@ -455,11 +523,19 @@ hipError_t launch(const Fp4AttentionArgs& a, hipStream_t st) {
   hipError_t e = hipGetDevice(&dev);
   if (e == hipSuccess) e = fp4_device_cus(dev, &cus);
   if (e != hipSuccess) return e;
+  // few rows: their tokens split over workgroups, as far as the longest sequence that the table has room for goes
+  const Paged& c = a.cache;
+  int64_t tokens = (int64_t)c.cols << c.shift;
+  if (a.window && (int64_t)a.window + a.sinks + 32 * 8 < tokens) tokens = (int64_t)a.window + a.sinks + 32 * 8;
+  const int64_t most = (tokens + kMinTiles * kTokens - 1) / (kMinTiles * kTokens);
+  int64_t splits = FP4_ATTENTION_SPLITS(a.T, c.batch, a.q_heads, c.heads);
+  if (splits > most) splits = most;
   if constexpr (D < 256) {
     // 256 rows share what is brought into LDS, once they fill the CUs
-    if ((int64_t)a.T * a.q_heads >= (int64_t)256 * cus) return launch<D, E4M3, 8>(a, dev, st);
+    if ((int64_t)a.T * a.q_heads * splits >= (int64_t)256 * cus)
+      return splits > 1 ? launch<D, E4M3, 8, true>(a, (int)splits, dev, st) : launch<D, E4M3, 8, false>(a, 1, dev, st);
   }
-  return launch<D, E4M3, 4>(a, dev, st);
+  return splits > 1 ? launch<D, E4M3, 4, true>(a, (int)splits, dev, st) : launch<D, E4M3, 4, false>(a, 1, dev, st);
 }
 
 }  // namespace
