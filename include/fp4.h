@@ -396,7 +396,7 @@ FP4_API int fp4_moe_experts(const void *X, int64_t T, int64_t D, int64_t ldx, co
  *  k_scales, v_scales  device float, 4-byte aligned, strides >= 1 and at most 2^40; NULL exactly with FP4_KV_BF16.
  *  table       device int [batch, cols], row stride table_stride >= cols. A page id outside [0, pages) (-1, say) is no page: its
  *              tokens are not visible and nothing is written for them.
- *  cols        >= 1, cols * page_size <= 2^30: tokens past that are as tokens of no page.
+ *  cols        >= 1, cols * page_size <= 2^30, times batch <= 2^35: tokens past that are as tokens of no page.
  *  lengths     device int [batch]; below 0 counts as 0, above 2^30 as 2^30.
  *  batch       1..65535, batch * query heads <= 2^22.
  */
@@ -460,8 +460,11 @@ FP4_API int fp4_kv_append(const fp4_kv_cache *cache, const int *starts, int64_t 
  */
 /* what the workspace holds: a decode call's pieces (one for each sequence and those below for all together), or as many parts of
  * every row's tokens as it takes to fill the GPU */
-#define FP4_ATTENTION_PIECES(q_heads, heads) \
-  ((heads) * (((q_heads) / (heads) + 15) / 16) >= 512 ? 1 : 512 / ((heads) * (((q_heads) / (heads) + 15) / 16)))
+#define FP4_ATTENTION_BLOCKS_(q_heads, heads) ((heads) * (((q_heads) / (heads) + 15) / 16))
+#define FP4_ATTENTION_ROUND_(q_heads, heads) \
+  (FP4_ATTENTION_BLOCKS_(q_heads, heads) >= 512 ? 1 : 512 / FP4_ATTENTION_BLOCKS_(q_heads, heads))
+#define FP4_ATTENTION_PIECES(batch, q_heads, heads) \
+  ((int)(((int64_t)(batch) + FP4_ATTENTION_ROUND_(q_heads, heads) - 1) / FP4_ATTENTION_ROUND_(q_heads, heads) * FP4_ATTENTION_ROUND_(q_heads, heads)))
 #define FP4_ATTENTION_MAX_(a, b) ((a) > (b) ? (a) : (b))
 #define FP4_ATTENTION_TILES_(T, batch, q_heads, heads) \
   (FP4_ATTENTION_MAX_(((int64_t)(T) * ((q_heads) / (heads)) + 127) / 128, (int64_t)(batch)) * (heads))
@@ -470,11 +473,12 @@ FP4_API int fp4_kv_append(const fp4_kv_cache *cache, const int *starts, int64_t 
    : FP4_ATTENTION_TILES_(T, batch, q_heads, heads) <= 8 ? 64                \
                                                         : 512 / FP4_ATTENTION_TILES_(T, batch, q_heads, heads))
 #define FP4_ATTENTION_PARTS_(T, batch, q_heads, heads) \
-  FP4_ATTENTION_MAX_((int64_t)FP4_ATTENTION_PIECES(q_heads, heads) + (batch), FP4_ATTENTION_SPLITS(T, batch, q_heads, heads) * (int64_t)(T))
+  FP4_ATTENTION_MAX_((int64_t)FP4_ATTENTION_PIECES(batch, q_heads, heads) + (batch), \
+                     FP4_ATTENTION_SPLITS(T, batch, q_heads, heads) * (int64_t)(T))
 #define FP4_ATTENTION_WORKSPACE_BYTES(T, batch, q_heads, heads, dim)                                          \
   ((size_t)(FP4_ATTENTION_SPLITS(T, batch, q_heads, heads) > 1                                                \
                 ? FP4_ATTENTION_PARTS_(T, batch, q_heads, heads)                                              \
-                : (int64_t)FP4_ATTENTION_PIECES(q_heads, heads) + (batch)) *                                  \
+                : (int64_t)FP4_ATTENTION_PIECES(batch, q_heads, heads) + (batch)) *                           \
    (size_t)(q_heads) * ((size_t)(dim) + 2) * 4)
 FP4_API int fp4_attention_decode(const fp4_kv_cache *cache, const void *Q, int64_t q_row, int64_t q_head, int q_heads, float scale,
                                  int64_t window, int64_t sinks, void *Out, void *workspace, size_t workspace_bytes,

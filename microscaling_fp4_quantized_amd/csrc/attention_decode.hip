@@ -4,14 +4,17 @@
 //
 // Bound by reading keys and values once. A workgroup takes a piece of a sequence for one key-value head and up to 16 of the query
 // heads that share it; its four waves take tiles of 32 tokens in turn, each with a running maximum, sum and output of its own, and
-// meet once at the end. Pieces of a longer sequence meet in a second launch (join).
+// meet once at the end. The tiles of all sequences, one after the other, are dealt out evenly: a workgroup has the same number of
+// them whatever the lengths, and goes on with the next sequence where one ends. Pieces of a sequence meet in a second launch (join).
 //
 // Both products run on the matrix cores with the tokens as rows and the heads as columns, so nothing has to change lanes:
 //   S^T = K Q^T: a lane's K rows are 16-byte loads from the cache. Row r of half a of a tile is token 8 (r / 4) + 4 a + r % 4: the two
 //   results then hold, in lane group q, the scores of tokens 8 q .. 8 q + 7 of one head.
 //   O^T = V^T P^T: just those are the lane's part of P^T. Of V a lane loads the same dims of its 8 tokens, and a byte permute of each
 //   pair of tokens turns them into rows of V^T, row r being dim 8 r + n of product n: no trip through LDS.
-// The loads of the next tile and the page numbers of the one after it are in flight while a tile is worked on.
+// The waves of a SIMD hide each other's loads; one tile ahead in registers was slower (one token 10.8 against 9.7 us, 131000 tokens 105
+// against 102), as half the waves. Values stream past the caches (131000 tokens 101 -> 92 us); keys do not, because two loads
+// share a line of theirs (8-bit codes 66 -> 70 us).
 //
 // 8-bit caches: codes are exact in bf16, so the matrix cores see codes and the scales are applied in float32, a key's to its score
 // and a value's to its p. p is rounded to bf16 for the second product (2^-9 of each p, which averages out); its sum is not.
@@ -30,11 +33,10 @@ constexpr float kSlack = 8.f;  // the running maximum may lag behind by this man
 struct Span {
   int n, lo, sinks, ga, gb, granules;
   __device__ int first_of(int g) const { return (g < ga ? g : g - ga + gb) * kGranule; }
-  __device__ int tiles() const { return (granules + 1) / 2; }
+  __device__ int tiles() const { return max(1, (granules + 1) / 2); }  // one of nothing for a sequence without tokens
 };
-__device__ __forceinline__ Span span_of(const Paged& c, int b, int window, int sinks) {
+__device__ __forceinline__ Span span_of(const Paged& c, int len, int window, int sinks) {
   Span s;
-  const int len = length_of(c, b);
   s.n = min(len, paged_room(c));
   s.lo = window ? max(len - window, 0) : 0;
   s.sinks = sinks;
@@ -45,44 +47,27 @@ __device__ __forceinline__ Span span_of(const Paged& c, int b, int window, int s
   s.granules = s.ga + max(end - s.gb, 0);
   return s;
 }
-
-// Pieces: `room` of them for all sequences together and one more for each sequence at most.
-struct Piece {
-  int b, index, count, slot, tiles;  // tiles of a piece
-};
-__device__ __forceinline__ Piece piece_of(const Paged& c, int window, int sinks, int room, int slot) {
-  const int lane = threadIdx.x & 63;
-  float total = 0.f;
-  for (int b = 0; b < c.batch; b += 64) {
-    float v = b + lane < c.batch ? (float)span_of(c, b + lane, window, sinks).tiles() : 0.f;
-#pragma unroll
-    for (int h = 1; h < 64; h <<= 1) v += __shfl_xor(v, h);
-    total += v;
-  }
-  // at least total / room, whatever the float sum lost: so no more than room + batch pieces
-  const int per = max(kMinTiles, (int)fminf(total / (float)room * 1.0001f + 1.f, 1e9f));
-  Piece p{-1, 0, 0, 0, per};
-  int base = 0;
-  for (int b = 0; b < c.batch; b += 64) {
-    const int mine = b + lane < c.batch ? max(1, (span_of(c, b + lane, window, sinks).tiles() + per - 1) / per) : 0;
-    const int upto = wave_prefix(mine);
-    const uint64_t after = __ballot(base + upto > slot);
-    if (after) {
-      const int at = __builtin_ctzll(after);
-      p.b = b + at;
-      p.count = __shfl(mine, at);
-      p.slot = base + __shfl(upto, at) - p.count;
-      p.index = slot - p.slot;
-      break;
-    }
-    base += __shfl(upto, 63);
-  }
-  p.b = __builtin_amdgcn_readfirstlane(p.b);
-  p.count = __builtin_amdgcn_readfirstlane(p.count);
-  p.slot = __builtin_amdgcn_readfirstlane(p.slot);
-  p.index = __builtin_amdgcn_readfirstlane(p.index);
-  return p;
+__device__ __forceinline__ int tiles_of(const Paged& c, int b, int window, int sinks) {
+  return b < c.batch ? span_of(c, length_of(c, b), window, sinks).tiles() : 0;
 }
+
+// The tiles of all sequences dealt out to `count` of at most `most` workgroups: the first `longer` have one more than `each`.
+struct Deal {
+  int total, count, each, longer;
+  __device__ Deal(const Paged& c, int window, int sinks, int most) {
+    total = 0;
+    for (int b = 0; b < c.batch; b += 64) total += wave_total(tiles_of(c, b + (threadIdx.x & 63), window, sinks));
+    total = __builtin_amdgcn_readfirstlane(total);
+    count = min(most, (total + kMinTiles - 1) / kMinTiles);
+    each = total / count;
+    longer = total - each * count;
+  }
+  __device__ int first_of(int w) const { return w * each + min(w, longer); }
+  __device__ int who(int tile) const {
+    const int with = longer * (each + 1);
+    return tile < with ? tile / (each + 1) : longer + (tile - with) / each;
+  }
+};
 
 // A tile's raw bytes and its visible tokens.
 template <int D, bool E4M3>
@@ -130,7 +115,7 @@ __device__ __forceinline__ void load(Raw<D, E4M3>& x, const Paged& c, int head, 
   for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int p = 0; p < R::VP; ++p)
-      x.v[i][p] = *reinterpret_cast<const typename R::VWord*>(v + i * c.token_stride + p * (64 * R::VW));
+      x.v[i][p] = __builtin_nontemporal_load(reinterpret_cast<const typename R::VWord*>(v + i * c.token_stride + p * (64 * R::VW)));
   if constexpr (E4M3) {
     const float* sc = (q & 1) ? c.v_scales : c.k_scales;
     x.scale = sc[pv * c.spage_stride + head * c.shead_stride + (in + r) * c.stoken_stride];
@@ -257,157 +242,164 @@ __device__ __forceinline__ void work(State<D, E4M3>& st, Raw<D, E4M3>& x, float 
 }
 
 template <int D, bool E4M3>
-__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode(Fp4AttentionArgs a, int group, int blocks, int room, int slots) {
+__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode(Fp4AttentionArgs a, int group, int blocks, int most, int slots) {
   typedef Raw<D, E4M3> R;
   constexpr int PITCH = D + 1;
   __shared__ alignas(16) float outs[kWaves][16][PITCH];
   __shared__ float tops[kWaves][16], sums[kWaves][16];
   const Paged& c = a.cache;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int slot = blockIdx.x / (c.heads * blocks), rest = blockIdx.x - slot * (c.heads * blocks);
+  // workgroup i runs on XCD i % 8: the heads of the same tokens go to one XCD, where heads that share keys share its L2 (64 query
+  // heads over one key-value head 31 -> 24 us)
+  const int all = c.heads * blocks, turn = blockIdx.x >> 3, w = turn / all * 8 + (blockIdx.x & 7), rest = turn % all;
   const int head = rest / blocks, g0 = 16 * (rest - head * blocks), heads = min(16, group - g0);
-  const Piece piece = piece_of(c, a.window, a.sinks, room, slot);
-  if (piece.b < 0) return;
-  const int b = piece.b;
-  const Span span = span_of(c, b, a.window, a.sinks);
-  const int* row = c.table + b * c.table_stride;
-  const int end = min((piece.index + 1) * piece.tiles, span.tiles());
-  int tile = piece.index * piece.tiles + wave;
-
-  State<D, E4M3> st;
-  const int r = lane & 15, q = lane >> 4;
-  Raw<D, E4M3> x0, x1;
-  Ids id = ids_of(c, row, span, tile, lane);
-  {
-    const uint16_t* qp = a.q + b * a.q_token + (head * group + g0 + min(r, heads - 1)) * a.q_head;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      // the dims of K's operand i: 32 i + 8 q, or of codes 64 (i / 2) + 16 q + 8 (i % 2)
-      const int d = E4M3 ? 64 * (i / 2) + 16 * q + 8 * (i & 1) : 32 * i + 8 * q;
-      st.q[i] = __builtin_bit_cast(v8bf, *reinterpret_cast<const v4u*>(qp + d));
+  const Deal deal(c, a.window, a.sinks, most);
+  if (w >= deal.count) return;
+  int at = deal.first_of(w);             // the next tile, of all sequences'
+  const int stop = deal.first_of(w + 1);
+  int b = 0, begin = 0, tiles = 0, len = 0;  // its sequence, that one's first tile, number of tiles and tokens
+  for (; b < c.batch; b += 64) {
+    const int own = b + lane < c.batch ? length_of(c, b + lane) : 0;
+    const int mine = b + lane < c.batch ? span_of(c, own, a.window, a.sinks).tiles() : 0, upto = wave_prefix(mine);
+    const uint64_t after = __ballot(begin + upto > at);
+    if (after) {
+      const int i = __builtin_ctzll(after);
+      b += i;
+      tiles = __shfl(mine, i);
+      len = __shfl(own, i);
+      begin += __shfl(upto, i) - tiles;
+      break;
     }
+    begin += __shfl(upto, 63);
   }
-#pragma unroll
-  for (int n = 0; n < D / 16; ++n) st.o[n] = v4f{0.f, 0.f, 0.f, 0.f};
-  st.m = kNever;
-  st.l = 0.f;
+  b = __builtin_amdgcn_readfirstlane(b);
+  begin = __builtin_amdgcn_readfirstlane(begin);
+  tiles = __builtin_amdgcn_readfirstlane(tiles);
+  len = __builtin_amdgcn_readfirstlane(len);
+  const int r = lane & 15, q = lane >> 4;
   const float factor = a.scale * kLog2e;
   float* scales = &outs[wave][0][0];  // free until the waves meet
-  if (tile < end) {
-    load<D, E4M3>(x0, c, head, span, id, lane);
-    id = ids_of(c, row, span, tile + kWaves, lane);
+
+  while (true) {
+    const Span span = span_of(c, len, a.window, a.sinks);
+    const int* row = c.table + b * c.table_stride;
+    const int end = min(stop - begin, tiles);
+    int tile = at - begin + wave;
+    State<D, E4M3> st;
+    Raw<D, E4M3> x;
+    Ids id = ids_of(c, row, span, tile, lane);
+    {
+      const uint16_t* qp = a.q + b * a.q_token + (head * group + g0 + min(r, heads - 1)) * a.q_head;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) arrived(st.q[i]);
-    while (true) {
-      if (tile + kWaves < end) load<D, E4M3>(x1, c, head, span, id, lane);
-      id = ids_of(c, row, span, tile + 2 * kWaves, lane);
-      work<D, E4M3>(st, x0, factor, scales, lane);
-      tile += kWaves;
-      if (tile >= end) break;
-      if (tile + kWaves < end) load<D, E4M3>(x0, c, head, span, id, lane);
-      id = ids_of(c, row, span, tile + 2 * kWaves, lane);
-      work<D, E4M3>(st, x1, factor, scales, lane);
-      tile += kWaves;
-      if (tile >= end) break;
-    }
-  }
-  st.l = sum_across<32>(sum_across<16>(st.l));
-  if (q == 0) {
-    tops[wave][r] = st.m;
-    sums[wave][r] = st.l;
-  }
-  __syncthreads();
-  const float top = fmaxf(fmaxf(tops[0][r], tops[1][r]), fmaxf(tops[2][r], tops[3][r]));
-  const float keep = share_of(v2f{st.m, st.l}, top);
-  if (r < heads) {
-#pragma unroll
-    for (int n = 0; n < D / 16; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) outs[wave][r][(n / R::VDIM) * (16 * R::VDIM) + (4 * q + i) * R::VDIM + n % R::VDIM] = st.o[n][i] * keep;
-  }
-  if (q == 0) sums[wave][r] = st.l * keep;
-  __syncthreads();
-  for (int e = threadIdx.x * 4; e < heads * D; e += 64 * kWaves * 4) {
-    const int h = e / D, d = e % D;
-    float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      l += sums[w][h];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] += outs[w][h][d + i];
-    }
-    const int hq = head * group + g0 + h;
-    if (piece.count == 1) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      *reinterpret_cast<v2u*>(a.out + ((int64_t)b * a.q_heads + hq) * D + d) =
-          v2u{bf16_pair(o[0] * inv, o[1] * inv), bf16_pair(o[2] * inv, o[3] * inv)};
-    } else {
-      const Parts parts = parts_of(a.workspace, (size_t)slots * a.q_heads, D);
-      *reinterpret_cast<v4f*>(parts.o + ((size_t)slot * a.q_heads + hq) * D + d) = v4f{o[0], o[1], o[2], o[3]};
-      if (d == 0) {
-        float m = tops[0][h];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) m = fmaxf(m, tops[w][h]);
-        parts.ml[(size_t)slot * a.q_heads + hq] = v2f{m, l};
+      for (int i = 0; i < D / 32; ++i) {
+        // the dims of K's operand i: 32 i + 8 q, or of codes 64 (i / 2) + 16 q + 8 (i % 2)
+        const int d = E4M3 ? 64 * (i / 2) + 16 * q + 8 * (i & 1) : 32 * i + 8 * q;
+        st.q[i] = __builtin_bit_cast(v8bf, *reinterpret_cast<const v4u*>(qp + d));
       }
     }
+#pragma unroll
+    for (int n = 0; n < D / 16; ++n) st.o[n] = v4f{0.f, 0.f, 0.f, 0.f};
+    st.m = kNever;
+    st.l = 0.f;
+    if (tile < end) {
+      while (true) {
+        load<D, E4M3>(x, c, head, span, id, lane);
+        id = ids_of(c, row, span, tile + kWaves, lane);
+        work<D, E4M3>(st, x, factor, scales, lane);
+        tile += kWaves;
+        if (tile >= end) break;
+      }
+    }
+    st.l = sum_across<32>(sum_across<16>(st.l));
+    if (q == 0) tops[wave][r] = st.m;
+    __syncthreads();
+    const float top = fmaxf(fmaxf(tops[0][r], tops[1][r]), fmaxf(tops[2][r], tops[3][r]));
+    const float keep = share_of(v2f{st.m, st.l}, top);
+    if (r < heads) {
+#pragma unroll
+      for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) outs[wave][r][(n / R::VDIM) * (16 * R::VDIM) + (4 * q + i) * R::VDIM + n % R::VDIM] = st.o[n][i] * keep;
+    }
+    if (q == 0) sums[wave][r] = st.l * keep;
+    __syncthreads();
+    const bool whole = at == begin && end == tiles;
+    for (int e = threadIdx.x * 4; e < heads * D; e += 64 * kWaves * 4) {
+      const int h = e / D, d = e % D;
+      float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < kWaves; ++k) {
+        l += sums[k][h];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] += outs[k][h][d + i];
+      }
+      const int hq = head * group + g0 + h;
+      if (whole) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        *reinterpret_cast<v2u*>(a.out + ((int64_t)b * a.q_heads + hq) * D + d) =
+            v2u{bf16_pair(o[0] * inv, o[1] * inv), bf16_pair(o[2] * inv, o[3] * inv)};
+      } else {
+        // piece (w, b) has place w + b: along the tiles either w or b grows from one piece to the next, or both
+        const Parts parts = parts_of(a.workspace, (size_t)slots * a.q_heads, D);
+        *reinterpret_cast<v4f*>(parts.o + ((size_t)(w + b) * a.q_heads + hq) * D + d) = v4f{o[0], o[1], o[2], o[3]};
+        if (d == 0) {
+          float m = tops[0][h];
+#pragma unroll
+          for (int k = 1; k < kWaves; ++k) m = fmaxf(m, tops[k][h]);
+          parts.ml[(size_t)(w + b) * a.q_heads + hq] = v2f{m, l};
+        }
+      }
+    }
+    at = begin + end;
+    if (at >= stop) return;
+    begin = at;
+    ++b;
+    len = min(max(uniform_load(c.lengths + b), 0), 1 << 30);
+    tiles = span_of(c, len, a.window, a.sinks).tiles();
+    __syncthreads();  // outs and tops are read
   }
 }
 
-// o = sum_c 2^(m_c - m) o_c / sum_c 2^(m_c - m) l_c over the pieces of a sequence: a workgroup for a sequence and a query head.
+// o = sum_c 2^(m_c - m) o_c / sum_c 2^(m_c - m) l_c over the pieces of a sequence. D / 4 lanes hold an output; a workgroup has
+// `wide` query heads of a sequence, its other lanes go over the pieces in turn with them.
 template <int D>
-__global__ __launch_bounds__(256) void join(Fp4AttentionArgs a, int room, int slots) {
+__global__ __launch_bounds__(256) void join(Fp4AttentionArgs a, int wide, int most, int slots) {
   constexpr int LANES = D / 4, GROUPS = 256 / LANES;
   __shared__ v4f red[GROUPS][LANES];
-  __shared__ float red_l[GROUPS];
-  const int b = blockIdx.y, hq = blockIdx.x;
-  // the first piece of sequence b: sum of the pieces of those before it
+  __shared__ v2f red_ml[GROUPS];
+  constexpr int kAtOnce = 4;  // pieces whose loads are in flight together
   const Paged& c = a.cache;
-  const int lane = threadIdx.x & 63;
-  float total = 0.f;
-  for (int i = 0; i < c.batch; i += 64) {
-    float v = i + lane < c.batch ? (float)span_of(c, i + lane, a.window, a.sinks).tiles() : 0.f;
-#pragma unroll
-    for (int h = 1; h < 64; h <<= 1) v += __shfl_xor(v, h);
-    total += v;
-  }
-  const int per = max(kMinTiles, (int)fminf(total / (float)room * 1.0001f + 1.f, 1e9f));
-  int before = 0;
-  for (int i = 0; i < b; i += 64)
-    before += wave_total(i + lane < b ? max(1, (span_of(c, i + lane, a.window, a.sinks).tiles() + per - 1) / per) : 0);
-  const int count = max(1, (span_of(c, b, a.window, a.sinks).tiles() + per - 1) / per);
-  if (count == 1) return;  // written by its only piece
+  const int lane = threadIdx.x & 63, b = blockIdx.y;
+  const Deal deal(c, a.window, a.sinks, most);
+  int begin = 0;
+  for (int i = 0; i < b; i += 64) begin += wave_total(i + lane < b ? tiles_of(c, i + lane, a.window, a.sinks) : 0);
+  const int first = deal.who(begin), last = deal.who(begin + tiles_of(c, b, a.window, a.sinks) - 1);
+  if (first == last) return;  // written by its only workgroup
+  const int g = threadIdx.x / LANES, e = 4 * (threadIdx.x % LANES), turns = GROUPS / wide;
+  const int hq = blockIdx.x * wide + g % wide, h = min(hq, a.q_heads - 1);
   const Parts parts = parts_of(a.workspace, (size_t)slots * a.q_heads, D);
-  const v2f* ml = parts.ml + (size_t)before * a.q_heads + hq;
-  float m = kNever;
-  for (int i = 0; i < count; i += 64)
-    if (i + lane < count) m = fmaxf(m, ml[(size_t)(i + lane) * a.q_heads][0]);
-#pragma unroll
-  for (int h = 1; h < 64; h <<= 1) m = fmaxf(m, __shfl_xor(m, h));
-  const float mm = m == kNever ? 0.f : m;
-  const int g = threadIdx.x / LANES, e = threadIdx.x % LANES;
+  v2f ml{kNever, 0.f};
   v4f o{0.f, 0.f, 0.f, 0.f};
-  float l = 0.f;
-  for (int i = g; i < count; i += GROUPS) {
-    const v2f x = ml[(size_t)i * a.q_heads];
-    const float keep = share_of(x, mm);
-    const v4f y = *reinterpret_cast<const v4f*>(parts.o + ((size_t)(before + i) * a.q_heads + hq) * D + 4 * e);
-    l = __builtin_fmaf(x[1], keep, l);
+  for (int w = first + g / wide; w <= last; w += kAtOnce * turns) {
+    v2f x[kAtOnce];
+    v4f y[kAtOnce];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) o[k] = __builtin_fmaf(y[k], keep, o[k]);
-  }
-  red[g][e] = o;
-  if (e == 0) red_l[g] = l;
-  __syncthreads();
-  if (g == 0) {
-#pragma unroll
-    for (int i = 1; i < GROUPS; ++i) {
-      l += red_l[i];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[k] += red[i][e][k];
+    for (int i = 0; i < kAtOnce; ++i) {
+      const size_t at = (size_t)(min(w + i * turns, last) + b) * a.q_heads + h;
+      x[i] = parts.ml[at];
+      y[i] = *reinterpret_cast<const v4f*>(parts.o + at * D + e);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    *reinterpret_cast<v2u*>(a.out + ((int64_t)b * a.q_heads + hq) * D + 4 * e) =
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      if (w + i * turns <= last) join_parts(ml, o, x[i], y[i]);
+  }
+  red[g][threadIdx.x % LANES] = o;
+  if (e == 0) red_ml[g] = ml;
+  __syncthreads();
+  if (g < wide && hq < a.q_heads) {
+    for (int i = g + wide; i < GROUPS; i += wide) join_parts(ml, o, red_ml[i], red[i][threadIdx.x % LANES]);
+    const float inv = ml[1] == 0.f ? 0.f : 1.f / ml[1];
+    *reinterpret_cast<v2u*>(a.out + ((int64_t)b * a.q_heads + hq) * D + e) =
         v2u{bf16_pair(o[0] * inv, o[1] * inv), bf16_pair(o[2] * inv, o[3] * inv)};
   }
 }
@@ -416,17 +408,20 @@ template <int D, bool E4M3>
 hipError_t launch(const Fp4AttentionArgs& a, hipStream_t st) {
   const Paged& c = a.cache;
   const int group = a.q_heads / c.heads, blocks = (group + 15) / 16;
-  const int room = FP4_ATTENTION_PIECES(a.q_heads, c.heads);
   // what the longest sequence that the table has room for can be cut into
   int64_t tokens = (int64_t)c.cols << c.shift;
   if (a.window && (int64_t)a.window + a.sinks + 2 * kTile < tokens) tokens = (int64_t)a.window + a.sinks + 2 * kTile;
-  const int64_t most = ((tokens + kTile - 1) / kTile + 1 + kMinTiles - 1) / kMinTiles;
-  const int slots = (int)(c.batch * most < room + c.batch ? c.batch * most : room + c.batch);
-  hipLaunchKernelGGL((decode<D, E4M3>), dim3((unsigned)(slots * c.heads * blocks)), dim3(64 * kWaves), 0, st, a, group, blocks, room,
+  const int64_t longest = (tokens + kTile - 1) / kTile + 1;
+  const int64_t needed = (longest * c.batch + kMinTiles - 1) / kMinTiles;
+  const int pieces = FP4_ATTENTION_PIECES(c.batch, a.q_heads, c.heads);
+  const int most = (int)(needed < pieces ? needed : pieces), slots = most + c.batch;
+  hipLaunchKernelGGL((decode<D, E4M3>), dim3((unsigned)((most + 7) / 8 * 8 * c.heads * blocks)), dim3(64 * kWaves), 0, st, a, group, blocks, most,
                      slots);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || most <= 1) return e;
-  hipLaunchKernelGGL((join<D>), dim3((unsigned)a.q_heads, (unsigned)c.batch), dim3(256), 0, st, a, room, slots);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || most == 1) return e;
+  constexpr int groups = 1024 / D;
+  const int wide = (int64_t)c.batch * a.q_heads >= 1024 ? groups : 1;  // few rows: all lanes to the pieces of one
+  hipLaunchKernelGGL((join<D>), dim3((unsigned)((a.q_heads + wide - 1) / wide), (unsigned)c.batch), dim3(256), 0, st, a, wide, most, slots);
   return hipGetLastError();
 }
 

@@ -75,6 +75,14 @@ __device__ __forceinline__ Parts parts_of(void* workspace, size_t n, int dim) {
 // What a partial result counts under the common maximum m. Without a maximum its sum is 0, or NaN where a score was.
 __device__ __forceinline__ float share_of(v2f ml, float m) { return ml[0] == kNever ? (ml[1] == 0.f ? 0.f : 1.f) : exp2_hw(ml[0] - m); }
 
+// Another partial result (x, y) into (ml, o).
+__device__ __forceinline__ void join_parts(v2f& ml, v4f& o, v2f x, v4f y) {
+  const float m = fmaxf(ml[0], x[0]), keep = share_of(ml, m), more = share_of(x, m);
+  ml = v2f{m, ml[1] * keep + x[1] * more};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) o[k] = o[k] * keep + y[k] * more;
+}
+
 // The low or the high halves of two words, a's in the low half.
 __device__ __forceinline__ unsigned low_halves(unsigned a, unsigned b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
 __device__ __forceinline__ unsigned high_halves(unsigned a, unsigned b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }

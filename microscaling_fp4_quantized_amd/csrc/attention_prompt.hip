@@ -466,7 +466,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 4 : 2) void pr
 // a head, 1024 / D heads of a token in a workgroup.
 template <int D>
 __global__ __launch_bounds__(256) void join(Fp4AttentionArgs a, int group, int tile_rows, int splits) {
-  constexpr int LANES = D / 4;
+  constexpr int LANES = D / 4, kAtOnce = 4;  // parts whose loads are in flight together
   const Paged& c = a.cache;
   const int t = blockIdx.x, h = blockIdx.y * (256 / LANES) + threadIdx.x / LANES, e = 4 * (threadIdx.x % LANES);
   const int b = __builtin_amdgcn_readfirstlane(sequence_of(a.starts, c.batch, t));
@@ -479,19 +479,22 @@ __global__ __launch_bounds__(256) void join(Fp4AttentionArgs a, int group, int t
   if (parts == 1) return;  // written by its only part
   const size_t n = (size_t)a.T * a.q_heads, at = (size_t)t * a.q_heads + h;
   const Parts from = parts_of(a.workspace, splits * n, D);
-  float m = kNever;
-  for (int p = 0; p < parts; ++p) m = fmaxf(m, from.ml[p * n + at][0]);
+  v2f ml{kNever, 0.f};
   v4f o{0.f, 0.f, 0.f, 0.f};
-  float l = 0.f;
-  for (int p = 0; p < parts; ++p) {
-    const v2f ml = from.ml[p * n + at];
-    const v4f y = *reinterpret_cast<const v4f*>(from.o + (p * n + at) * D + e);
-    const float keep = share_of(ml, m);
-    l = __builtin_fmaf(ml[1], keep, l);
+  for (int p = 0; p < parts; p += kAtOnce) {
+    v2f x[kAtOnce];
+    v4f y[kAtOnce];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) o[k] = __builtin_fmaf(y[k], keep, o[k]);
+    for (int i = 0; i < kAtOnce; ++i) {
+      const size_t place = min(p + i, parts - 1) * n + at;
+      x[i] = from.ml[place];
+      y[i] = *reinterpret_cast<const v4f*>(from.o + place * D + e);
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      if (p + i < parts) join_parts(ml, o, x[i], y[i]);
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float inv = ml[1] == 0.f ? 0.f : 1.f / ml[1];
   *reinterpret_cast<v2u*>(a.out + at * D + e) = v2u{bf16_pair(o[0] * inv, o[1] * inv), bf16_pair(o[2] * inv, o[3] * inv)};
 }
 

@@ -159,6 +159,8 @@ int check_cache(const char* who, const fp4_kv_cache* c, int64_t q_heads, fp4::Pa
                 (long long)c->cols, (long long)c->table_stride);
   if (c->batch < 1 || c->batch > 65535 || c->batch * q_heads > (1 << 22))
     return fail(FP4_E_SHAPE, "%s: need 1 <= batch <= 65535 and batch * query heads <= 2^22 (batch=%lld)", who, (long long)c->batch);
+  if (c->batch * c->cols > ((int64_t)1 << 35) / c->page_size)
+    return fail(FP4_E_SHAPE, "%s: batch * cols * page_size above 2^35", who);
   const int64_t unit = e4m3 ? 16 : 8;
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || c->page_stride % unit || c->head_stride % unit || c->token_stride % unit)
     return fail(FP4_E_ALIGN, "%s: pages must be 16-byte aligned, their strides multiples of %d", who, (int)unit);

@@ -62,7 +62,7 @@ def test_the_caches_validation(lib, call, late):
     assert c(token_stride=(1 << 25) + 16) == c(head_stride=FAR) == SHAPE and c(token_stride=1 << 25) == ALIGN
     assert c(dtype=1, scale_page_stride=0) == c(dtype=1, scale_token_stride=-1) == c(dtype=1, scale_head_stride=FAR) == SHAPE
     assert c(cols=0) == c(cols=6) == c(cols=(1 << 26) + 1, table_stride=1 << 27) == c(table_stride=FAR) == SHAPE
-    assert c(batch=0) == c(batch=65536) == SHAPE
+    assert c(batch=0) == c(batch=65536) == c(batch=33, cols=1 << 26, table_stride=1 << 26) == SHAPE
     assert c(k=A16 + 8) == c(v=A16 + 4) == c(page_stride=4 * 16 * 128 + 4) == c(token_stride=132) == ALIGN
     assert c(dtype=1, token_stride=136) == c(dtype=1, k_scales=A16 + 2) == c(table=A16 + 1) == c(lengths=A16 + 2) == ALIGN
     if call is not append:
