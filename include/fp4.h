@@ -416,7 +416,7 @@ typedef struct fp4_kv_cache {
 /*
  * New tokens stand in rows: those of sequence b in rows starts[b] .. starts[b + 1] - 1, the last of them being the sequence's
  * last token, so row t is its token lengths[b] - (starts[b + 1] - t). starts is device int [batch + 1], not falling, from 0 to at
- * most T; rows from starts[batch] on belong to nobody: they are not read, and what they would write is left as it was. starts
+ * most T; rows from starts[batch] on belong to nobody: what they would write is left as it was. starts
  * NULL: T == batch, one new token each.
  *
  * fp4_kv_append - keys and values of T rows into the cache, keys and queries rotated on the way:

@@ -26,7 +26,49 @@ __device__ __forceinline__ unsigned head_max(unsigned m) {
   return m;
 }
 
-template <int D, bool E4M3>
+// Calls that read more than this stream rows and rotated queries past the caches; of smaller ones the next kernel finds them there.
+// Both ways, us: 26601 tokens of 48 heads of 128 (327 MB) 119.5 / 103.4, 3216 of 20 heads (16 MB) 9.3 / 9.7. The cache's entries are
+// stored the usual way: a token's 8 or 16 bytes of a lane do not fill a line (streamed: 111.7).
+constexpr int64_t kStreamBytes = (int64_t)96 << 20;
+
+template <bool STREAM>
+__device__ __forceinline__ void put(void* to, v4u v) {
+  if constexpr (STREAM) __builtin_nontemporal_store(v, reinterpret_cast<v4u*>(to));
+  else *reinterpret_cast<v4u*>(to) = v;
+}
+template <bool STREAM>
+__device__ __forceinline__ v4u take(const void* from) {
+  return STREAM ? __builtin_nontemporal_load(reinterpret_cast<const v4u*>(from)) : *reinterpret_cast<const v4u*>(from);
+}
+
+// 16 elements of a token's head, as two halves of 8: those of a rotated piece that are not interleaved lie half a rotation apart.
+struct Piece {
+  int head, piece, e0, e1;  // the halves' first elements
+  bool query, key, turn;
+  v4u w0, w1;
+};
+template <int D, bool STREAM>
+__device__ __forceinline__ Piece piece_of(const Fp4AppendArgs& a, int t, int u) {
+  constexpr int PIECES = D / 16;
+  Piece p;
+  const int h = u / PIECES;
+  p.piece = u % PIECES;
+  p.query = h < a.q_heads;
+  p.key = !p.query && h < a.q_heads + a.cache.heads;
+  p.head = p.query ? h : p.key ? h - a.q_heads : h - a.q_heads - a.cache.heads;
+  p.turn = (p.query || p.key) && p.piece < a.half / 8;
+  const bool apart = p.turn && !a.interleaved;
+  p.e0 = apart ? 8 * p.piece : 16 * p.piece;
+  p.e1 = apart ? a.half + 8 * p.piece : 16 * p.piece + 8;
+  const uint16_t* x = p.query ? a.q + t * a.q_token + p.head * a.q_head
+                      : p.key ? a.k + t * a.k_token + p.head * a.k_head
+                              : a.v + t * a.v_token + p.head * a.v_head;
+  p.w0 = take<STREAM>(x + p.e0);
+  p.w1 = take<STREAM>(x + p.e1);
+  return p;
+}
+
+template <int D, bool E4M3, bool STREAM>
 __global__ __launch_bounds__(64 * kWaves) void kv_append(Fp4AppendArgs a, int parts) {
   constexpr int PIECES = D / 16;  // lanes of a head
   __shared__ float trig[kWaves][2][D / 2];
@@ -35,6 +77,7 @@ __global__ __launch_bounds__(64 * kWaves) void kv_append(Fp4AppendArgs a, int pa
   const int64_t id = (int64_t)blockIdx.x * kWaves + wave;
   const int t = (int)(id / parts), part = (int)(id - (int64_t)t * parts);
   if (t >= a.T) return;
+  const int units = (a.q_heads + 2 * c.heads) * PIECES;
   const int b = __builtin_amdgcn_readfirstlane(sequence_of(a.starts, c.batch, t));
   if (b < 0) return;
   const int i = c.lengths[b] - (a.starts ? a.starts[b + 1] - t : 1);
@@ -59,74 +102,52 @@ __global__ __launch_bounds__(64 * kWaves) void kv_append(Fp4AppendArgs a, int pa
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
 
-  const int rotated = a.half / 8;  // pieces of a head that are
-  const int units = (a.q_heads + 2 * c.heads) * PIECES;
-  const int64_t place = held ? (int64_t)page * c.page_stride + (int64_t)(i & ((1 << c.shift) - 1)) * c.token_stride : 0;
-  const int64_t splace = held && E4M3 ? (int64_t)page * c.spage_stride + (int64_t)(i & ((1 << c.shift) - 1)) * c.stoken_stride : 0;
+  const int64_t in = i & ((1 << c.shift) - 1);
+  const int64_t place = held ? page * c.page_stride + in * c.token_stride : 0;
+  const int64_t splace = held && E4M3 ? page * c.spage_stride + in * c.stoken_stride : 0;
   for (int u = part * 64 + lane; u < units; u += parts * 64) {
-    const int h = u / PIECES, piece = u % PIECES;
-    const bool query = h < a.q_heads, key = !query && h < a.q_heads + c.heads;
-    if (!query && !held) continue;
-    const int hk = key ? h - a.q_heads : h - a.q_heads - c.heads;
-    const uint16_t* x = query ? a.q + t * a.q_token + h * a.q_head
-                        : key ? a.k + t * a.k_token + hk * a.k_head
-                              : a.v + t * a.v_token + hk * a.v_head;
-    // where the piece's two halves of 8 stand in the head
-    const bool turn = (query || key) && piece < rotated;
-    int e0 = 16 * piece, e1 = 16 * piece + 8;
-    if (turn && !a.interleaved) {
-      e0 = 8 * piece;
-      e1 = a.half + 8 * piece;
-    }
-    const v4u w0 = *reinterpret_cast<const v4u*>(x + e0), w1 = *reinterpret_cast<const v4u*>(x + e1);
+    const Piece p = piece_of<D, STREAM>(a, t, u);
+    if (!p.query && !held) continue;  // for all lanes of a head
     float f[16];
-    widen8(w0, f);
-    widen8(w1, f + 8);
-    if (turn) {
-      float cs[8], sn[8];
+    widen8(p.w0, f);
+    widen8(p.w1, f + 8);
+    if (p.turn) {
+      const float *cs = cosines + 8 * p.piece, *sn = sines + 8 * p.piece;
+      if (a.interleaved) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        cs[j] = cosines[8 * piece + j];
-        sn[j] = sines[8 * piece + j];
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float x0, x1;
-        if (a.interleaved) {
-          x0 = f[2 * j];
-          x1 = f[2 * j + 1];
-        } else {
-          x0 = f[j];
-          x1 = f[j + 8];
+        for (int j = 0; j < 8; ++j) {
+          const float x0 = f[2 * j], x1 = f[2 * j + 1];
+          f[2 * j] = x0 * cs[j] - x1 * sn[j];
+          f[2 * j + 1] = x0 * sn[j] + x1 * cs[j];
         }
-        const float y0 = x0 * cs[j] - x1 * sn[j], y1 = x0 * sn[j] + x1 * cs[j];
-        if (a.interleaved) {
-          f[2 * j] = y0;
-          f[2 * j + 1] = y1;
-        } else {
-          f[j] = y0;
-          f[j + 8] = y1;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float x0 = f[j], x1 = f[j + 8];
+          f[j] = x0 * cs[j] - x1 * sn[j];
+          f[j + 8] = x0 * sn[j] + x1 * cs[j];
         }
       }
     }
-    if (query) {
-      uint16_t* y = a.q_out + t * a.out_token + h * a.out_head;
-      *reinterpret_cast<v4u*>(y + e0) = narrow8(f);
-      *reinterpret_cast<v4u*>(y + e1) = narrow8(f + 8);
-    } else if (E4M3) {
+    if (p.query) {
+      uint16_t* y = a.q_out + t * a.out_token + p.head * a.out_head;
+      put<STREAM>(y + p.e0, narrow8(f));
+      put<STREAM>(y + p.e1, narrow8(f + 8));
+      continue;
+    }
+    uint8_t* y = const_cast<uint8_t*>(p.key ? c.k : c.v) + place + p.head * c.head_stride;
+    if (E4M3) {
       unsigned m = 0;
 #pragma unroll
       for (int j = 0; j < 16; ++j) m = max(m, abs_bits(f[j]));
       m = head_max<PIECES>(m);
       const float inv = f8_inverse(m);
-      uint8_t* y = const_cast<uint8_t*>(key ? c.k : c.v) + place + hk * c.head_stride;
-      *reinterpret_cast<v2u*>(y + e0) = f8_codes8(f, inv);
-      *reinterpret_cast<v2u*>(y + e1) = f8_codes8(f + 8, inv);
-      if (piece == 0) const_cast<float*>(key ? c.k_scales : c.v_scales)[splace + hk * c.shead_stride] = f8_scale(m);
+      *reinterpret_cast<v2u*>(y + p.e0) = f8_codes8(f, inv);
+      *reinterpret_cast<v2u*>(y + p.e1) = f8_codes8(f + 8, inv);
+      if (p.piece == 0) const_cast<float*>(p.key ? c.k_scales : c.v_scales)[splace + p.head * c.shead_stride] = f8_scale(m);
     } else {
-      uint8_t* y = const_cast<uint8_t*>(key ? c.k : c.v) + place + hk * c.head_stride;
-      *reinterpret_cast<v4u*>(y + 2 * e0) = turn ? narrow8(f) : w0;
-      *reinterpret_cast<v4u*>(y + 2 * e1) = turn ? narrow8(f + 8) : w1;
+      *reinterpret_cast<v4u*>(y + 2 * p.e0) = p.turn ? narrow8(f) : p.w0;
+      *reinterpret_cast<v4u*>(y + 2 * p.e1) = p.turn ? narrow8(f + 8) : p.w1;
     }
   }
 }
@@ -137,7 +158,8 @@ hipError_t launch(const Fp4AppendArgs& a, hipStream_t st) {
   int64_t parts = (2048 + a.T - 1) / a.T;  // few tokens are spread over 8 waves of each CU
   if (parts > per) parts = per;
   const int64_t waves = a.T * parts;
-  hipLaunchKernelGGL((kv_append<D, E4M3>), dim3((unsigned)((waves + kWaves - 1) / kWaves)), dim3(64 * kWaves), 0, st, a, (int)parts);
+  auto kern = (int64_t)a.T * (a.q_heads + 2 * a.cache.heads) * D * 2 > kStreamBytes ? kv_append<D, E4M3, true> : kv_append<D, E4M3, false>;
+  hipLaunchKernelGGL(kern, dim3((unsigned)((waves + kWaves - 1) / kWaves)), dim3(64 * kWaves), 0, st, a, (int)parts);
   return hipGetLastError();
 }
 
