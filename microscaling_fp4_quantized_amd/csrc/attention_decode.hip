@@ -57,7 +57,6 @@ struct Deal {
   __device__ Deal(const Paged& c, int window, int sinks, int most) {
     total = 0;
     for (int b = 0; b < c.batch; b += 64) total += wave_total(tiles_of(c, b + (threadIdx.x & 63), window, sinks));
-    total = __builtin_amdgcn_readfirstlane(total);
     count = min(most, (total + kMinTiles - 1) / kMinTiles);
     each = total / count;
     longer = total - each * count;
@@ -265,17 +264,13 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode(Fp4Atten
     if (after) {
       const int i = __builtin_ctzll(after);
       b += i;
-      tiles = __shfl(mine, i);
-      len = __shfl(own, i);
-      begin += __shfl(upto, i) - tiles;
+      tiles = __builtin_amdgcn_readlane(mine, i);
+      len = __builtin_amdgcn_readlane(own, i);
+      begin += __builtin_amdgcn_readlane(upto, i) - tiles;
       break;
     }
-    begin += __shfl(upto, 63);
+    begin += __builtin_amdgcn_readlane(upto, 63);
   }
-  b = __builtin_amdgcn_readfirstlane(b);
-  begin = __builtin_amdgcn_readfirstlane(begin);
-  tiles = __builtin_amdgcn_readfirstlane(tiles);
-  len = __builtin_amdgcn_readfirstlane(len);
   const int r = lane & 15, q = lane >> 4;
   const float factor = a.scale * kLog2e;
   float* scales = &outs[wave][0][0];  // free until the waves meet

@@ -235,24 +235,26 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 4 : 2) void pr
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int slot = blockIdx.x / c.heads, head = blockIdx.x - slot * c.heads;
   // which rows: the last tiles first, they see the most
-  int b = -1, tile = tiles - 1 - slot;
+  int b = -1, tile = tiles - 1 - slot, len = 0;
+  Rows rows{0, 0};
   for (int b0 = 0; b0 < c.batch; b0 += 64) {
-    const int mine = b0 + lane < c.batch ? (rows_of(a.starts, b0 + lane, a.T).count * group + kRows - 1) / kRows : 0;
-    const int upto = wave_prefix(mine);
+    const bool is = b0 + lane < c.batch;
+    const Rows own = is ? rows_of(a.starts, b0 + lane, a.T) : Rows{0, 0};
+    const int tokens = is ? length_of(c, b0 + lane) : 0;
+    const int mine = (own.count * group + kRows - 1) / kRows, upto = wave_prefix(mine);
     const uint64_t after = __ballot(upto > tile);
     if (after) {
       const int at = __builtin_ctzll(after);
       b = b0 + at;
-      tile -= __shfl(upto, at) - __shfl(mine, at);
+      tile -= __builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(mine, at);
+      rows = Rows{__builtin_amdgcn_readlane(own.first, at), __builtin_amdgcn_readlane(own.count, at)};
+      len = __builtin_amdgcn_readlane(tokens, at);
       break;
     }
-    tile -= __shfl(upto, 63);
+    tile -= __builtin_amdgcn_readlane(upto, 63);
   }
-  b = __builtin_amdgcn_readfirstlane(b);
-  tile = __builtin_amdgcn_readfirstlane(tile);
   if (b < 0) return;
-  const Rows rows = rows_of(a.starts, b, a.T);
-  const int len = length_of(c, b), base = len - rows.count;  // place of the first new token
+  const int base = len - rows.count;                              // place of the first new token
   const int last = rows.count * group - 1;                        // its last row
   const int row = tile * kRows + wave * 32 + (lane & 31);
   const int mine = min(row, last), token = mine / group, place = base + token;

@@ -27,21 +27,22 @@ __device__ __forceinline__ int paged_room(const Paged& p) { return p.cols << p.s
 // differences from a window (at most 2^30 too) stay within 32 bits.
 __device__ __forceinline__ int length_of(const Paged& p, int b) { return min(max(p.lengths[b], 0), 1 << 30); }
 
-// Sum over the 64 lanes, and over the lanes up to this one.
-__device__ __forceinline__ int wave_total(int v) {
-#pragma unroll
-  for (int h = 1; h < 64; h <<= 1) v += __shfl_xor(v, h);
-  return v;
+// Sum over the lanes up to this one, and over all 64: additions with DPP, in rows of 16 and then across them (through LDS, as shuffles
+// go, these sums were a microsecond of a call).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_part(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
 }
 __device__ __forceinline__ int wave_prefix(int v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int h = 1; h < 64; h <<= 1) {
-    const int o = __shfl_up(v, h);
-    if (lane >= h) v += o;
-  }
+  v += dpp_part<0x111, 0xF>(v);  // row_shr:1, 2, 4, 8
+  v += dpp_part<0x112, 0xF>(v);
+  v += dpp_part<0x114, 0xF>(v);
+  v += dpp_part<0x118, 0xF>(v);
+  v += dpp_part<0x142, 0xA>(v);  // row_bcast:15 into rows 1 and 3
+  v += dpp_part<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
   return v;
 }
+__device__ __forceinline__ int wave_total(int v) { return __builtin_amdgcn_readlane(wave_prefix(v), 63); }
 
 // The sequence of row t of a batch of rows, or -1 where it belongs to none. starts is NULL for one row each.
 __device__ __forceinline__ int sequence_of(const int* starts, int batch, int t) {
