@@ -755,8 +755,8 @@ def _data(t):
 
 def attention_workspace_bytes(T: int, B: int, q_heads: int, heads: int, dim: int) -> int:
     """FP4_ATTENTION_WORKSPACE_BYTES(T, B, q_heads, heads, dim) of include/fp4.h."""
-    blocks = heads * ((q_heads // heads + 15) // 16)
-    step = 1 if blocks >= 512 else 512 // blocks
+    units = heads // (4 if heads % 4 == 0 else 2 if heads % 2 == 0 else 1) * ((q_heads // heads + 15) // 16)
+    step = 1 if units >= 512 else 512 // units
     parts = (B + step - 1) // step * step + B
     tiles = max((T * (q_heads // heads) + 127) // 128, B) * heads
     if tiles <= 256:

@@ -3,8 +3,9 @@
 //   o_h = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q_h k_j - m),  over the visible tokens j
 //
 // Bound by reading keys and values once. A workgroup takes a piece of a sequence for one key-value head and up to 16 of the query
-// heads that share it; its four waves take tiles of 32 tokens in turn, each with a running maximum, sum and output of its own, and
-// meet once at the end. The tiles of all sequences, one after the other, are dealt out evenly: a workgroup has the same number of
+// heads that share it; its waves take tiles of 32 tokens in turn, each with a running maximum, sum and output of its own, and
+// meet once at the end. Where a token's heads lie side by side in short rows, the waves take two or four heads instead: rows of 128
+// bytes, read by workgroups that are not in step, cost memory a quarter of its rate (64 sequences, 8 bits: 64.6 -> 57 us). The tiles of all sequences, one after the other, are dealt out evenly: a workgroup has the same number of
 // them whatever the lengths, and goes on with the next sequence where one ends. Pieces of a sequence meet in a second launch (join).
 //
 // Both products run on the matrix cores with the tokens as rows and the heads as columns, so nothing has to change lanes:
@@ -24,9 +25,7 @@
 namespace fp4 {
 namespace {
 
-constexpr int kWaves = 4;
 constexpr int kTile = 32;
-constexpr int kMinTiles = 4;   // of a piece: one for each wave
 constexpr float kSlack = 8.f;  // the running maximum may lag behind by this many powers of two: p stays below 2^8
 
 // The visible tokens of a sequence, as granules of 16: ga of them from token 0 on, then more from granule gb on.
@@ -51,13 +50,14 @@ __device__ __forceinline__ int tiles_of(const Paged& c, int b, int window, int s
   return b < c.batch ? span_of(c, length_of(c, b), window, sinks).tiles() : 0;
 }
 
-// The tiles of all sequences dealt out to `count` of at most `most` workgroups: the first `longer` have one more than `each`.
+// The tiles of all sequences dealt out to `count` of at most `most` workgroups, about `least` for each if there are few: the first
+// `longer` have one more than `each`.
 struct Deal {
   int total, count, each, longer;
-  __device__ Deal(const Paged& c, int window, int sinks, int most) {
+  __device__ Deal(const Paged& c, int window, int sinks, int most, int least) {
     total = 0;
     for (int b = 0; b < c.batch; b += 64) total += wave_total(tiles_of(c, b + (threadIdx.x & 63), window, sinks));
-    count = min(most, (total + kMinTiles - 1) / kMinTiles);
+    count = min(most, (total + least - 1) / least);
     each = total / count;
     longer = total - each * count;
   }
@@ -240,19 +240,24 @@ __device__ __forceinline__ void work(State<D, E4M3>& st, Raw<D, E4M3>& x, float 
   }
 }
 
-template <int D, bool E4M3>
-__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode(Fp4AttentionArgs a, int group, int blocks, int most, int slots) {
+// BESIDE: key-value heads of a workgroup, side by side in memory; its other waves share a head's tiles. Four heads have two waves each:
+// half the pieces to join (64 sequences of 1721 tokens, 8 bits: 57 -> 51 us).
+constexpr int waves_of(int beside) { return beside == 4 ? 8 : 4; }
+
+template <int D, bool E4M3, int BESIDE>
+__global__ __launch_bounds__(64 * waves_of(BESIDE), 2) void decode(Fp4AttentionArgs a, int group, int together, int most, int slots) {
   typedef Raw<D, E4M3> R;
-  constexpr int PITCH = D + 1;
-  __shared__ alignas(16) float outs[kWaves][16][PITCH];
-  __shared__ float tops[kWaves][16], sums[kWaves][16];
+  constexpr int PITCH = D + 1, WAVES = waves_of(BESIDE);
+  __shared__ alignas(16) float outs[WAVES][16][PITCH];
+  __shared__ float tops[WAVES][16], sums[WAVES][16];
   const Paged& c = a.cache;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // workgroup i runs on XCD i % 8: the heads of the same tokens go to one XCD, where heads that share keys share its L2 (64 query
   // heads over one key-value head 31 -> 24 us)
-  const int all = c.heads * blocks, turn = blockIdx.x >> 3, w = turn / all * 8 + (blockIdx.x & 7), rest = turn % all;
-  const int head = rest / blocks, g0 = 16 * (rest - head * blocks), heads = min(16, group - g0);
-  const Deal deal(c, a.window, a.sinks, most);
+  const int turn = blockIdx.x >> 3, w = turn / together * 8 + (blockIdx.x & 7), first = turn % together * BESIDE;
+  constexpr int WAYS = WAVES / BESIDE;
+  const int way = wave % WAYS, head = first + wave / WAYS, g0 = 16 * blockIdx.y, heads = min(16, group - g0);
+  const Deal deal(c, a.window, a.sinks, most, WAYS);
   if (w >= deal.count) return;
   int at = deal.first_of(w);             // the next tile, of all sequences'
   const int stop = deal.first_of(w + 1);
@@ -279,7 +284,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode(Fp4Atten
     const Span span = span_of(c, len, a.window, a.sinks);
     const int* row = c.table + b * c.table_stride;
     const int end = min(stop - begin, tiles);
-    int tile = at - begin + wave;
+    int tile = at - begin + way;
     State<D, E4M3> st;
     Raw<D, E4M3> x;
     Ids id = ids_of(c, row, span, tile, lane);
@@ -299,16 +304,18 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode(Fp4Atten
     if (tile < end) {
       while (true) {
         load<D, E4M3>(x, c, head, span, id, lane);
-        id = ids_of(c, row, span, tile + kWaves, lane);
+        id = ids_of(c, row, span, tile + WAYS, lane);
         work<D, E4M3>(st, x, factor, scales, lane);
-        tile += kWaves;
+        tile += WAYS;
         if (tile >= end) break;
       }
     }
     st.l = sum_across<32>(sum_across<16>(st.l));
     if (q == 0) tops[wave][r] = st.m;
     __syncthreads();
-    const float top = fmaxf(fmaxf(tops[0][r], tops[1][r]), fmaxf(tops[2][r], tops[3][r]));
+    float top = st.m;
+#pragma unroll
+    for (int k = 1; k < WAYS; ++k) top = fmaxf(top, tops[wave ^ k][r]);
     const float keep = share_of(v2f{st.m, st.l}, top);
     if (r < heads) {
 #pragma unroll
@@ -319,29 +326,32 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode(Fp4Atten
     if (q == 0) sums[wave][r] = st.l * keep;
     __syncthreads();
     const bool whole = at == begin && end == tiles;
-    for (int e = threadIdx.x * 4; e < heads * D; e += 64 * kWaves * 4) {
-      const int h = e / D, d = e % D;
-      float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < kWaves; ++k) {
-        l += sums[k][h];
+    for (int from = 0; from < WAVES; from += WAYS) {  // the first waves of the heads
+      for (int e = threadIdx.x * 4; e < heads * D; e += 64 * WAVES * 4) {
+        const int h = e / D, d = e % D;
+        float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] += outs[k][h][d + i];
-      }
-      const int hq = head * group + g0 + h;
-      if (whole) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        *reinterpret_cast<v2u*>(a.out + ((int64_t)b * a.q_heads + hq) * D + d) =
-            v2u{bf16_pair(o[0] * inv, o[1] * inv), bf16_pair(o[2] * inv, o[3] * inv)};
-      } else {
-        // piece (w, b) has place w + b: along the tiles either w or b grows from one piece to the next, or both
-        const Parts parts = parts_of(a.workspace, (size_t)slots * a.q_heads, D);
-        *reinterpret_cast<v4f*>(parts.o + ((size_t)(w + b) * a.q_heads + hq) * D + d) = v4f{o[0], o[1], o[2], o[3]};
-        if (d == 0) {
-          float m = tops[0][h];
+        for (int k = from; k < from + WAYS; ++k) {
+          l += sums[k][h];
 #pragma unroll
-          for (int k = 1; k < kWaves; ++k) m = fmaxf(m, tops[k][h]);
-          parts.ml[(size_t)(w + b) * a.q_heads + hq] = v2f{m, l};
+          for (int x = 0; x < 4; ++x) o[x] += outs[k][h][d + x];
+        }
+        const int hq = (first + from / WAYS) * group + g0 + h;
+        if (whole) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          *reinterpret_cast<v2u*>(a.out + ((int64_t)b * a.q_heads + hq) * D + d) =
+              v2u{bf16_pair(o[0] * inv, o[1] * inv), bf16_pair(o[2] * inv, o[3] * inv)};
+        } else {
+          // piece (w, b) has place w + b: along the tiles either w or b grows from one piece to the next, or both
+          const Parts parts = parts_of(a.workspace, (size_t)slots * a.q_heads, D);
+          *reinterpret_cast<v4f*>(parts.o + ((size_t)(w + b) * a.q_heads + hq) * D + d) = v4f{o[0], o[1], o[2], o[3]};
+          if (d == 0) {
+            float m = tops[from][h];
+#pragma unroll
+            for (int k = from + 1; k < from + WAYS; ++k) m = fmaxf(m, tops[k][h]);
+            parts.ml[(size_t)(w + b) * a.q_heads + hq] = v2f{m, l};
+          }
         }
       }
     }
@@ -358,14 +368,14 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void decode(Fp4Atten
 // o = sum_c 2^(m_c - m) o_c / sum_c 2^(m_c - m) l_c over the pieces of a sequence. D / 4 lanes hold an output; a workgroup has
 // `wide` query heads of a sequence, its other lanes go over the pieces in turn with them.
 template <int D>
-__global__ __launch_bounds__(256) void join(Fp4AttentionArgs a, int wide, int most, int slots) {
+__global__ __launch_bounds__(256) void join(Fp4AttentionArgs a, int wide, int most, int least, int slots) {
   constexpr int LANES = D / 4, GROUPS = 256 / LANES;
   __shared__ v4f red[GROUPS][LANES];
   __shared__ v2f red_ml[GROUPS];
   constexpr int kAtOnce = 4;  // pieces whose loads are in flight together
   const Paged& c = a.cache;
   const int lane = threadIdx.x & 63, b = blockIdx.y;
-  const Deal deal(c, a.window, a.sinks, most);
+  const Deal deal(c, a.window, a.sinks, most, least);
   int begin = 0;
   for (int i = 0; i < b; i += 64) begin += wave_total(i + lane < b ? tiles_of(c, i + lane, a.window, a.sinks) : 0);
   const int first = deal.who(begin), last = deal.who(begin + tiles_of(c, b, a.window, a.sinks) - 1);
@@ -399,25 +409,42 @@ __global__ __launch_bounds__(256) void join(Fp4AttentionArgs a, int wide, int mo
   }
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, int BESIDE>
 hipError_t launch(const Fp4AttentionArgs& a, hipStream_t st) {
   const Paged& c = a.cache;
-  const int group = a.q_heads / c.heads, blocks = (group + 15) / 16;
+  const int group = a.q_heads / c.heads, blocks = (group + 15) / 16, together = c.heads / BESIDE;
+  constexpr int WAVES = waves_of(BESIDE), WAYS = WAVES / BESIDE;
   // what the longest sequence that the table has room for can be cut into
   int64_t tokens = (int64_t)c.cols << c.shift;
   if (a.window && (int64_t)a.window + a.sinks + 2 * kTile < tokens) tokens = (int64_t)a.window + a.sinks + 2 * kTile;
   const int64_t longest = (tokens + kTile - 1) / kTile + 1;
-  const int64_t needed = (longest * c.batch + kMinTiles - 1) / kMinTiles;
-  const int pieces = FP4_ATTENTION_PIECES(c.batch, a.q_heads, c.heads);
-  const int most = (int)(needed < pieces ? needed : pieces), slots = most + c.batch;
-  hipLaunchKernelGGL((decode<D, E4M3>), dim3((unsigned)((most + 7) / 8 * 8 * c.heads * blocks)), dim3(64 * kWaves), 0, st, a, group, blocks, most,
-                     slots);
+  const int64_t needed = (longest * c.batch + WAYS - 1) / WAYS;
+  const int64_t pieces = FP4_ATTENTION_PIECES(c.batch, together * blocks * (WAVES / 4));
+  const int most = (int)(needed < pieces ? needed : pieces), slots = most + (int)c.batch;
+  hipLaunchKernelGGL((decode<D, E4M3, BESIDE>), dim3((unsigned)((most + 7) / 8 * 8 * together), (unsigned)blocks), dim3(64 * WAVES), 0, st,
+                     a, group, together, most, slots);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || most == 1) return e;
   constexpr int groups = 1024 / D;
-  const int wide = (int64_t)c.batch * a.q_heads >= 1024 ? groups : 1;  // few rows: all lanes to the pieces of one
-  hipLaunchKernelGGL((join<D>), dim3((unsigned)((a.q_heads + wide - 1) / wide), (unsigned)c.batch), dim3(256), 0, st, a, wide, most, slots);
+  // few rows: all lanes to the pieces of one (both ways, us: 1 x 131000 tokens 90 / 93, 64 sequences 64.5 / 61.4)
+  const int wide = (int64_t)c.batch * a.q_heads >= 1024 ? groups : 1;
+  hipLaunchKernelGGL((join<D>), dim3((unsigned)((a.q_heads + wide - 1) / wide), (unsigned)c.batch), dim3(256), 0, st, a, wide, most, WAYS,
+                     slots);
   return hipGetLastError();
+}
+
+template <int D, bool E4M3>
+hipError_t launch(const Fp4AttentionArgs& a, hipStream_t st) {
+  // heads that lie side by side, in rows of 256 bytes at most: up to 512 bytes of them to a workgroup
+  constexpr int bytes = D * (E4M3 ? 1 : 2);
+  if constexpr (bytes <= 256) {
+    if (a.cache.head_stride == bytes) {
+      if constexpr (bytes <= 128)
+        if (a.cache.heads % 4 == 0) return launch<D, E4M3, 4>(a, st);
+      if (a.cache.heads % 2 == 0) return launch<D, E4M3, 2>(a, st);
+    }
+  }
+  return launch<D, E4M3, 1>(a, st);
 }
 
 }  // namespace

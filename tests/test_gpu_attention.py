@@ -221,6 +221,16 @@ def test_many_sequences():
     run(c, 3, [min(n, i % 5) for i, n in enumerate(lengths)], pad=4)
 
 
+@pytest.mark.parametrize("layout", ["tokens", "gaps", "heads"])
+@pytest.mark.parametrize("H,Hq", [(4, 4), (4, 72), (2, 6), (8, 32), (6, 12), (3, 3)])
+@pytest.mark.parametrize("D,e4m3", [(64, False), (64, True), (128, False), (128, True), (256, True)])
+def test_heads_side_by_side(layout, H, Hq, D, e4m3):
+    """Rows of heads that lie next to each other go to one workgroup, two or four at a time; those that do not, one by one."""
+    c = Cache([1, 40, 31, 700, 0, 333], H, D, 16, e4m3, layout).fill()
+    run(c, Hq)
+    run(c, Hq, window=100, sinks=5)
+
+
 def test_long_decode_is_split():
     for e4m3 in (False, True):
         c = Cache([20000, 3, 4097], 1, 64, 64, e4m3).fill()
