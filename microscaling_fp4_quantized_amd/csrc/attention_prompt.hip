@@ -222,10 +222,17 @@ __device__ __forceinline__ Rows rows_of(const int* starts, int b, int T) {
   return {t0, t1 - t0};
 }
 
+// Whether eight waves share what is brought into LDS, where there are rows for them: 310 us at 8192 tokens and heads of 64, with workgroups
+// of four waves 338; 582 and 623 with heads of 128 in 8 bits. Heads of 64 in 8 bits need more than the 128 registers that four waves of a
+// SIMD have, and do better with three of 168 in workgroups of four waves (a window of 4096: 499 us, 607 with eight waves and 37 registers
+// spilled); heads of 256 fill the registers of a SIMD with one wave.
+template <int D, bool E4M3>
+constexpr bool kEight = D == 128 || (D == 64 && !E4M3);
+
 // SPLIT: blockIdx.y takes one of `splits` parts of its rows' tokens, at most. A kernel of its own, because what it adds to the registers
 // costs heads of 64 4% (455 -> 468 us with a window).
 template <int D, bool E4M3, int WAVES, bool SPLIT>
-__global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 4 : 2) void prompt(Fp4AttentionArgs a, int group, int tiles, int splits) {
+__global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 128 ? 2 : E4M3 ? 3 : 4) void prompt(Fp4AttentionArgs a, int group, int tiles, int splits) {
   extern __shared__ __align__(16) uint8_t memory[];
   typedef Lds<D, E4M3> L;
   constexpr int kRows = 32 * WAVES;
@@ -357,12 +364,17 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 64 ? 4 : 2) void pr
         hidden |= (~seen & 0xFFu) << (8 * n);
       }
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int i = 0; i < 32; i += 4) {
+        unsigned off[4];  // all ones if hidden; as asm, because the compiler makes a compare and a select of each
+        asm("v_bfe_i32 %0, %4, %5, 1\n\tv_bfe_i32 %1, %4, %6, 1\n\tv_bfe_i32 %2, %4, %7, 1\n\tv_bfe_i32 %3, %4, %8, 1"
+            : "=&v"(off[0]), "=&v"(off[1]), "=&v"(off[2]), "=&v"(off[3])
+            : "v"(hidden), "n"(i), "n"(i + 1), "n"(i + 2), "n"(i + 3));
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const unsigned off = (unsigned)((int)(hidden << (31 - 16 * u - i)) >> 31);
-          s[u][i] = __uint_as_float((__float_as_uint(s[u][i]) & ~off) | (__float_as_uint(kNever) & off));
+        for (int k = 0; k < 4; ++k) {  // off ? kNever : s
+          float& x = s[i / 16][i % 16 + k];
+          x = __uint_as_float(__builtin_amdgcn_bitop3_b32(off[k], __float_as_uint(kNever), __float_as_uint(x), 0xCA));
         }
+      }
     }
     if (!for_all(held(id), j)) {
       if (const unsigned long long odd = lds.odd[it & 3]) {  // a row that sees such a token is none of numbers
@@ -535,7 +547,7 @@ hipError_t launch(const Fp4AttentionArgs& a, hipStream_t st) {
   const int64_t most = (tokens + kMinTiles * kTokens - 1) / (kMinTiles * kTokens);
   int64_t splits = FP4_ATTENTION_SPLITS(a.T, c.batch, a.q_heads, c.heads);
   if (splits > most) splits = most;
-  if constexpr (D < 256) {
+  if constexpr (kEight<D, E4M3>) {
     // 256 rows share what is brought into LDS, once they fill the CUs
     if ((int64_t)a.T * a.q_heads * splits >= (int64_t)256 * cus)
       return splits > 1 ? launch<D, E4M3, 8, true>(a, (int)splits, dev, st) : launch<D, E4M3, 8, false>(a, 1, dev, st);
