@@ -224,7 +224,7 @@ __device__ __forceinline__ Rows rows_of(const int* starts, int b, int T) {
 
 // Whether eight waves share what is brought into LDS, where there are rows for them: 310 us at 8192 tokens and heads of 64, with workgroups
 // of four waves 338; 582 and 623 with heads of 128 in 8 bits. Heads of 64 in 8 bits need more than the 128 registers that four waves of a
-// SIMD have, and do better with three of 168 in workgroups of four waves (a window of 4096: 499 us, 607 with eight waves and 37 registers
+// SIMD have, and do better with three of 168 in workgroups of four waves (a window of 1024: 499 us, 607 with eight waves and 37 registers
 // spilled); heads of 256 fill the registers of a SIMD with one wave.
 template <int D, bool E4M3>
 constexpr bool kEight = D == 128 || (D == 64 && !E4M3);
@@ -393,9 +393,13 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 128 ? 2 : E4M3 ? 3 
       top = m;
       sum *= keep;
 #pragma unroll
-      for (int m2 = 0; m2 < D / 32; ++m2)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[m2][i] *= keep;
+      for (int m2 = 0; m2 < D / 32; ++m2) {
+        // heads of 256 have their outputs in accumulation registers: held there up to here, or the compiler moves all of them to
+        // others and back for every tile (230 -> 200 us at 4096 tokens)
+        if constexpr (D == 256) asm volatile("" : "+a"(o[m2]));
+        o[m2] *= keep;
+        if constexpr (D == 256) asm volatile("" : "+a"(o[m2]));
+      }
     }
     const float m = top == kNever ? 0.f : top;
     unsigned w[16];
