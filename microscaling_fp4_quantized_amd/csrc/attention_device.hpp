@@ -58,6 +58,13 @@ __device__ __forceinline__ void arrived(T& x) {
   x = __builtin_bit_cast(T, w);
 }
 
+// The same number, from here on as far as the compiler knows: what follows from it is computed where it is needed and holds no registers
+// from before. An offset of 32 bits goes into a load with its scalar address so; addresses made ahead of the loop took 64 bits each.
+__device__ __forceinline__ unsigned here(unsigned x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // A word that all lanes read alike and that no kernel running now writes, into scalar registers.
 __device__ __forceinline__ int uniform_load(const int* p) {
   return *(const __attribute__((address_space(4))) int*)(reinterpret_cast<uintptr_t>(p));

@@ -1,9 +1,10 @@
 // Attention of many new tokens of each sequence over a paged key-value cache: causal, with or without a window and first tokens
 // that stay visible.
 //
-// Bound by the matrix cores (4 D operations for a row, a head and a visible token). A workgroup takes 128 rows of a sequence and a
-// key-value head: the query heads that share the head are rows side by side, so that few tokens still fill a tile and the keys
-// are read once for all of them. Its four waves have 32 rows each and go over tiles of 64 tokens that all of them read from LDS.
+// Bound by the matrix cores (4 D operations for a row, a head and a visible token), heads of 64 by the vector instructions of the softmax.
+// A workgroup takes 256 or 128 rows of a sequence and a key-value head: the query heads that share the head are rows side by side, so that
+// few tokens still fill a tile and the keys are read once for all of them. Its eight or four waves have 32 rows each and go over tiles of 64
+// tokens that all of them read from LDS. With 32 rows a wave the reads keep LDS busy for about half the time that the products take.
 //
 //   S^T = K Q^T (32 x 32 x 16 products): a lane has the scores of one row, half of the tile's tokens, so maxima and sums need one
 //   step across the wave. K's row r is token r with bits 2 and 3 exchanged: the scores of a lane are then 8 consecutive tokens of
@@ -11,6 +12,12 @@
 //   O^T = V^T P^T: P goes on in registers. V is turned on its way into LDS, by byte permutes of 4 tokens x 8 dims of a thread.
 // Rows of 16 more bytes (K) and of 9 chunks of 16 bytes (V^T) keep the 16-byte reads of 32 rows free of bank conflicts.
 // The next tile's loads are in flight during a tile's products, in registers, and go into the other half of LDS behind them.
+//
+// Measured: 8192 tokens of 32 heads of 128 524 to 545 us on different machines, 1.01 to 1.05 PFLOP/s, where torch's large bf16 product
+// reaches 1.22; the matrix cores are busy 47% of the CUs' cycles, vector instructions as much. Three sequences of up to 9000 tokens of 64
+// heads of 64 with a window of 1024 401 to 422 us, 0.7 PFLOP/s: vector instructions take 85% of the cycles, exponentials a third of that. Not faster:
+// the scores a tile ahead of the sums (609 us against 545; heads of 256 207 and 200), two groups of waves half a tile apart (566 and 526),
+// leaving out the tiles that a wave's rows do not see but another's do (552 and 540).
 //
 // The running maximum may lag behind by 2^8 before sums and outputs are scaled again. p is rounded to bf16 for the second product;
 // its sum is not. 8-bit caches: codes are exact in bf16, the scales are applied in float32 to scores and p.
@@ -95,6 +102,7 @@ struct Fetch {
   }
   __device__ __forceinline__ void keys(P& x, const Paged& c, int head, const Ids& id, int j, int g, int lane) const {
     const uint8_t* at = c.k + place(c, head, pick(id, g), j + g * kGranule);
+    const unsigned k = here(this->k);
 #pragma unroll
     for (int i = 0; i < P::KL; ++i) {
       const v4u y = *reinterpret_cast<const v4u*>(at + (k + i * (64 / P::LANES) * token));
@@ -105,6 +113,7 @@ struct Fetch {
   }
   __device__ __forceinline__ void values(P& x, const Paged& c, int head, const Ids& id, int j, int g, int lane) const {
     const uint8_t* at = c.v + place(c, head, pick(id, g), j + g * kGranule);
+    const unsigned v = here(this->v);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -225,14 +234,15 @@ __device__ __forceinline__ Rows rows_of(const int* starts, int b, int T) {
 // Whether eight waves share what is brought into LDS, where there are rows for them: 310 us at 8192 tokens and heads of 64, with workgroups
 // of four waves 338; 582 and 623 with heads of 128 in 8 bits. Heads of 64 in 8 bits need more than the 128 registers that four waves of a
 // SIMD have, and do better with three of 168 in workgroups of four waves (a window of 1024: 499 us, 607 with eight waves and 37 registers
-// spilled); heads of 256 fill the registers of a SIMD with one wave.
+// spilled); heads of 256 fill the registers of a SIMD with one wave. No variant may keep anything in scratch memory: the loop would wait for
+// it, and with it for the next tile's loads.
 template <int D, bool E4M3>
 constexpr bool kEight = D == 128 || (D == 64 && !E4M3);
 
 // SPLIT: blockIdx.y takes one of `splits` parts of its rows' tokens, at most. A kernel of its own, because what it adds to the registers
 // costs heads of 64 4% (455 -> 468 us with a window).
 template <int D, bool E4M3, int WAVES, bool SPLIT>
-__global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 128 ? 2 : E4M3 ? 3 : 4) void prompt(Fp4AttentionArgs a, int group, int tiles, int splits) {
+__global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 128 ? 2 : WAVES == 8 ? 4 : 3) void prompt(Fp4AttentionArgs a, int group, int tiles, int splits) {
   extern __shared__ __align__(16) uint8_t memory[];
   typedef Lds<D, E4M3> L;
   constexpr int kRows = 32 * WAVES;
@@ -441,6 +451,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 128 ? 2 : E4M3 ? 3 
   constexpr int VDIM = Part<D, E4M3>::VDIM;
   if (SPLIT && parts > 1) {
     // a lane has VDIM dims in a row of every eighth: (m2 / 4) 128 + VDIM r + {0 .. VDIM - 1}
+    const int token = here(place) - base, row = r0 + wave * 32 + ((E4M3 ? here(lane) : lane) & 31);
     if (row <= last) {
       const size_t n = (size_t)a.T * a.q_heads, at = part * n + (size_t)(rows.first + token) * a.q_heads + head * group + (row - token * group);
       const Parts to = parts_of(a.workspace, splits * n, D);
@@ -544,7 +555,8 @@ hipError_t launch(const Fp4AttentionArgs& a, hipStream_t st) {
   hipError_t e = hipGetDevice(&dev);
   if (e == hipSuccess) e = fp4_device_cus(dev, &cus);
   if (e != hipSuccess) return e;
-  // few rows: their tokens split over workgroups, as far as the longest sequence that the table has room for goes
+  // few rows: their tokens split over workgroups, as far as the longest sequence that the table has room for goes. Us with and without: two
+  // pieces of 512 tokens behind 16000 269 / 391, one token behind 60000 88 / 1381.
   const Paged& c = a.cache;
   int64_t tokens = (int64_t)c.cols << c.shift;
   if (a.window && (int64_t)a.window + a.sinks + 32 * 8 < tokens) tokens = (int64_t)a.window + a.sinks + 32 * 8;
@@ -552,7 +564,9 @@ hipError_t launch(const Fp4AttentionArgs& a, hipStream_t st) {
   int64_t splits = FP4_ATTENTION_SPLITS(a.T, c.batch, a.q_heads, c.heads);
   if (splits > most) splits = most;
   if constexpr (kEight<D, E4M3>) {
-    // 256 rows share what is brought into LDS, once they fill the CUs
+    // 256 rows share what is brought into LDS, once they fill the CUs. Us with 256 and 128 rows, heads of 128: 8192 tokens 540 / 588, two
+    // pieces of 512 tokens behind 16000 272 / 305; below the line 4 sequences of 200 to 900 tokens 50.9 / 49.8, two of 16 tokens behind
+    // 30000 125 / 82, one token behind 60000 140 / 89.
     if ((int64_t)a.T * a.q_heads * splits >= (int64_t)256 * cus)
       return splits > 1 ? launch<D, E4M3, 8, true>(a, (int)splits, dev, st) : launch<D, E4M3, 8, false>(a, 1, dev, st);
   }
