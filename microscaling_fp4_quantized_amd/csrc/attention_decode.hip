@@ -24,6 +24,8 @@
 //
 // 8-bit caches: codes are exact in bf16, so the matrix cores see codes and the scales are applied in float32, a key's to its score
 // and a value's to its p. p is rounded to bf16 for the second product (at most 2^-8 of each p, and as often up as down); its sum is not.
+#include <algorithm>
+
 #include "../../include/fp4.h"
 #include "attention_device.hpp"
 
@@ -425,8 +427,10 @@ hipError_t launch(const Fp4AttentionArgs& a, hipStream_t st) {
   if (a.window && (int64_t)a.window + a.sinks + 2 * kTile < tokens) tokens = (int64_t)a.window + a.sinks + 2 * kTile;
   const int64_t longest = (tokens + kTile - 1) / kTile + 1;
   const int64_t needed = (longest * c.batch + WAYS - 1) / WAYS;
-  const int64_t pieces = FP4_ATTENTION_PIECES(c.batch, together * blocks * (WAVES / 4));
-  const int most = (int)(needed < pieces ? needed : pieces), slots = most + (int)c.batch;
+  // more units can round up to more pieces than fewer do, and the workspace is for the fewest
+  const int64_t pieces = std::min(FP4_ATTENTION_PIECES(c.batch, together * blocks * (WAVES / 4)),
+                                  FP4_ATTENTION_PIECES(c.batch, FP4_ATTENTION_UNITS_(a.q_heads, c.heads)));
+  const int most = (int)std::min(needed, pieces), slots = most + (int)c.batch;
   hipLaunchKernelGGL((decode<D, E4M3, BESIDE>), dim3((unsigned)((most + 7) / 8 * 8 * together), (unsigned)blocks), dim3(64 * WAVES), 0, st,
                      a, group, together, most, slots);
   const hipError_t e = hipGetLastError();

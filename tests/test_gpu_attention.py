@@ -231,6 +231,20 @@ def test_heads_side_by_side(layout, H, Hq, D, e4m3):
     run(c, Hq, window=100, sinks=5)
 
 
+@pytest.mark.parametrize("H,Hq,nB,layout", [(12, 12, 169, "heads"), (24, 24, 85, "tokens"), (24, 48, 85, "heads"), (20, 20, 101, "tokens")])
+def test_a_workspace_of_just_its_bytes_is_enough(H, Hq, nB, layout):
+    """Where the pieces of a batch, rounded up to whole rounds of workgroups, come to more than the workspace is for."""
+    D = 64
+    c = Cache([97 + (37 * b) % 120 for b in range(nB)], H, D, 16, False, layout).fill()
+    args, q = c.device(), queries(nB, Hq, D)
+    bytes_ = F.attention_workspace_bytes(nB, nB, Hq, H, D)
+    memory = torch.full((bytes_ + (8 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+    got = F.fp4_attention_decode(q.cuda(), *args, workspace=memory[:bytes_], **c.more)
+    want, tol = attention(c, q, range(nB + 1), D ** -0.5)
+    check(got, want, tol, f"decode {nB} sequences heads {Hq}/{H} {layout}")
+    assert (memory[bytes_:] == 0xA5).all()
+
+
 def test_long_decode_is_split():
     for e4m3 in (False, True):
         c = Cache([20000, 3, 4097], 1, 64, 64, e4m3).fill()
