@@ -397,7 +397,8 @@ FP4_API int fp4_moe_experts(const void *X, int64_t T, int64_t D, int64_t ldx, co
  *  table       device int [batch, cols], row stride table_stride >= cols. A page id outside [0, pages) (-1, say) is no page: its
  *              tokens are not visible and nothing is written for them.
  *  cols        >= 1, cols * page_size <= 2^30, times batch <= 2^35: tokens past that are as tokens of no page.
- *  lengths     device int [batch]; below 0 counts as 0, above 2^30 as 2^30.
+ *  lengths     device int [batch]; below 0 counts as 0, above 2^30 as 2^30 (a new row's place is counted from it as it is: one before
+ *              the sequence or past its table is written nowhere, its query is rotated by that place).
  *  batch       1..65535, batch * query heads <= 2^22.
  */
 enum { FP4_KV_BF16 = 0, FP4_KV_E4M3 = 1 };
@@ -447,8 +448,8 @@ FP4_API int fp4_kv_append(const fp4_kv_cache *cache, const int *starts, int64_t 
  * over the visible tokens j of the sequence: j <= i and (window == 0 or i - j < window or j < sinks).
  * fp4_attention_decode is for one new token of each sequence (row b belongs to sequence b); fp4_attention_prompt for many.
  * Rows that see no token get zeros. Scores, p's sum and the output's sum are float32; p is rounded to bf16 for the product with v.
- * A NaN or infinity in a visible key or value, or in q, gives outputs of that row and head that are not numbers, and
- * no others.
+ * A NaN or infinity in a visible key or value, or in q, gives outputs of that row and head that are not finite, and no others;
+ * but a score of minus infinity is one of a token that the row does not see.
  *  Q            device bf16, rows of q_heads heads of dim: strides as above. q_heads a multiple of cache->heads, up to 1024.
  *  scale        finite and positive.   window, sinks >= 0 (above 2^30 they count as 2^30).
  *  Out          device bf16 [T, q_heads, dim], 16-byte aligned.

@@ -567,7 +567,9 @@ hipError_t launch(const Fp4AttentionArgs& a, hipStream_t st) {
     // 256 rows share what is brought into LDS, once they fill the CUs. Us with 256 and 128 rows, heads of 128: 8192 tokens 540 / 588, two
     // pieces of 512 tokens behind 16000 272 / 305; below the line 4 sequences of 200 to 900 tokens 50.9 / 49.8, two of 16 tokens behind
     // 30000 125 / 82, one token behind 60000 140 / 89.
-    if ((int64_t)a.T * a.q_heads * splits >= (int64_t)256 * cus)
+    // (A grid has fewer than 2^32 work-items.)
+    const int64_t blocks = (((int64_t)a.T * (a.q_heads / c.heads) + 255) / 256 + c.batch) * c.heads;
+    if ((int64_t)a.T * a.q_heads * splits >= (int64_t)256 * cus && blocks < (1 << 23))
       return splits > 1 ? launch<D, E4M3, 8, true>(a, (int)splits, dev, st) : launch<D, E4M3, 8, false>(a, 1, dev, st);
   }
   return splits > 1 ? launch<D, E4M3, 4, true>(a, (int)splits, dev, st) : launch<D, E4M3, 4, false>(a, 1, dev, st);

@@ -80,7 +80,7 @@ __global__ __launch_bounds__(64 * kWaves) void kv_append(Fp4AppendArgs a, int pa
   const int units = (a.q_heads + 2 * c.heads) * PIECES;
   const int b = __builtin_amdgcn_readfirstlane(sequence_of(a.starts, c.batch, t));
   if (b < 0) return;
-  const int i = c.lengths[b] - (a.starts ? a.starts[b + 1] - t : 1);
+  const int i = (int)((unsigned)c.lengths[b] - (unsigned)(a.starts ? a.starts[b + 1] - t : 1));
   int page = -1;
   if (i >= 0 && (i >> c.shift) < c.cols) page = c.table[b * c.table_stride + (i >> c.shift)];
   const bool held = (unsigned)page < (unsigned)c.pages;
