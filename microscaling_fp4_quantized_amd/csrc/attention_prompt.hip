@@ -13,7 +13,7 @@
 // Rows of 16 more bytes (K) and of 9 chunks of 16 bytes (V^T) keep the 16-byte reads of 32 rows free of bank conflicts.
 // The next tile's loads are in flight during a tile's products, in registers, and go into the other half of LDS behind them.
 //
-// Measured: 8192 tokens of 32 heads of 128 524 to 545 us on different machines, 1.01 to 1.05 PFLOP/s, where torch's large bf16 product
+// Measured: 8192 tokens of 32 heads of 128 524 to 556 us on different machines, 0.99 to 1.05 PFLOP/s, where torch's large bf16 product
 // reaches 1.22; the matrix cores are busy 47% of the CUs' cycles, vector instructions as much. Three sequences of up to 9000 tokens of 64
 // heads of 64 with a window of 1024 401 to 422 us, 0.7 PFLOP/s: vector instructions take 85% of the cycles, exponentials a third of that. Not faster:
 // the scores a tile ahead of the sums (609 us against 545; heads of 256 207 and 200), two groups of waves half a tile apart (566 and 526),
@@ -82,7 +82,8 @@ __device__ __forceinline__ int pick(const Ids& x, int g) {
   return (g & 2) ? b : a;
 }
 
-// A granule's place is the same for a wave (scalar registers), the offset within it stays the thread's.
+// A granule's place is the same for a wave (scalar registers), the offset within it stays the thread's. Heads of 64, which are short of
+// registers, make their addresses where they use them (seven sequences of 1 to 150 tokens and heads of 128: 10.5 us, 10.85 so).
 template <int D, bool E4M3>
 struct Fetch {
   typedef Part<D, E4M3> P;
@@ -102,7 +103,7 @@ struct Fetch {
   }
   __device__ __forceinline__ void keys(P& x, const Paged& c, int head, const Ids& id, int j, int g, int lane) const {
     const uint8_t* at = c.k + place(c, head, pick(id, g), j + g * kGranule);
-    const unsigned k = here(this->k);
+    const unsigned k = D == 64 ? here(this->k) : this->k;
 #pragma unroll
     for (int i = 0; i < P::KL; ++i) {
       const v4u y = *reinterpret_cast<const v4u*>(at + (k + i * (64 / P::LANES) * token));
@@ -113,7 +114,7 @@ struct Fetch {
   }
   __device__ __forceinline__ void values(P& x, const Paged& c, int head, const Ids& id, int j, int g, int lane) const {
     const uint8_t* at = c.v + place(c, head, pick(id, g), j + g * kGranule);
-    const unsigned v = here(this->v);
+    const unsigned v = D == 64 ? here(this->v) : this->v;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -451,7 +452,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 128 ? 2 : WAVES == 
   constexpr int VDIM = Part<D, E4M3>::VDIM;
   if (SPLIT && parts > 1) {
     // a lane has VDIM dims in a row of every eighth: (m2 / 4) 128 + VDIM r + {0 .. VDIM - 1}
-    const int token = here(place) - base, row = r0 + wave * 32 + ((E4M3 ? here(lane) : lane) & 31);
+    const int token = (D == 64 ? here(place) : place) - base, row = r0 + wave * 32 + ((D == 64 && E4M3 ? here(lane) : lane) & 31);
     if (row <= last) {
       const size_t n = (size_t)a.T * a.q_heads, at = part * n + (size_t)(rows.first + token) * a.q_heads + head * group + (row - token * group);
       const Parts to = parts_of(a.workspace, splits * n, D);
