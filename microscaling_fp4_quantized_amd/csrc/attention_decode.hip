@@ -377,10 +377,7 @@ __global__ __launch_bounds__(64 * waves_of(BESIDE), 2) void decode(Fp4AttentionA
 // `wide` query heads of a sequence, its other lanes go over the pieces in turn with them.
 template <int D>
 __global__ __launch_bounds__(256) void join(Fp4AttentionArgs a, int wide, int most, int least, int slots) {
-  constexpr int LANES = D / 4, GROUPS = 256 / LANES;
-  __shared__ v4f red[GROUPS][LANES];
-  __shared__ v2f red_ml[GROUPS];
-  constexpr int kAtOnce = 4;  // pieces whose loads are in flight together
+  constexpr int LANES = D / 4;
   const Paged& c = a.cache;
   const int lane = threadIdx.x & 63, b = blockIdx.y;
   const Deal deal(c, a.window, a.sinks, most, least);
@@ -388,31 +385,13 @@ __global__ __launch_bounds__(256) void join(Fp4AttentionArgs a, int wide, int mo
   for (int i = 0; i < b; i += 64) begin += wave_total(i + lane < b ? tiles_of(c, i + lane, a.window, a.sinks) : 0);
   const int first = deal.who(begin), last = deal.who(begin + tiles_of(c, b, a.window, a.sinks) - 1);
   if (first == last) return;  // written by its only workgroup
-  const int g = threadIdx.x / LANES, e = 4 * (threadIdx.x % LANES), turns = GROUPS / wide;
-  const int hq = blockIdx.x * wide + g % wide, h = min(hq, a.q_heads - 1);
+  const int hq = blockIdx.x * wide + threadIdx.x / LANES % wide, h = min(hq, a.q_heads - 1);
   const Parts parts = parts_of(a.workspace, (size_t)slots * a.q_heads, D);
-  v2f ml{kNever, 0.f};
-  v4f o{0.f, 0.f, 0.f, 0.f};
-  for (int w = first + g / wide; w <= last; w += kAtOnce * turns) {
-    v2f x[kAtOnce];
-    v4f y[kAtOnce];
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const size_t at = (size_t)(min(w + i * turns, last) + b) * a.q_heads + h;
-      x[i] = parts.ml[at];
-      y[i] = *reinterpret_cast<const v4f*>(parts.o + at * D + e);
-    }
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i)
-      if (w + i * turns <= last) join_parts(ml, o, x[i], y[i]);
-  }
-  red[g][threadIdx.x % LANES] = o;
-  if (e == 0) red_ml[g] = ml;
-  __syncthreads();
-  if (g < wide && hq < a.q_heads) {
-    for (int i = g + wide; i < GROUPS; i += wide) join_parts(ml, o, red_ml[i], red[i][threadIdx.x % LANES]);
+  v2f ml;
+  v4f o;
+  if (join_all<D>(parts, wide, first, last, [&](int w) { return (size_t)(w + b) * a.q_heads + h; }, ml, o) && hq < a.q_heads) {
     const float inv = ml[1] == 0.f ? 0.f : 1.f / ml[1];
-    *reinterpret_cast<v2u*>(a.out + ((int64_t)b * a.q_heads + hq) * D + e) =
+    *reinterpret_cast<v2u*>(a.out + ((int64_t)b * a.q_heads + hq) * D + 4 * (threadIdx.x % LANES)) =
         v2u{bf16_pair(o[0] * inv, o[1] * inv), bf16_pair(o[2] * inv, o[3] * inv)};
   }
 }

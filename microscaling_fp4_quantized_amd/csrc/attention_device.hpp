@@ -94,4 +94,37 @@ __device__ __forceinline__ void join_parts(v2f& ml, v4f& o, v2f x, v4f y) {
 __device__ __forceinline__ unsigned low_halves(unsigned a, unsigned b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
 __device__ __forceinline__ unsigned high_halves(unsigned a, unsigned b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
 
+// Partial results first .. last of outputs joined by the 256 threads of a workgroup: `wide` outputs side by side, D / 4 lanes hold one
+// of them, the other lanes go over the partial results in turn with them. True for the lanes that have the sum in the end.
+template <int D, class Place>
+__device__ __forceinline__ bool join_all(const Parts& parts, int wide, int first, int last, Place place, v2f& ml, v4f& o) {
+  constexpr int LANES = D / 4, GROUPS = 256 / LANES;
+  constexpr int kAtOnce = 4;  // whose loads are in flight together
+  __shared__ v4f red[GROUPS][LANES];
+  __shared__ v2f red_ml[GROUPS];
+  const int g = threadIdx.x / LANES, lane = threadIdx.x % LANES, turns = GROUPS / wide;
+  ml = v2f{kNever, 0.f};
+  o = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int w = first + g / wide; w <= last; w += kAtOnce * turns) {
+    v2f x[kAtOnce];
+    v4f y[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const size_t at = place(min(w + i * turns, last));
+      x[i] = parts.ml[at];
+      y[i] = *reinterpret_cast<const v4f*>(parts.o + at * D + 4 * lane);
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      if (w + i * turns <= last) join_parts(ml, o, x[i], y[i]);
+  }
+  if (turns == 1) return true;
+  red[g][lane] = o;
+  if (lane == 0) red_ml[g] = ml;
+  __syncthreads();
+  if (g >= wide) return false;
+  for (int i = g + wide; i < GROUPS; i += wide) join_parts(ml, o, red_ml[i], red[i][lane]);
+  return true;
+}
+
 }  // namespace fp4

@@ -220,8 +220,13 @@ __device__ __forceinline__ Range range_of(const Paged& c, int len, int i0, int i
   r.tiles = r.ta + max(end - r.tb, 0);
   return r;
 }
-// Parts that are worth a workgroup each, at most.
-__device__ __forceinline__ int worth(const Range& r) { return max(1, (r.tiles + kMinTiles - 1) / kMinTiles); }
+// Parts of so many tiles that are worth a workgroup each. Few rows are joined quickly: up to 32 parts of half the size for them. Us with and
+// without: 16 tokens behind 1000 13.8 / 16.1, 8 of 16 heads of 256 behind 600 18.3 / 23.0; but 300 tokens, all for one of their own, 18.0 / 17.1,
+// 64 of 16 heads behind 8000 in 64 parts and not 32 24.8 / 19.5.
+__host__ __device__ inline int64_t worth(int64_t tiles, int64_t T, int q_heads, int dim) {
+  const int64_t parts = (tiles + kMinTiles - 1) / kMinTiles, fine = (tiles + 1) / 2;
+  return T * q_heads * dim > (1 << 18) || parts >= 32 ? parts : fine < 32 ? fine : 32;
+}
 
 // Rows of a sequence: new tokens times the heads of a group.
 struct Rows {
@@ -285,7 +290,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 128 ? 2 : WAVES == 
   const int* pages = c.table + b * c.table_stride;
 
   const Range range = range_of(c, len, base + tile * kRows / group, base + min(tile * kRows + kRows - 1, last) / group, a.window, a.sinks);
-  const int parts = SPLIT ? min(splits, worth(range)) : 1, part = SPLIT ? blockIdx.y : 0;
+  const int parts = SPLIT ? max((int)min((int64_t)splits, worth(range.tiles, a.T, a.q_heads, D)), 1) : 1, part = SPLIT ? blockIdx.y : 0;
   if (part >= parts) return;
   const int from = SPLIT ? (int)((int64_t)range.tiles * part / parts) : 0;
   const int end = SPLIT ? (int)((int64_t)range.tiles * (part + 1) / parts) : range.tiles;
@@ -509,40 +514,27 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : D == 128 ? 2 : WAVES == 
   }
 }
 
-// out = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p over the parts of a row and head, where there is more than one. D / 4 lanes for
-// a head, 1024 / D heads of a token in a workgroup.
+// out = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p over the parts of a row and head, where there is more than one. A workgroup has
+// `wide` heads of a token.
 template <int D>
-__global__ __launch_bounds__(256) void join(Fp4AttentionArgs a, int group, int tile_rows, int splits) {
-  constexpr int LANES = D / 4, kAtOnce = 4;  // parts whose loads are in flight together
+__global__ __launch_bounds__(256) void join(Fp4AttentionArgs a, int group, int tile_rows, int splits, int wide) {
+  constexpr int LANES = D / 4;
   const Paged& c = a.cache;
-  const int t = blockIdx.x, h = blockIdx.y * (256 / LANES) + threadIdx.x / LANES, e = 4 * (threadIdx.x % LANES);
+  const int t = blockIdx.x, hq = blockIdx.y * wide + threadIdx.x / LANES % wide, h = min(hq, a.q_heads - 1);
   const int b = __builtin_amdgcn_readfirstlane(sequence_of(a.starts, c.batch, t));
-  if (b < 0 || h >= a.q_heads) return;
+  if (b < 0) return;
   const Rows rows = rows_of(a.starts, b, a.T);
   const int len = length_of(c, b), base = len - rows.count, last = rows.count * group - 1;
   const int first = ((t - rows.first) * group + h % group) / tile_rows * tile_rows;
-  const int parts = min(splits, worth(range_of(c, len, base + first / group, base + min(first + tile_rows - 1, last) / group,
-                                                  a.window, a.sinks)));
-  if (parts == 1) return;  // written by its only part
+  const Range range = range_of(c, len, base + first / group, base + min(first + tile_rows - 1, last) / group, a.window, a.sinks);
+  const int parts = max((int)min((int64_t)splits, worth(range.tiles, a.T, a.q_heads, D)), 1);
   const size_t n = (size_t)a.T * a.q_heads, at = (size_t)t * a.q_heads + h;
-  const Parts from = parts_of(a.workspace, splits * n, D);
-  v2f ml{kNever, 0.f};
-  v4f o{0.f, 0.f, 0.f, 0.f};
-  for (int p = 0; p < parts; p += kAtOnce) {
-    v2f x[kAtOnce];
-    v4f y[kAtOnce];
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const size_t place = min(p + i, parts - 1) * n + at;
-      x[i] = from.ml[place];
-      y[i] = *reinterpret_cast<const v4f*>(from.o + place * D + e);
-    }
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i)
-      if (p + i < parts) join_parts(ml, o, x[i], y[i]);
-  }
+  v2f ml;
+  v4f o;
+  const bool has = join_all<D>(parts_of(a.workspace, splits * n, D), wide, 0, parts > 1 ? parts - 1 : -1, [&](int p) { return p * n + at; }, ml, o);
+  if (!has || parts == 1 || hq >= a.q_heads) return;  // one part: written by it
   const float inv = ml[1] == 0.f ? 0.f : 1.f / ml[1];
-  *reinterpret_cast<v2u*>(a.out + at * D + e) = v2u{bf16_pair(o[0] * inv, o[1] * inv), bf16_pair(o[2] * inv, o[3] * inv)};
+  *reinterpret_cast<v2u*>(a.out + at * D + 4 * (threadIdx.x % LANES)) = v2u{bf16_pair(o[0] * inv, o[1] * inv), bf16_pair(o[2] * inv, o[3] * inv)};
 }
 
 template <int D, bool E4M3, int WAVES, bool SPLIT>
@@ -562,8 +554,10 @@ hipError_t launch(const Fp4AttentionArgs& a, int splits, int dev, hipStream_t st
   hipLaunchKernelGGL(kern, dim3((unsigned)(tiles * a.cache.heads), splits), dim3(64 * WAVES), bytes, st, a, group, (int)tiles, splits);
   e = hipGetLastError();
   if (e != hipSuccess || !SPLIT) return e;
-  constexpr int heads = 1024 / D;
-  hipLaunchKernelGGL((join<D>), dim3((unsigned)a.T, (unsigned)((a.q_heads + heads - 1) / heads)), dim3(256), 0, st, a, group, rows, splits);
+  // heads of a workgroup of the join: fewer where they have many parts (one token behind 60000, 64 parts: 87 us with all, 76 so)
+  int wide = 1024 / D;
+  while (wide > 1 && splits * wide > 4 * (1024 / D)) wide /= 2;
+  hipLaunchKernelGGL((join<D>), dim3((unsigned)a.T, (unsigned)((a.q_heads + wide - 1) / wide)), dim3(256), 0, st, a, group, rows, splits, wide);
   return hipGetLastError();
 }
 
@@ -574,11 +568,11 @@ hipError_t launch(const Fp4AttentionArgs& a, hipStream_t st) {
   if (e == hipSuccess) e = fp4_device_cus(dev, &cus);
   if (e != hipSuccess) return e;
   // few rows: their tokens split over workgroups, as far as the longest sequence that the table has room for goes. Us with and without: two
-  // pieces of 512 tokens behind 16000 269 / 391, one token behind 60000 88 / 1381.
+  // pieces of 512 tokens behind 16000 274 / 391, one token behind 60000 77 / 1381.
   const Paged& c = a.cache;
   int64_t tokens = (int64_t)c.cols << c.shift;
   if (a.window && (int64_t)a.window + a.sinks + 32 * 8 < tokens) tokens = (int64_t)a.window + a.sinks + 32 * 8;
-  const int64_t most = (tokens + kMinTiles * kTokens - 1) / (kMinTiles * kTokens);
+  const int64_t tiles = (tokens + kTokens - 1) / kTokens, most = tiles > kMinTiles ? worth(tiles, a.T, a.q_heads, D) : 1;
   int64_t splits = FP4_ATTENTION_SPLITS(a.T, c.batch, a.q_heads, c.heads);
   if (splits > most) splits = most;
   if constexpr (kEight<D, E4M3>) {

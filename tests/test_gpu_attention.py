@@ -245,6 +245,20 @@ def test_a_workspace_of_just_its_bytes_is_enough(H, Hq, nB, layout):
     assert (memory[bytes_:] == 0xA5).all()
 
 
+@pytest.mark.parametrize("H,Hq,news,D,e4m3", [(2, 8, [3, 17], 64, False), (1, 16, [9], 128, True), (4, 4, [1, 1, 40], 256, False), (8, 8, [60], 128, False)])
+def test_a_workspace_of_just_its_bytes_is_enough_for_split_rows(H, Hq, news, D, e4m3):
+    c = Cache([2000 + 700 * i for i in range(len(news))], H, D, 64, e4m3).fill()
+    T, nB = sum(news), len(news)
+    args, q = c.device(), queries(T, Hq, D)
+    st = torch.tensor([0, *torch.tensor(news).cumsum(0).tolist()], dtype=torch.int32)
+    bytes_ = F.attention_workspace_bytes(T, nB, Hq, H, D)
+    memory = torch.full((bytes_ + (8 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+    got = F.fp4_attention_prompt(q.cuda(), *args, st.cuda(), workspace=memory[:bytes_], **c.more)
+    want, tol = attention(c, q, st.tolist(), D ** -0.5)
+    check(got, want, tol, f"prompt rows {news} heads {Hq}/{H} of {D}")
+    assert (memory[bytes_:] == 0xA5).all()
+
+
 def test_long_decode_is_split():
     for e4m3 in (False, True):
         c = Cache([20000, 3, 4097], 1, 64, 64, e4m3).fill()
