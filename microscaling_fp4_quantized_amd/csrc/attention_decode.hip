@@ -7,7 +7,8 @@
 // meet once at the end. Where a token's heads lie side by side in short rows, the waves take two or four heads instead: rows of 128
 // bytes, read by workgroups that are not in step, cost memory a quarter of its rate (64 sequences, 8 bits: 64.6 -> 57 us). The tiles of
 // all sequences, one after the other, are dealt out evenly: a workgroup has the same number of them whatever the lengths, and goes on
-// with the next sequence where one ends. Pieces of a sequence meet in a second launch (join).
+// with the next sequence where one ends. Pieces of a sequence meet in a second launch (join). Where the table or the window keep sequences
+// short, a workgroup has one whole, and there is no second launch.
 //
 // Measured, with the join: 1000 tokens of 8 key-value heads 9.3 us, 5.6 of them here and 3.4 in the join, which together are near what two
 // launches take; 131000 tokens 91 us (537 MB at 5.9 TB/s, as fast as memory is copied); 64 sequences in 8 bits 60 us (235 MB at 4.3 TB/s
@@ -264,24 +265,34 @@ __global__ __launch_bounds__(64 * waves_of(BESIDE), 2) void decode(Fp4AttentionA
   const int turn = blockIdx.x >> 3, w = turn / together * 8 + (blockIdx.x & 7), first = turn % together * BESIDE;
   constexpr int WAYS = WAVES / BESIDE;
   const int way = wave % WAYS, head = first + wave / WAYS, g0 = 16 * blockIdx.y, heads = min(16, group - g0);
-  const Deal deal(c, a.window, a.sinks, most, WAYS);
-  if (w >= deal.count) return;
-  int at = deal.first_of(w);             // the next tile, of all sequences'
-  const int stop = deal.first_of(w + 1);
+  int at, stop;                              // the next tile, of all sequences', and where the workgroup's end
   int b = 0, begin = 0, tiles = 0, len = 0;  // its sequence, that one's first tile, number of tiles and tokens
-  for (; b < c.batch; b += 64) {
-    const int own = b + lane < c.batch ? length_of(c, b + lane) : 0;
-    const int mine = b + lane < c.batch ? span_of(c, own, a.window, a.sinks).tiles() : 0, upto = wave_prefix(mine);
-    const uint64_t after = __ballot(begin + upto > at);
-    if (after) {
-      const int i = __builtin_ctzll(after);
-      b += i;
-      tiles = __builtin_amdgcn_readlane(mine, i);
-      len = __builtin_amdgcn_readlane(own, i);
-      begin += __builtin_amdgcn_readlane(upto, i) - tiles;
-      break;
+  if (most == 0) {  // a sequence each
+    if (w >= c.batch) return;
+    b = w;
+    len = length_of(c, b);
+    tiles = span_of(c, len, a.window, a.sinks).tiles();
+    at = 0;
+    stop = tiles;
+  } else {
+    const Deal deal(c, a.window, a.sinks, most, WAYS);
+    if (w >= deal.count) return;
+    at = deal.first_of(w);
+    stop = deal.first_of(w + 1);
+    for (; b < c.batch; b += 64) {
+      const int own = b + lane < c.batch ? length_of(c, b + lane) : 0;
+      const int mine = b + lane < c.batch ? span_of(c, own, a.window, a.sinks).tiles() : 0, upto = wave_prefix(mine);
+      const uint64_t after = __ballot(begin + upto > at);
+      if (after) {
+        const int i = __builtin_ctzll(after);
+        b += i;
+        tiles = __builtin_amdgcn_readlane(mine, i);
+        len = __builtin_amdgcn_readlane(own, i);
+        begin += __builtin_amdgcn_readlane(upto, i) - tiles;
+        break;
+      }
+      begin += __builtin_amdgcn_readlane(upto, 63);
     }
-    begin += __builtin_amdgcn_readlane(upto, 63);
   }
   const float factor = a.scale * kLog2e;
   float* scales = &outs[wave][0][0];  // free until the waves meet
@@ -404,20 +415,31 @@ hipError_t launch(const Fp4AttentionArgs& a, hipStream_t st) {
   // what the longest sequence that the table has room for can be cut into
   int64_t tokens = (int64_t)c.cols << c.shift;
   if (a.window && (int64_t)a.window + a.sinks + 2 * kTile < tokens) tokens = (int64_t)a.window + a.sinks + 2 * kTile;
-  const int64_t longest = (tokens + kTile - 1) / kTile + 1;
+  const int64_t longest = (tokens + kTile - 1) / kTile + (a.window ? 1 : 0);
+  // Short sequences are not cut: a workgroup has one, and there is nothing to join. Up to 5 tiles a wave, and up to 10 where the workgroups
+  // fill the CUs, four times over if lengths can differ. Us cut and whole, 32 over 8 heads of 128: 16 sequences of up to 101 tokens 11.6 / 5.0,
+  // 64 of 251 16.2 / 11.5, 128 of 10 to 1001 35.8 / 30.6, 256 of them 67.8 / 65.7, 37 with a window of 1024 in 8 bits 23.3 / 21.2; but 1 of 1001
+  // 9.4 / 17.6, 64 of 10 to 1001 22.1 / 23.1, 64 of 10 to 2001 27.8 / 40.0.
+  int dev = 0, cus = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e == hipSuccess) e = fp4_device_cus(dev, &cus);
+  if (e != hipSuccess) return e;
+  const int64_t workgroups = (int64_t)c.batch * together * blocks * (WAVES / 4);
+  const bool whole = longest <= 5 * WAYS || (longest <= 10 * WAYS && workgroups >= (int64_t)cus * (tokens < c.cols * ((int64_t)1 << c.shift) ? 1 : 4));
   const int64_t needed = (longest * c.batch + WAYS - 1) / WAYS;
   // more units can round up to more pieces than fewer do, and the workspace is for the fewest
   const int64_t pieces = std::min(FP4_ATTENTION_PIECES(c.batch, together * blocks * (WAVES / 4)),
                                   FP4_ATTENTION_PIECES(c.batch, FP4_ATTENTION_UNITS_(a.q_heads, c.heads)));
-  const int most = (int)std::min(needed, pieces), slots = most + (int)c.batch;
-  hipLaunchKernelGGL((decode<D, E4M3, BESIDE>), dim3((unsigned)((most + 7) / 8 * 8 * together), (unsigned)blocks), dim3(64 * WAVES), 0, st,
-                     a, group, together, most, slots);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || most == 1) return e;
+  const int64_t most = std::min(needed, pieces), count = whole ? c.batch : most;
+  const int slots = (int)(most + c.batch);
+  hipLaunchKernelGGL((decode<D, E4M3, BESIDE>), dim3((unsigned)((count + 7) / 8 * 8 * together), (unsigned)blocks), dim3(64 * WAVES), 0, st,
+                     a, group, together, whole ? 0 : (int)most, slots);
+  e = hipGetLastError();
+  if (e != hipSuccess || whole || most == 1) return e;
   constexpr int groups = 1024 / D;
   // few rows: all lanes to the pieces of one (both ways, us: 1 x 131000 tokens 90 / 93, 64 sequences 64.5 / 61.4)
   const int wide = (int64_t)c.batch * a.q_heads >= 1024 ? groups : 1;
-  hipLaunchKernelGGL((join<D>), dim3((unsigned)((a.q_heads + wide - 1) / wide), (unsigned)c.batch), dim3(256), 0, st, a, wide, most, WAYS,
+  hipLaunchKernelGGL((join<D>), dim3((unsigned)((a.q_heads + wide - 1) / wide), (unsigned)c.batch), dim3(256), 0, st, a, wide, (int)most, WAYS,
                      slots);
   return hipGetLastError();
 }

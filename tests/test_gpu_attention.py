@@ -259,6 +259,29 @@ def test_a_workspace_of_just_its_bytes_is_enough_for_split_rows(H, Hq, news, D, 
     assert (memory[bytes_:] == 0xA5).all()
 
 
+@pytest.mark.parametrize("H,Hq,nB,layout,e4m3", [(12, 12, 169, "heads", False), (24, 24, 85, "tokens", False), (20, 40, 101, "tokens", True),
+                                                 (1, 4, 300, "heads", True)])
+def test_many_short_sequences_with_room_for_long_ones(H, Hq, nB, layout, e4m3):
+    """Cut and joined, as the table could hold long ones; and a workspace of just its bytes is enough then too."""
+    D = 64
+    c = Cache([97 + (37 * b) % 120 if b % 9 else b % 3 for b in range(nB)], H, D, 16, e4m3, layout, cols_more=300).fill()
+    args, q = c.device(), queries(nB, Hq, D)
+    bytes_ = F.attention_workspace_bytes(nB, nB, Hq, H, D)
+    memory = torch.full((bytes_ + (8 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+    got = F.fp4_attention_decode(q.cuda(), *args, workspace=memory[:bytes_], **c.more)
+    want, tol = attention(c, q, range(nB + 1), D ** -0.5)
+    check(got, want, tol, f"decode {nB} sequences heads {Hq}/{H} {layout}")
+    assert (memory[bytes_:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("D,Hq,H,e4m3,layout", [(64, 64, 8, False, "heads"), (128, 32, 8, True, "heads"), (128, 64, 8, True, "tokens"), (256, 4, 4, False, "heads")])
+def test_short_sequences_are_not_cut(D, Hq, H, e4m3, layout):
+    """Sequences that a workgroup takes whole: by their table, and by a window that fills the GPU with them."""
+    run(Cache([1, 0, 15, 33, 64, 97, 120, 128], H, D, 16, e4m3, layout, cols_more=0).fill(), Hq)
+    c = Cache([0, 1, 30, 260, 900, 1500, *(700 + 31 * i for i in range(31))], H, D, 16, e4m3, layout).fill()
+    run(c, Hq, window=200, sinks=5)
+
+
 def test_long_decode_is_split():
     for e4m3 in (False, True):
         c = Cache([20000, 3, 4097], 1, 64, 64, e4m3).fill()
