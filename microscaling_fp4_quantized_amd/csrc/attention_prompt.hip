@@ -13,9 +13,9 @@
 // Rows of 16 more bytes (K) and of 9 chunks of 16 bytes (V^T) keep the 16-byte reads of 32 rows free of bank conflicts.
 // The next tile's loads are in flight during a tile's products, in registers, and go into the other half of LDS behind them.
 //
-// Measured: 8192 tokens of 32 heads of 128 524 to 556 us on different machines, 0.99 to 1.05 PFLOP/s, where torch's large bf16 product
-// reaches 1.22; the matrix cores are busy 47% of the CUs' cycles, vector instructions as much. Three sequences of up to 9000 tokens of 64
-// heads of 64 with a window of 1024 401 to 422 us, 0.7 PFLOP/s: vector instructions take 85% of the cycles, exponentials a third of that. Not faster:
+// Measured: 8192 tokens of 32 heads of 128 517 to 555 us on different machines, 0.99 to 1.06 PFLOP/s, where torch's large bf16 product
+// reaches 1.22; the matrix cores are busy 50% of the CUs' cycles, vector instructions as much. Three sequences of up to 9000 tokens of 64
+// heads of 64 with a window of 1024 395 to 421 us, 0.7 PFLOP/s: vector instructions take 90% of the cycles, exponentials a third of that. Not faster:
 // the scores a tile ahead of the sums (609 us against 545; heads of 256 207 and 200), two groups of waves half a tile apart (566 and 526),
 // leaving out the tiles that a wave's rows do not see but another's do (552 and 540).
 //
