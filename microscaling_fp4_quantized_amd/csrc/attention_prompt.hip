@@ -15,12 +15,13 @@
 //
 // Measured: 8192 tokens of 32 heads of 128 517 to 555 us on different machines, 0.99 to 1.06 PFLOP/s, where torch's large bf16 product
 // reaches 1.22; the matrix cores are busy 50% of the CUs' cycles, vector instructions as much. Three sequences of up to 9000 tokens of 64
-// heads of 64 with a window of 1024 395 to 421 us, 0.7 PFLOP/s: vector instructions take 90% of the cycles, exponentials a third of that. Not faster:
-// the scores a tile ahead of the sums (609 us against 545; heads of 256 207 and 200), two groups of waves half a tile apart (566 and 526),
+// heads of 64 with a window of 1024 395 to 421 us, 0.7 PFLOP/s: vector instructions take 90% of the cycles, exponentials a third of
+// that. Not faster: the scores a tile ahead of the sums (609 us against 545; heads of 256 207 and 200), two groups of waves half a tile apart (566 and 526),
 // leaving out the tiles that a wave's rows do not see but another's do (552 and 540).
 //
 // The running maximum may lag behind by 2^8 before sums and outputs are scaled again. p is rounded to bf16 for the second product;
-// its sum is not. 8-bit caches: codes are exact in bf16, the scales are applied in float32 to scores and p.
+// its sum, in float32, is of the rounded ones, so what rounding does to both cancels in part. 8-bit caches: codes are exact in bf16, the scales
+// are applied in float32 to scores and p, and the sum is of p before its scale.
 #include <atomic>
 
 #include "../../include/fp4.h"
