@@ -755,6 +755,9 @@ def _data(t):
 
 def attention_workspace_bytes(T: int, B: int, q_heads: int, heads: int, dim: int) -> int:
     """FP4_ATTENTION_WORKSPACE_BYTES(T, B, q_heads, heads, dim) of include/fp4.h."""
+    if T < 1 or B < 1 or dim < 1 or heads < 1 or q_heads < heads or q_heads % heads:
+        raise ValueError(f"attention_workspace_bytes: there must be rows, sequences and heads, and the query heads a multiple of the "
+                         f"cache's, got T={T} B={B} q_heads={q_heads} heads={heads} dim={dim}")
     units = heads // (4 if heads % 4 == 0 else 2 if heads % 2 == 0 else 1) * ((q_heads // heads + 15) // 16)
     step = 1 if units >= 512 else 512 // units
     parts = (B + step - 1) // step * step + B
@@ -774,7 +777,7 @@ def _attention_bytes(q, cache):
 def _attention(name, q, cache, scale, window, sinks, starts, out, workspace):
     fast = _fast(q) if out is not None else None
     call = fast and (fast.decode if starts is None else fast.prompt)
-    if call and isinstance(workspace, torch.Tensor):
+    if call and isinstance(workspace, torch.Tensor) and q.dim() == 3 and q.shape[2]:
         rows = () if starts is None else (starts,)
         # the library knows what the workspace has to hold
         status = call(q, *cache, *rows, q.shape[-1] ** -0.5 if scale is None else scale, window, sinks, out, workspace)
@@ -787,13 +790,15 @@ def _attention(name, q, cache, scale, window, sinks, starts, out, workspace):
     T, Hq, D, q_row, q_head = _head_rows(q, name, "q")
     dev = q.device
     c = _kv_cache(name, *cache)
-    if D != c.dim or Hq % c.heads or not Hq:
+    if not D or D != c.dim or not c.heads or not Hq or Hq % c.heads:
         raise ValueError(f"{name}: q must have a multiple of the cache's {c.heads} heads of {c.dim}, got {tuple(q.shape)}")
     if starts is None:
         if T != c.batch:
             raise ValueError(f"{name}: there must be one row for each of {c.batch} sequences, got {T}")
     else:
         _expect(starts, (c.batch + 1,), torch.int32, name, "starts")
+    if not T or not c.batch:
+        raise ValueError(f"{name}: there must be a row and a sequence, got {T} and {c.batch}")
     if out is None:
         out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
     else:
