@@ -721,6 +721,8 @@ def fp4_kv_append(k: torch.Tensor, v: torch.Tensor, k_pages, v_pages, table, len
             if not isinstance(positions, torch.Tensor) or positions.dim() not in (1, 2):
                 raise ValueError(f"{name}: positions must be a tensor [T] or [axes, T]")
             n_axes = positions.shape[0] if positions.dim() == 2 else 1
+            if not n_axes:
+                raise ValueError(f"{name}: positions must have an axis")
             _expect(positions, (n_axes, T) if positions.dim() == 2 else (T,), torch.int32, name, "positions")
         if axes is not None:
             if positions is None:

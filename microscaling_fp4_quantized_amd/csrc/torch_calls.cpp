@@ -322,7 +322,7 @@ PyObject* append(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (!a.good) Py_RETURN_NONE;
   const int64_t n_axes = positions == nullptr ? 0 : flat ? 1 : positions->size(0);
   if (positions != nullptr && (positions->scalar_type() != ScalarType::Int || !positions->is_contiguous() || positions->numel() != n_axes * T ||
-                               n_axes > 1024))
+                               n_axes < 1 || n_axes > 1024))
     Py_RETURN_NONE;
   const void* axes = a.plain(ScalarType::Int, {half}, true);
   const bool interleaved = a.truth();
