@@ -459,28 +459,27 @@ FP4_API int fp4_kv_append(const fp4_kv_cache *cache, const int *starts, int64_t 
  * Two launches at most, on `stream`. Results do not depend on timing: partial sums meet in a fixed order.
  * Errors: FP4_E_NULLPTR, FP4_E_SHAPE (also scale, window, sinks and a short workspace), FP4_E_FORMAT (dtype), FP4_E_ALIGN.
  */
-/* what the workspace holds: a decode call's pieces (one for each sequence and those below for all together), or as many parts of
- * every row's tokens as it takes to fill the GPU */
+/* What the workspace holds: a decode call's pieces (one for each sequence and those below for all together), or as many parts of
+ * every row's tokens as it takes to fill the GPU: a row has FP4_ATTENTION_SPLITS of them at most, 64 or fewer, and all rows of a call
+ * that splits them 65536 / q_heads. The bytes grow with T and with batch, so that one sized for the longest call serves the others. */
 #define FP4_ATTENTION_ROUND_(units) ((units) >= 512 ? 1 : 512 / (units))
 #define FP4_ATTENTION_PIECES(batch, units) \
   (((int64_t)(batch) + FP4_ATTENTION_ROUND_(units) - 1) / FP4_ATTENTION_ROUND_(units) * FP4_ATTENTION_ROUND_(units))
 #define FP4_ATTENTION_UNITS_(q_heads, heads) \
   ((heads) / ((heads) % 4 == 0 ? 4 : (heads) % 2 == 0 ? 2 : 1) * (((q_heads) / (heads) + 15) / 16))
 #define FP4_ATTENTION_MAX_(a, b) ((a) > (b) ? (a) : (b))
+#define FP4_ATTENTION_MIN_(a, b) ((a) < (b) ? (a) : (b))
 #define FP4_ATTENTION_TILES_(T, batch, q_heads, heads) \
   (FP4_ATTENTION_MAX_(((int64_t)(T) * ((q_heads) / (heads)) + 127) / 128, (int64_t)(batch)) * (heads))
 #define FP4_ATTENTION_SPLITS(T, batch, q_heads, heads)                      \
   (FP4_ATTENTION_TILES_(T, batch, q_heads, heads) > 256 ? 1                  \
    : FP4_ATTENTION_TILES_(T, batch, q_heads, heads) <= 8 ? 64                \
                                                         : 512 / FP4_ATTENTION_TILES_(T, batch, q_heads, heads))
-#define FP4_ATTENTION_PARTS_(T, batch, q_heads, heads) \
+#define FP4_ATTENTION_PARTS_(T, batch, q_heads, heads)                                            \
   FP4_ATTENTION_MAX_(FP4_ATTENTION_PIECES(batch, FP4_ATTENTION_UNITS_(q_heads, heads)) + (batch), \
-                     FP4_ATTENTION_SPLITS(T, batch, q_heads, heads) * (int64_t)(T))
-#define FP4_ATTENTION_WORKSPACE_BYTES(T, batch, q_heads, heads, dim)                                          \
-  ((size_t)(FP4_ATTENTION_SPLITS(T, batch, q_heads, heads) > 1                                                \
-                ? FP4_ATTENTION_PARTS_(T, batch, q_heads, heads)                                              \
-                : FP4_ATTENTION_PIECES(batch, FP4_ATTENTION_UNITS_(q_heads, heads)) + (batch)) *              \
-   (size_t)(q_heads) * ((size_t)(dim) + 2) * 4)
+                     FP4_ATTENTION_MIN_(64 * (int64_t)(T), (int64_t)65536 / (q_heads)))
+#define FP4_ATTENTION_WORKSPACE_BYTES(T, batch, q_heads, heads, dim) \
+  ((size_t)FP4_ATTENTION_PARTS_(T, batch, q_heads, heads) * (size_t)(q_heads) * ((size_t)(dim) + 2) * 4)
 FP4_API int fp4_attention_decode(const fp4_kv_cache *cache, const void *Q, int64_t q_row, int64_t q_head, int q_heads, float scale,
                                  int64_t window, int64_t sinks, void *Out, void *workspace, size_t workspace_bytes,
                                  void *stream);

@@ -756,16 +756,13 @@ def _data(t):
 
 
 def attention_workspace_bytes(T: int, B: int, q_heads: int, heads: int, dim: int) -> int:
-    """FP4_ATTENTION_WORKSPACE_BYTES(T, B, q_heads, heads, dim) of include/fp4.h."""
+    """FP4_ATTENTION_WORKSPACE_BYTES(T, B, q_heads, heads, dim) of include/fp4.h: as many at least for more rows or sequences."""
     if T < 1 or B < 1 or dim < 1 or heads < 1 or q_heads < heads or q_heads % heads:
         raise ValueError(f"attention_workspace_bytes: there must be rows, sequences and heads, and the query heads a multiple of the "
                          f"cache's, got T={T} B={B} q_heads={q_heads} heads={heads} dim={dim}")
     units = heads // (4 if heads % 4 == 0 else 2 if heads % 2 == 0 else 1) * ((q_heads // heads + 15) // 16)
     step = 1 if units >= 512 else 512 // units
-    parts = (B + step - 1) // step * step + B
-    tiles = max((T * (q_heads // heads) + 127) // 128, B) * heads
-    if tiles <= 256:
-        parts = max(parts, min(64, 512 // tiles) * T)
+    parts = max((B + step - 1) // step * step + B, min(64 * T, 65536 // q_heads))
     return parts * q_heads * (dim + 2) * 4
 
 
