@@ -25,15 +25,12 @@
 //
 // 8-bit caches: codes are exact in bf16, so the matrix cores see codes and the scales are applied in float32, a key's to its score
 // and a value's to its p. p is rounded to bf16 for the second product (at most 2^-8 of each p, and as often up as down); its sum is not.
-#include <algorithm>
-
-#include "../../include/fp4.h"
 #include "attention_device.hpp"
 
 namespace fp4 {
 namespace {
 
-constexpr int kTile = 32;
+constexpr int kTile = kDecodeTile;
 constexpr float kSlack = 8.f;  // the running maximum may lag behind by this many powers of two: p stays below 2^8
 
 // The visible tokens of a sequence, as granules of 16: ga of them from token 0 on, then more from granule gb on.
@@ -248,14 +245,10 @@ __device__ __forceinline__ void work(State<D, E4M3>& st, Raw<D, E4M3>& x, float 
   }
 }
 
-// BESIDE: key-value heads of a workgroup, side by side in memory; its other waves share a head's tiles. Four heads have two waves each:
-// half the pieces to join (64 sequences of 1721 tokens, 8 bits: 57 -> 51 us).
-constexpr int waves_of(int beside) { return beside == 4 ? 8 : 4; }
-
 template <int D, bool E4M3, int BESIDE>
-__global__ __launch_bounds__(64 * waves_of(BESIDE), 2) void decode(Fp4AttentionArgs a, int group, int together, int most, int slots) {
+__global__ __launch_bounds__(64 * decode_waves(BESIDE), 2) void decode(Fp4AttentionArgs a, int group, int together, int most, int slots) {
   typedef Raw<D, E4M3> R;
-  constexpr int PITCH = D + 1, WAVES = waves_of(BESIDE);
+  constexpr int PITCH = D + 1, WAVES = decode_waves(BESIDE);
   __shared__ alignas(16) float outs[WAVES][16][PITCH];
   __shared__ float tops[WAVES][16], sums[WAVES][16];
   const Paged& c = a.cache;
@@ -408,54 +401,34 @@ __global__ __launch_bounds__(256) void join(Fp4AttentionArgs a, int wide, int mo
 }
 
 template <int D, bool E4M3, int BESIDE>
-hipError_t launch(const Fp4AttentionArgs& a, hipStream_t st) {
+hipError_t launch(const Fp4AttentionArgs& a, const DecodeWay& way, hipStream_t st) {
   const Paged& c = a.cache;
   const int group = a.q_heads / c.heads, blocks = (group + 15) / 16, together = c.heads / BESIDE;
-  constexpr int WAVES = waves_of(BESIDE), WAYS = WAVES / BESIDE;
-  // what the longest sequence that the table has room for can be cut into
-  int64_t tokens = (int64_t)c.cols << c.shift;
-  if (a.window && (int64_t)a.window + a.sinks + 2 * kTile < tokens) tokens = (int64_t)a.window + a.sinks + 2 * kTile;
-  const int64_t longest = (tokens + kTile - 1) / kTile + (a.window ? 1 : 0);
-  // Short sequences are not cut: a workgroup has one, and there is nothing to join. Up to 5 tiles a wave, and up to 10 where the workgroups
-  // fill the CUs, four times over if lengths can differ. Us cut and whole, 32 over 8 heads of 128: 16 sequences of up to 101 tokens 11.6 / 5.0,
-  // 64 of 251 16.2 / 11.5, 128 of 10 to 1001 35.8 / 30.6, 256 of them 67.8 / 65.7, 37 with a window of 1024 in 8 bits 23.3 / 21.2; but 1 of 1001
-  // 9.4 / 17.6, 64 of 10 to 1001 22.1 / 23.1, 64 of 10 to 2001 27.8 / 40.0.
-  int dev = 0, cus = 0;
-  hipError_t e = hipGetDevice(&dev);
-  if (e == hipSuccess) e = fp4_device_cus(dev, &cus);
-  if (e != hipSuccess) return e;
-  const int64_t workgroups = (int64_t)c.batch * together * blocks * (WAVES / 4);
-  const bool whole = longest <= 5 * WAYS || (longest <= 10 * WAYS && workgroups >= (int64_t)cus * (tokens < c.cols * ((int64_t)1 << c.shift) ? 1 : 4));
-  const int64_t needed = (longest * c.batch + WAYS - 1) / WAYS;
-  // more units can round up to more pieces than fewer do, and the workspace is for the fewest
-  const int64_t pieces = std::min(FP4_ATTENTION_PIECES(c.batch, together * blocks * (WAVES / 4)),
-                                  FP4_ATTENTION_PIECES(c.batch, FP4_ATTENTION_UNITS_(a.q_heads, c.heads)));
-  const int64_t most = std::min(needed, pieces), count = whole ? c.batch : most;
-  const int slots = (int)(most + c.batch);
+  constexpr int WAVES = decode_waves(BESIDE), WAYS = WAVES / BESIDE;
+  const int64_t count = way.whole ? c.batch : way.most;
+  const int slots = (int)(way.most + c.batch);
   hipLaunchKernelGGL((decode<D, E4M3, BESIDE>), dim3((unsigned)((count + 7) / 8 * 8 * together), (unsigned)blocks), dim3(64 * WAVES), 0, st,
-                     a, group, together, whole ? 0 : (int)most, slots);
-  e = hipGetLastError();
-  if (e != hipSuccess || whole || most == 1) return e;
-  constexpr int groups = 1024 / D;
-  // few rows: all lanes to the pieces of one (both ways, us: 1 x 131000 tokens 90 / 93, 64 sequences 64.5 / 61.4)
-  const int wide = (int64_t)c.batch * a.q_heads >= 1024 ? groups : 1;
-  hipLaunchKernelGGL((join<D>), dim3((unsigned)((a.q_heads + wide - 1) / wide), (unsigned)c.batch), dim3(256), 0, st, a, wide, (int)most, WAYS,
-                     slots);
+                     a, group, together, way.whole ? 0 : (int)way.most, slots);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || way.wide == 0) return e;
+  hipLaunchKernelGGL((join<D>), dim3((unsigned)((a.q_heads + way.wide - 1) / way.wide), (unsigned)c.batch), dim3(256), 0, st, a, way.wide,
+                     (int)way.most, WAYS, slots);
   return hipGetLastError();
 }
 
 template <int D, bool E4M3>
 hipError_t launch(const Fp4AttentionArgs& a, hipStream_t st) {
-  // heads that lie side by side, in rows of 256 bytes at most: up to 512 bytes of them to a workgroup
+  int dev = 0, cus = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e == hipSuccess) e = fp4_device_cus(dev, &cus);
+  if (e != hipSuccess) return e;
+  const DecodeWay way = decode_way(fp4_call_of(a, D, E4M3), cus);
   constexpr int bytes = D * (E4M3 ? 1 : 2);
-  if constexpr (bytes <= 256) {
-    if (a.cache.head_stride == bytes) {
-      if constexpr (bytes <= 128)
-        if (a.cache.heads % 4 == 0) return launch<D, E4M3, 4>(a, st);
-      if (a.cache.heads % 2 == 0) return launch<D, E4M3, 2>(a, st);
-    }
-  }
-  return launch<D, E4M3, 1>(a, st);
+  if constexpr (bytes <= 128)
+    if (way.beside == 4) return launch<D, E4M3, 4>(a, way, st);
+  if constexpr (bytes <= 256)
+    if (way.beside == 2) return launch<D, E4M3, 2>(a, way, st);
+  return launch<D, E4M3, 1>(a, way, st);
 }
 
 }  // namespace

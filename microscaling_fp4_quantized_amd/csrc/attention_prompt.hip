@@ -24,14 +24,12 @@
 // are applied in float32 to scores and p, and the sum is of p before its scale.
 #include <atomic>
 
-#include "../../include/fp4.h"
 #include "attention_device.hpp"
 
 namespace fp4 {
 namespace {
 
-constexpr int kTokens = 64;  // of a tile
-constexpr int kMinTiles = 4;  // of a part, where a row's tokens are split over workgroups
+constexpr int kTokens = kPromptTokens;
 constexpr float kSlack = 8.f;
 
 typedef float v16f __attribute__((ext_vector_type(16)));
@@ -221,14 +219,6 @@ __device__ __forceinline__ Range range_of(const Paged& c, int len, int i0, int i
   r.tiles = r.ta + max(end - r.tb, 0);
   return r;
 }
-// Parts of so many tiles that are worth a workgroup each. Few rows are joined quickly: up to 32 parts of half the size for them. Us with and
-// without: 16 tokens behind 1000 13.8 / 16.1, 8 of 16 heads of 256 behind 600 18.3 / 23.0; but 300 tokens, all for one of their own, 18.0 / 17.1,
-// 64 of 16 heads behind 8000 in 64 parts and not 32 24.8 / 19.5.
-__host__ __device__ inline int64_t worth(int64_t tiles, int64_t T, int q_heads, int dim) {
-  const int64_t parts = (tiles + kMinTiles - 1) / kMinTiles, fine = (tiles + 1) / 2;
-  return T * q_heads * dim > (1 << 18) || parts >= 32 ? parts : fine < 32 ? fine : 32;
-}
-
 // Rows of a sequence: new tokens times the heads of a group.
 struct Rows {
   int first, count;  // its first row of q, and its new tokens
@@ -237,14 +227,6 @@ __device__ __forceinline__ Rows rows_of(const int* starts, int b, int T) {
   const int t0 = min(max(starts[b], 0), T), t1 = min(max(starts[b + 1], t0), T);
   return {t0, t1 - t0};
 }
-
-// Whether eight waves share what is brought into LDS, where there are rows for them: 310 us at 8192 tokens and heads of 64, with workgroups
-// of four waves 338; 582 and 623 with heads of 128 in 8 bits. Heads of 64 in 8 bits need more than the 128 registers that four waves of a
-// SIMD have, and do better with three of 168 in workgroups of four waves (a window of 1024: 499 us, 607 with eight waves and 37 registers
-// spilled); heads of 256 fill the registers of a SIMD with one wave. No variant may keep anything in scratch memory: the loop would wait for
-// it, and with it for the next tile's loads.
-template <int D, bool E4M3>
-constexpr bool kEight = D == 128 || (D == 64 && !E4M3);
 
 // SPLIT: blockIdx.y takes one of `splits` parts of its rows' tokens, at most. A kernel of its own, because what it adds to the registers
 // costs heads of 64 4% (455 -> 468 us with a window).
@@ -539,8 +521,8 @@ __global__ __launch_bounds__(256) void join(Fp4AttentionArgs a, int group, int t
 }
 
 template <int D, bool E4M3, int WAVES, bool SPLIT>
-hipError_t launch(const Fp4AttentionArgs& a, int splits, int dev, hipStream_t st) {
-  const int group = a.q_heads / a.cache.heads, rows = 32 * WAVES;
+hipError_t launch(const Fp4AttentionArgs& a, const PromptWay& way, int dev, hipStream_t st) {
+  const int group = a.q_heads / a.cache.heads, rows = 32 * WAVES, splits = SPLIT ? way.splits : 1;
   const int64_t tiles = ((int64_t)a.T * group + rows - 1) / rows + a.cache.batch;
   constexpr int bytes = sizeof(Lds<D, E4M3>);
   static std::atomic<int> ready[64];  // by device
@@ -555,10 +537,8 @@ hipError_t launch(const Fp4AttentionArgs& a, int splits, int dev, hipStream_t st
   hipLaunchKernelGGL(kern, dim3((unsigned)(tiles * a.cache.heads), splits), dim3(64 * WAVES), bytes, st, a, group, (int)tiles, splits);
   e = hipGetLastError();
   if (e != hipSuccess || !SPLIT) return e;
-  // heads of a workgroup of the join: fewer where they have many parts (one token behind 60000, 64 parts: 87 us with all, 76 so)
-  int wide = 1024 / D;
-  while (wide > 1 && splits * wide > 4 * (1024 / D)) wide /= 2;
-  hipLaunchKernelGGL((join<D>), dim3((unsigned)a.T, (unsigned)((a.q_heads + wide - 1) / wide)), dim3(256), 0, st, a, group, rows, splits, wide);
+  hipLaunchKernelGGL((join<D>), dim3((unsigned)a.T, (unsigned)((a.q_heads + way.wide - 1) / way.wide)), dim3(256), 0, st, a, group, rows, splits,
+                     way.wide);
   return hipGetLastError();
 }
 
@@ -568,24 +548,10 @@ hipError_t launch(const Fp4AttentionArgs& a, hipStream_t st) {
   hipError_t e = hipGetDevice(&dev);
   if (e == hipSuccess) e = fp4_device_cus(dev, &cus);
   if (e != hipSuccess) return e;
-  // few rows: their tokens split over workgroups, as far as the longest sequence that the table has room for goes. Us with and without: two
-  // pieces of 512 tokens behind 16000 274 / 391, one token behind 60000 77 / 1381.
-  const Paged& c = a.cache;
-  int64_t tokens = (int64_t)c.cols << c.shift;
-  if (a.window && (int64_t)a.window + a.sinks + 32 * 8 < tokens) tokens = (int64_t)a.window + a.sinks + 32 * 8;
-  const int64_t tiles = (tokens + kTokens - 1) / kTokens, most = tiles > kMinTiles ? worth(tiles, a.T, a.q_heads, D) : 1;
-  int64_t splits = FP4_ATTENTION_SPLITS(a.T, c.batch, a.q_heads, c.heads);
-  if (splits > most) splits = most;
-  if constexpr (kEight<D, E4M3>) {
-    // 256 rows share what is brought into LDS, once they fill the CUs. Us with 256 and 128 rows, heads of 128: 8192 tokens 540 / 588, two
-    // pieces of 512 tokens behind 16000 272 / 305; below the line 4 sequences of 200 to 900 tokens 50.9 / 49.8, two of 16 tokens behind
-    // 30000 125 / 82, one token behind 60000 140 / 89.
-    // (A grid has fewer than 2^32 work-items.)
-    const int64_t blocks = (((int64_t)a.T * (a.q_heads / c.heads) + 255) / 256 + c.batch) * c.heads;
-    if ((int64_t)a.T * a.q_heads * splits >= (int64_t)256 * cus && blocks < (1 << 23))
-      return splits > 1 ? launch<D, E4M3, 8, true>(a, (int)splits, dev, st) : launch<D, E4M3, 8, false>(a, 1, dev, st);
-  }
-  return splits > 1 ? launch<D, E4M3, 4, true>(a, (int)splits, dev, st) : launch<D, E4M3, 4, false>(a, 1, dev, st);
+  const PromptWay way = prompt_way(fp4_call_of(a, D, E4M3), cus);
+  if constexpr (prompt_eight(D, E4M3))
+    if (way.waves == 8) return way.splits > 1 ? launch<D, E4M3, 8, true>(a, way, dev, st) : launch<D, E4M3, 8, false>(a, way, dev, st);
+  return way.splits > 1 ? launch<D, E4M3, 4, true>(a, way, dev, st) : launch<D, E4M3, 4, false>(a, way, dev, st);
 }
 
 }  // namespace

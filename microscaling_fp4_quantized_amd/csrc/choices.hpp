@@ -1,9 +1,11 @@
-// Host-side choices of the 8-bit and mixture-of-experts operators, free of HIP so that they can be compiled and checked alone.
+// Host-side choices of the 8-bit, mixture-of-experts and attention operators, free of HIP so that they can be compiled and checked alone.
 #pragma once
 
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+
+#include "../../include/fp4.h"
 
 namespace fp4 {
 
@@ -90,5 +92,104 @@ inline bool few_pairs(int T, int k, int64_t E, int64_t D, int64_t I) {
 // sooner than the two that are taken.
 constexpr int kShortK = 1536;
 inline int expert_waves(int64_t K, int64_t workgroups) { return workgroups < 1024 ? 8 : K <= kShortK ? 1 : 2; }
+
+// ---- attention ---------------------------------------------------------------------------------------------------------
+
+// A call of the attention operators, as far as it decides which kernels it takes.
+struct AttentionCall {
+  int dim;
+  bool e4m3;
+  int64_t T, batch;  // rows (decode: batch)
+  int q_heads, heads;
+  int64_t room;  // tokens of a sequence that the table has room for
+  int window, sinks;
+  bool side_by_side;  // a token's heads follow each other in memory
+};
+
+constexpr int kDecodeTile = 32;     // tokens
+constexpr int kPromptTokens = 64;   // of a tile
+constexpr int kPromptMinTiles = 4;  // of a part, where a row's tokens are split over workgroups
+
+// Key-value heads of a decode workgroup, side by side in memory; its other waves share a head's tiles. Four heads have two waves each:
+// half the pieces to join (64 sequences of 1721 tokens, 8 bits: 57 -> 51 us).
+constexpr int decode_waves(int beside) { return beside == 4 ? 8 : 4; }
+
+struct DecodeWay {
+  int beside;    // 1, 2 or 4
+  bool whole;    // a workgroup has a sequence, without a second launch
+  int64_t most;  // pieces at most
+  int wide;      // query heads of a workgroup of the join; 0: no join
+};
+
+inline DecodeWay decode_way(const AttentionCall& c, int cus) {
+  DecodeWay way{1, false, 1, 0};
+  // heads that lie side by side, in rows of 256 bytes at most: up to 512 bytes of them to a workgroup
+  const int bytes = c.dim * (c.e4m3 ? 1 : 2);
+  if (c.side_by_side && bytes <= 256) way.beside = bytes <= 128 && c.heads % 4 == 0 ? 4 : c.heads % 2 == 0 ? 2 : 1;
+  const int waves = decode_waves(way.beside), ways = waves / way.beside;
+  const int blocks = (c.q_heads / c.heads + 15) / 16, together = c.heads / way.beside;
+  // what the longest sequence that the table has room for can be cut into
+  int64_t tokens = c.room;
+  if (c.window && (int64_t)c.window + c.sinks + 2 * kDecodeTile < tokens) tokens = (int64_t)c.window + c.sinks + 2 * kDecodeTile;
+  const int64_t longest = (tokens + kDecodeTile - 1) / kDecodeTile + (c.window ? 1 : 0);
+  // Short sequences are not cut: a workgroup has one, and there is nothing to join. Up to 5 tiles a wave, and up to 10 where the workgroups
+  // fill the CUs, four times over if lengths can differ. Us cut and whole, 32 over 8 heads of 128: 16 sequences of up to 101 tokens 11.6 / 5.0,
+  // 64 of 251 16.2 / 11.5, 128 of 10 to 1001 35.8 / 30.6, 256 of them 67.8 / 65.7, 37 with a window of 1024 in 8 bits 23.3 / 21.2; but 1 of 1001
+  // 9.4 / 17.6, 64 of 10 to 1001 22.1 / 23.1, 64 of 10 to 2001 27.8 / 40.0.
+  const int64_t workgroups = c.batch * together * blocks * (waves / 4);
+  way.whole = longest <= 5 * ways || (longest <= 10 * ways && workgroups >= (int64_t)cus * (tokens < c.room ? 1 : 4));
+  const int64_t needed = (longest * c.batch + ways - 1) / ways;
+  // more units can round up to more pieces than fewer do, and the workspace is for the fewest
+  const int64_t pieces = std::min<int64_t>(FP4_ATTENTION_PIECES(c.batch, together * blocks * (waves / 4)),
+                                           FP4_ATTENTION_PIECES(c.batch, FP4_ATTENTION_UNITS_(c.q_heads, c.heads)));
+  way.most = std::min(needed, pieces);
+  // few rows: all lanes to the pieces of one (both ways, us: 1 x 131000 tokens 90 / 93, 64 sequences 64.5 / 61.4)
+  if (!way.whole && way.most > 1) way.wide = c.batch * c.q_heads >= 1024 ? 1024 / c.dim : 1;
+  return way;
+}
+
+// Parts of so many tiles that are worth a workgroup each. Few rows are joined quickly: up to 32 parts of half the size for them. Us with and
+// without: 16 tokens behind 1000 13.8 / 16.1, 8 of 16 heads of 256 behind 600 18.3 / 23.0; but 300 tokens, all for one of their own, 18.0 / 17.1,
+// 64 of 16 heads behind 8000 in 64 parts and not 32 24.8 / 19.5.
+constexpr int64_t worth(int64_t tiles, int64_t T, int q_heads, int dim) {
+  const int64_t parts = (tiles + kPromptMinTiles - 1) / kPromptMinTiles, fine = (tiles + 1) / 2;
+  return T * q_heads * dim > (1 << 18) || parts >= 32 ? parts : fine < 32 ? fine : 32;
+}
+
+// Whether eight waves share what is brought into LDS, where there are rows for them: 310 us at 8192 tokens and heads of 64, with workgroups
+// of four waves 338; 582 and 623 with heads of 128 in 8 bits. Heads of 64 in 8 bits need more than the 128 registers that four waves of a
+// SIMD have, and do better with three of 168 in workgroups of four waves (a window of 1024: 499 us, 607 with eight waves and 37 registers
+// spilled); heads of 256 fill the registers of a SIMD with one wave. No variant may keep anything in scratch memory: the loop would wait for
+// it, and with it for the next tile's loads.
+constexpr bool prompt_eight(int dim, bool e4m3) { return dim == 128 || (dim == 64 && !e4m3); }
+
+struct PromptWay {
+  int waves;   // 4 or 8, of 32 rows each
+  int splits;  // parts of a row's tokens at most
+  int wide;    // query heads of a workgroup of the join; 0: no join
+};
+
+inline PromptWay prompt_way(const AttentionCall& c, int cus) {
+  PromptWay way{4, 1, 0};
+  // few rows: their tokens split over workgroups, as far as the longest sequence that the table has room for goes. Us with and without: two
+  // pieces of 512 tokens behind 16000 274 / 391, one token behind 60000 77 / 1381.
+  int64_t tokens = c.room;
+  if (c.window && (int64_t)c.window + c.sinks + 32 * 8 < tokens) tokens = (int64_t)c.window + c.sinks + 32 * 8;
+  const int64_t tiles = (tokens + kPromptTokens - 1) / kPromptTokens;
+  const int64_t most = tiles > kPromptMinTiles ? worth(tiles, c.T, c.q_heads, c.dim) : 1;
+  way.splits = (int)std::min<int64_t>(FP4_ATTENTION_SPLITS(c.T, c.batch, c.q_heads, c.heads), most);
+  // 256 rows share what is brought into LDS, once they fill the CUs. Us with 256 and 128 rows, heads of 128: 8192 tokens 540 / 588, two
+  // pieces of 512 tokens behind 16000 272 / 305; below the line 4 sequences of 200 to 900 tokens 50.9 / 49.8, two of 16 tokens behind
+  // 30000 125 / 82, one token behind 60000 140 / 89.
+  // (A grid has fewer than 2^32 work-items.)
+  const int64_t blocks = ((c.T * (c.q_heads / c.heads) + 255) / 256 + c.batch) * c.heads;
+  if (prompt_eight(c.dim, c.e4m3) && c.T * c.q_heads * way.splits >= (int64_t)256 * cus && blocks < (1 << 23)) way.waves = 8;
+  if (way.splits > 1) {
+    // heads of a workgroup of the join: fewer where they have many parts (one token behind 60000, 64 parts: 87 us with all, 76 so)
+    way.wide = 1024 / c.dim;
+    while (way.wide > 1 && way.splits * way.wide > 4 * (1024 / c.dim)) way.wide /= 2;
+  }
+  return way;
+}
 
 }  // namespace fp4

@@ -80,5 +80,9 @@ struct Fp4AttentionArgs {
   int T, q_heads, window, sinks;
   void* workspace;
 };
+inline fp4::AttentionCall fp4_call_of(const Fp4AttentionArgs& a, int dim, bool e4m3) {
+  const fp4::Paged& c = a.cache;
+  return {dim, e4m3, a.T, c.batch, a.q_heads, c.heads, (int64_t)c.cols << c.shift, a.window, a.sinks, c.head_stride == (int64_t)dim * (e4m3 ? 1 : 2)};
+}
 hipError_t fp4_launch_attention_decode(const Fp4AttentionArgs& a, int dim, bool e4m3, hipStream_t stream);
 hipError_t fp4_launch_attention_prompt(const Fp4AttentionArgs& a, int dim, bool e4m3, hipStream_t stream);
