@@ -549,8 +549,10 @@ hipError_t launch(const Fp4AttentionArgs& a, hipStream_t st) {
   if (e == hipSuccess) e = fp4_device_cus(dev, &cus);
   if (e != hipSuccess) return e;
   const PromptWay way = prompt_way(fp4_call_of(a, D, E4M3), cus);
-  if constexpr (prompt_eight(D, E4M3))
-    if (way.waves == 8) return way.splits > 1 ? launch<D, E4M3, 8, true>(a, way, dev, st) : launch<D, E4M3, 8, false>(a, way, dev, st);
+  if constexpr (prompt_eight(D, E4M3, true))
+    if (way.waves == 8 && way.splits > 1) return launch<D, E4M3, 8, true>(a, way, dev, st);
+  if constexpr (prompt_eight(D, E4M3, false))
+    if (way.waves == 8) return launch<D, E4M3, 8, false>(a, way, dev, st);
   return way.splits > 1 ? launch<D, E4M3, 4, true>(a, way, dev, st) : launch<D, E4M3, 4, false>(a, way, dev, st);
 }
 

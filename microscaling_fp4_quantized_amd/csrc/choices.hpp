@@ -160,8 +160,9 @@ constexpr int64_t worth(int64_t tiles, int64_t T, int q_heads, int dim) {
 // of four waves 338; 582 and 623 with heads of 128 in 8 bits. Heads of 64 in 8 bits need more than the 128 registers that four waves of a
 // SIMD have, and do better with three of 168 in workgroups of four waves (a window of 1024: 499 us, 607 with eight waves and 37 registers
 // spilled); heads of 256 fill the registers of a SIMD with one wave. No variant may keep anything in scratch memory: the loop would wait for
-// it, and with it for the next tile's loads.
-constexpr bool prompt_eight(int dim, bool e4m3) { return dim == 128 || (dim == 64 && !e4m3); }
+// it, and with it for the next tile's loads. Where tokens are split, heads of 64 are sooner with four waves (512 rows of 64 heads in two
+// parts 187 us, with eight 215).
+constexpr bool prompt_eight(int dim, bool e4m3, bool split) { return dim == 128 || (dim == 64 && !e4m3 && !split); }
 
 struct PromptWay {
   int waves;   // 4 or 8, of 32 rows each
@@ -172,18 +173,28 @@ struct PromptWay {
 inline PromptWay prompt_way(const AttentionCall& c, int cus) {
   PromptWay way{4, 1, 0};
   // few rows: their tokens split over workgroups, as far as the longest sequence that the table has room for goes. Us with and without: two
-  // pieces of 512 tokens behind 16000 274 / 391, one token behind 60000 77 / 1381.
+  // pieces of 512 tokens behind 9000 and 16001 251 / 371, one token behind 60000 77 / 1381. No further than 256 tiles of 128 rows: two parts of
+  // more would help sequences of different lengths (two pieces of 640 tokens 296 / 421) and cost others (2000 tokens behind nothing
+  // 76 / 61, behind 7000 301 / 286 and with heads of 256 757 / 645).
   int64_t tokens = c.room;
   if (c.window && (int64_t)c.window + c.sinks + 32 * 8 < tokens) tokens = (int64_t)c.window + c.sinks + 32 * 8;
   const int64_t tiles = (tokens + kPromptTokens - 1) / kPromptTokens;
   const int64_t most = tiles > kPromptMinTiles ? worth(tiles, c.T, c.q_heads, c.dim) : 1;
   way.splits = (int)std::min<int64_t>(FP4_ATTENTION_SPLITS(c.T, c.batch, c.q_heads, c.heads), most);
-  // 256 rows share what is brought into LDS, once they fill the CUs. Us with 256 and 128 rows, heads of 128: 8192 tokens 540 / 588, two
-  // pieces of 512 tokens behind 16000 272 / 305; below the line 4 sequences of 200 to 900 tokens 50.9 / 49.8, two of 16 tokens behind
-  // 30000 125 / 82, one token behind 60000 140 / 89.
-  // (A grid has fewer than 2^32 work-items.)
-  const int64_t blocks = ((c.T * (c.q_heads / c.heads) + 255) / 256 + c.batch) * c.heads;
-  if (prompt_eight(c.dim, c.e4m3) && c.T * c.q_heads * way.splits >= (int64_t)256 * cus && blocks < (1 << 23)) way.waves = 8;
+  const int64_t tiles8 = (c.T * (c.q_heads / c.heads) + 255) / 256;  // of 256 rows
+  if (way.splits > 1) {
+    // 256 rows share what is brought into LDS: an eighth sooner where their workgroups are one round, every CU but a 32nd of them having one,
+    // and none two, and where no part is so short that its start shows. Us with 128 and 256 rows (splits), two sequences behind 9000 and 16001, 32
+    // over 8 heads of 128: 1000 to 1024 rows (2) 281 / 250, 500 (4) 148 / 134, 256 (8) 85 / 78; 128 (16) 57 / 84, 200 (9) 104 / 108; 641 (3: 264
+    // workgroups) 199 / 200, in 8 bits 215 / 224; one behind 8000, 16 heads: 2000 (2) 185 / 168, 900 (4) 100 / 93, 500 (8) 62 / 60; 1200 (3: 240)
+    // 117 / 172, 768 (5: 240) 83 / 120, 600 (6: 288) 99 / 104, 256 (16) 44 / 67.
+    const int64_t groups = std::max(tiles8, c.batch) * c.heads * way.splits;
+    if (prompt_eight(c.dim, c.e4m3, true) && way.splits <= 8 && groups <= cus && groups >= cus - cus / 32) way.waves = 8;
+  } else {
+    // Once they fill the CUs: 8192 tokens 540 with 256 rows, 588 with 128; below the line 4 sequences of 200 to 900 tokens 50.9 / 49.8.
+    // (A grid has fewer than 2^32 work-items.)
+    if (prompt_eight(c.dim, c.e4m3, false) && c.T * c.q_heads >= (int64_t)256 * cus && (tiles8 + c.batch) * c.heads < (1 << 23)) way.waves = 8;
+  }
   if (way.splits > 1) {
     // heads of a workgroup of the join: fewer where they have many parts (one token behind 60000, 64 parts: 87 us with all, 76 so)
     way.wide = 1024 / c.dim;
