@@ -434,7 +434,8 @@ typedef struct fp4_kv_cache {
  *  positions    device int [n_axes, T], or NULL.   axes: device int [rotated / 2], or NULL: axis 0. An axis outside
  *               [0, n_axes) does not rotate.   n_axes: 1..16 with positions, else 0.
  *  T            1..2^24, T * (q_heads + 2 * heads) <= 2^30.
- * Two rows of one cache place (a page that stands twice in the table) leave either's values there.
+ * Two rows of one cache place (a page that stands twice in the table) leave a mixture of both there, with E4M3 also one's codes under the
+ * other's scale; no other place changes.
  * One launch on `stream`. Errors: FP4_E_NULLPTR, FP4_E_SHAPE, FP4_E_FORMAT (dtype), FP4_E_ALIGN.
  */
 FP4_API int fp4_kv_append(const fp4_kv_cache *cache, const int *starts, int64_t T, const void *K, int64_t k_row, int64_t k_head,
@@ -449,14 +450,19 @@ FP4_API int fp4_kv_append(const fp4_kv_cache *cache, const int *starts, int64_t 
  * fp4_attention_decode is for one new token of each sequence (row b belongs to sequence b); fp4_attention_prompt for many.
  * Rows that see no token get zeros. Scores, p's sum and the output's sum are float32; p is rounded to bf16 for the product with v.
  * A NaN or infinity in a visible key or value, or in q, gives outputs of that row and head that are not finite, and no others;
- * but a score of minus infinity is one of a token that the row does not see.
+ * but a score of minus infinity is one of a token that the row does not see. Which dims of such an output are not finite depends on the
+ * call: those of an infinite or NaN value where fp4_attention_prompt's rows all see a tile of tokens whole, and in decode; all of them elsewhere.
+ * Sums are of p up to 2^8, so visible values whose magnitudes add up to more than 2^119 may give infinities.
  *  Q            device bf16, rows of q_heads heads of dim: strides as above. q_heads a multiple of cache->heads, up to 1024.
  *  scale        finite and positive.   window, sinks >= 0 (above 2^30 they count as 2^30).
- *  Out          device bf16 [T, q_heads, dim], 16-byte aligned.
+ *  Out          device bf16 [T, q_heads, dim], 16-byte aligned; overlaps no other buffer.
  *  T            1..2^24, T * q_heads <= 2^30.
  *  workspace, workspace_bytes  device buffer of at least FP4_ATTENTION_WORKSPACE_BYTES(T, batch, q_heads, heads, dim) bytes, 16-byte
  *               aligned, the call's alone while it runs (T = batch for the decode call).
  * Two launches at most, on `stream`. Results do not depend on timing: partial sums meet in a fixed order.
+ * Every workgroup of a prompt call, and of a decode call that cuts sequences, looks through all lengths, 64 at a time: batches of some hundred
+ * sequences are what they are made for. Us for one row each of 8 heads, up to 16 tokens, room for 4096 (decode) or 1024: 256 sequences 17 and 31,
+ * 1024 92 and 152, 4096 940 and 1240, 16384 14000 and 28500. Decode without a cut (65535 sequences 2250) and append without starts look at their own alone.
  * Errors: FP4_E_NULLPTR, FP4_E_SHAPE (also scale, window, sinks and a short workspace), FP4_E_FORMAT (dtype), FP4_E_ALIGN.
  */
 /* What the workspace holds: a decode call's pieces (one for each sequence and those below for all together), or as many parts of

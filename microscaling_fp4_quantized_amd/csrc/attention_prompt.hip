@@ -1,7 +1,7 @@
 // Attention of many new tokens of each sequence over a paged key-value cache: causal, with or without a window and first tokens
 // that stay visible.
 //
-// Bound by the matrix cores (4 D operations for a row, a head and a visible token), heads of 64 by the vector instructions of the softmax.
+// Bound by the matrix cores (4 D operations for a row, a head and a visible token); heads of 64 have more vector instructions than products.
 // A workgroup takes 256 or 128 rows of a sequence and a key-value head: the query heads that share the head are rows side by side, so that
 // few tokens still fill a tile and the keys are read once for all of them. Its eight or four waves have 32 rows each and go over tiles of 64
 // tokens that all of them read from LDS. With 32 rows a wave the reads keep LDS busy for about half the time that the products take.
@@ -14,9 +14,9 @@
 // The next tile's loads are in flight during a tile's products, in registers, and go into the other half of LDS behind them.
 //
 // Measured: 8192 tokens of 32 heads of 128 517 to 555 us on different machines, 0.99 to 1.06 PFLOP/s, where torch's large bf16 product
-// reaches 1.22; the matrix cores are busy 50% of the CUs' cycles, vector instructions as much. Three sequences of up to 9000 tokens of 64
-// heads of 64 with a window of 1024 395 to 421 us, 0.7 PFLOP/s: vector instructions take 90% of the cycles, exponentials a third of
-// that. Not faster: the scores a tile ahead of the sums (609 us against 545; heads of 256 207 and 200), two groups of waves half a tile apart (566 and 526),
+// reaches 1.22; the matrix cores are busy 50% of the CUs' cycles, vector instructions 43%. Three sequences of up to 9000 tokens of 64
+// heads of 64 with a window of 1024 395 to 421 us, 0.7 PFLOP/s: vector instructions take 72% of the cycles (exponentials, 8 cycles each, as many
+// as half of the products'), the matrix cores 39%. Not faster: the scores a tile ahead of the sums (609 us against 545; heads of 256 207 and 200), two groups of waves half a tile apart (566 and 526),
 // leaving out the tiles that a wave's rows do not see but another's do (552 and 540).
 //
 // The running maximum may lag behind by 2^8 before sums and outputs are scaled again. p is rounded to bf16 for the second product;
