@@ -173,9 +173,10 @@ struct PromptWay {
 inline PromptWay prompt_way(const AttentionCall& c, int cus) {
   PromptWay way{4, 1, 0};
   // few rows: their tokens split over workgroups, as far as the longest sequence that the table has room for goes. Us with and without: two
-  // pieces of 512 tokens behind 9000 and 16001 251 / 371, one token behind 60000 77 / 1381. No further than 256 tiles of 128 rows: two parts of
-  // more would help sequences of different lengths (two pieces of 640 tokens 296 / 421) and cost others (2000 tokens behind nothing
-  // 76 / 61, behind 7000 301 / 286 and with heads of 256 757 / 645).
+  // pieces of 512 tokens behind 9000 and 16001 251 / 371, one token behind 60000 77 / 1381. No further than 256 tiles of 128 rows, so 1025 and
+  // 1100 rows of those pieces take 415 and 417 (8 bits 491 and 495), 1000 to 1024 251 (283): two parts of more would help sequences of different
+  // lengths (1025 rows 277, 1280 296 / 421) and cost others (2000 tokens behind nothing 76 / 61, behind 7000 301 / 286 and with heads of 256
+  // 757 / 645).
   int64_t tokens = c.room;
   if (c.window && (int64_t)c.window + c.sinks + 32 * 8 < tokens) tokens = (int64_t)c.window + c.sinks + 32 * 8;
   const int64_t tiles = (tokens + kPromptTokens - 1) / kPromptTokens;
